@@ -355,6 +355,136 @@ lora4_status lora4_loftq_init(const uint16_t *W_bf16, int64_t N, int64_t K, int3
                               float *scales2, uint16_t *A, uint16_t *B, void *workspace,
                               size_t workspace_bytes, void *stream);
 
+/* ---- The feed-forward half of a block -----------------------------------------
+ * The operators that stand before, around and behind the linear layer in the
+ * feed-forward half of a pre-norm block: the RMS norm with the residual's
+ * addition, the gate and up projections with their activation and product, and
+ * the linear layer with bias, activation and residual in its epilogue (down
+ * and output projections, biased projections, an ungated first projection).
+ * All conventions of this header hold: bf16 tensors, dense and row-major,
+ * 16-byte aligned, sums in fp32, every output rounded once, caller-owned
+ * workspaces (every call leaves its workspace's contents behind and needs no
+ * initial value there: calls that overlap, captured graphs included, need one
+ * workspace each). The same inputs give the same bits on every call. */
+
+/* Activations. LORA4_ACT_GELU is x Phi(x) with the normal distribution's
+ * Phi, LORA4_ACT_GELU_TANH its tanh form
+ * x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2; LORA4_ACT_SILU is
+ * x / (1 + e^-x). */
+typedef enum {
+  LORA4_ACT_NONE = 0,
+  LORA4_ACT_SILU = 1,
+  LORA4_ACT_GELU = 2,
+  LORA4_ACT_GELU_TANH = 3
+} lora4_activation;
+
+/* RMS norm: h = X + R (h = X if R is NULL), Y = h rstd weight with
+ * rstd = 1 / sqrt(mean(h^2) + eps) of each row.
+ *  X, R    : bf16 [M, D]; R may be NULL. 1 <= D <= 16384, any D.
+ *  weight  : bf16 [D]. eps: finite, >= 0.
+ *  H       : bf16 [M, D] output bf16(h), may be NULL (must be without R). May
+ *            be X or R itself; no other overlap is allowed.
+ *  Y       : bf16 [M, D] output (the norm is of the unrounded h), may be NULL
+ *            if codes is given.
+ *  codes, scales_e8m0 : the MXFP8 form of Y, uint8 [M, D] and [M, D / 32], bit
+ *            for bit what quant_pack_mxfp8 gives for the bf16 Y; both or
+ *            neither, D % 32 == 0.
+ * The sum of squares is held in fp32: a row with |h| past about 1e19 is out of
+ * its range. Infinities and NaNs make their own row's outputs non-finite.
+ * M may be 0. Errors: LORA4_ERR_SHAPE, LORA4_ERR_NULL, LORA4_ERR_ALIGN,
+ * LORA4_ERR_HIP. */
+lora4_status lora4_rmsnorm_forward(const uint16_t *X, const uint16_t *R, const uint16_t *weight, int64_t M,
+                                   int64_t D, float eps, uint16_t *H, uint16_t *Y, uint8_t *codes,
+                                   uint8_t *scales_e8m0, void *stream);
+
+/* Backward of the norm at the bf16 h (the forward's H, or its X where there
+ * was no residual): with n = h rstd and t = dY weight,
+ *   dX = rstd (t - n mean(t n)) + dH      (the gradient of X and of R)
+ *   dW = sum over the rows of dY n
+ *  dY, H   : bf16 [M, D]. dH: bf16 [M, D], the gradient that reaches h past
+ *            the norm (the residual stream's), or NULL.
+ *  dX      : bf16 [M, D] output; may be dH itself.
+ *  dW      : bf16 [D] output, or NULL (a frozen weight).
+ *  workspace : lora4_rmsnorm_workspace_bytes(M, D) bytes; only needed with dW,
+ *            may be NULL without.
+ * M may be 0: then dW is set to zero. */
+size_t lora4_rmsnorm_workspace_bytes(int64_t M, int64_t D);
+lora4_status lora4_rmsnorm_backward(const uint16_t *dY, const uint16_t *H, const uint16_t *weight,
+                                    const uint16_t *dH, int64_t M, int64_t D, float eps, uint16_t *dX,
+                                    uint16_t *dW, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gated projections: with the gate's and the up projection's base and adapter,
+ *   G = X deq(Wg)^T + s (X Ag^T) Bg^T,   U = X deq(Wu)^T + s (X Au^T) Bu^T,
+ *   H = act(G) * U                        (of the unrounded G and U)
+ *  W       : 2 E groups: groups 2 e and 2 e + 1 are the gate and the up base
+ *            [N, K] of expert e (E = 1: a plain layer).
+ *  activation : a lora4_activation.
+ *  X       : bf16 [M, K].
+ *  A, B    : bf16 [2 E][r, K] and [2 E][N, r], in the order of W's groups.
+ *  r       : 1 <= r <= 128 (the rank of each projection). s: finite.
+ *  group_offsets : E == 1: NULL; otherwise E + 1 row offsets as for
+ *            lora4_forward.
+ *  H       : bf16 [M, N] output.
+ *  GU      : bf16 [M, 2 N] output, G in columns 0 .. N - 1 and U in N .. 2 N - 1
+ *            (kept for the backward); may be NULL.
+ *  Z       : bf16 [M, 2 r] output, X Ag^T then X Au^T; may be NULL.
+ *  workspace : lora4_gated_workspace_bytes(0, W, M, r) bytes (0 reports
+ *            invalid arguments). Where W has several groups pass W as it is.
+ * Few tokens per expert (single-token decoding, small batches) run a kernel
+ * of their own. LORA4_ERR_SHAPE also for bases past 32-bit offsets within a
+ * group (2 GiB of codes). M may be 0: nothing is launched. */
+size_t lora4_gated_workspace_bytes(int which, const lora4_W *W, int64_t M, int32_t r);
+lora4_status lora4_gated_forward(const lora4_W *W, int32_t activation, const uint16_t *X, int64_t M,
+                                 const uint16_t *A, const uint16_t *B, int32_t r, float s,
+                                 const int64_t *group_offsets, uint16_t *H, uint16_t *GU, uint16_t *Z,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward of the gated projections, from dH and the saved GU:
+ *   dG = dH U act'(G), dU = dH act(G)   (rounded to bf16 for the products)
+ *   dZg = s dG Bg, dX = dG deq(Wg) + dU deq(Wu) + dZg Ag + dZu Au,
+ *   dAg = dZg^T X, dBg = s dG^T Zg, and the same for the up projection.
+ *  GU      : bf16 [M, 2 N] from lora4_gated_forward.
+ *  Z       : bf16 [M, 2 r] from it, or NULL to recompute.
+ *  dX      : bf16 [M, K] output.
+ *  dA, dB  : bf16 [2 E][r, K] and [2 E][N, r] outputs (zero for an expert with
+ *            no rows).
+ *  workspace : lora4_gated_workspace_bytes(1, W, M, r) bytes.
+ * M may be 0: then dA and dB are set to zero. */
+lora4_status lora4_gated_backward(const lora4_W *W, int32_t activation, const uint16_t *X, const uint16_t *dH,
+                                  const uint16_t *GU, int64_t M, const uint16_t *A, const uint16_t *B, int32_t r,
+                                  float s, const int64_t *group_offsets, const uint16_t *Z, uint16_t *dX,
+                                  uint16_t *dA, uint16_t *dB, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/* The linear layer with an epilogue:
+ *   P = X deq(W)^T + s (X A^T) B^T + bias,   Y = act(P) + residual
+ * Arguments as lora4_forward, and
+ *  bias     : bf16 [groups][N], or NULL.
+ *  residual : bf16 [M, N], or NULL; Y may be the residual itself.
+ *  P        : bf16 [M, N] output, the pre-activation kept for the backward;
+ *             may be NULL.
+ *  workspace: lora4_epilogue_workspace_bytes(0, W, M, r) bytes. */
+size_t lora4_epilogue_workspace_bytes(int which, const lora4_W *W, int64_t M, int32_t r);
+lora4_status lora4_forward_epilogue(const lora4_W *W, int32_t activation, const uint16_t *X, int64_t M,
+                                    const uint16_t *A, const uint16_t *B, int32_t r, float s,
+                                    const int64_t *group_offsets, const uint16_t *bias, const uint16_t *residual,
+                                    uint16_t *Y, uint16_t *P, uint16_t *Z, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* Its backward: dP = dY act'(P) (rounded to bf16 for the products), dbias =
+ * the column sums of dP, and dX, dA, dB of lora4_backward for dP. The
+ * residual's gradient is dY itself.
+ *  P     : bf16 [M, N] from lora4_forward_epilogue; may be NULL without an
+ *          activation.
+ *  dbias : bf16 [groups][N] output, or NULL.
+ *  workspace : lora4_epilogue_workspace_bytes(1, W, M, r) bytes.
+ * M may be 0: then dA, dB and dbias are set to zero. */
+lora4_status lora4_backward_epilogue(const lora4_W *W, int32_t activation, const uint16_t *X, const uint16_t *dY,
+                                     const uint16_t *P, int64_t M, const uint16_t *A, const uint16_t *B, int32_t r,
+                                     float s, const int64_t *group_offsets, const uint16_t *Z, uint16_t *dX,
+                                     uint16_t *dA, uint16_t *dB, uint16_t *dbias, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 /* A static, human-readable name for a status code. */
 const char *lora4_status_string(lora4_status status);
 

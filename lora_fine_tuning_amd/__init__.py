@@ -23,12 +23,16 @@ LIB_PATH = os.path.join(HERE, "liblora4.so")
 
 LORA4_NF4, LORA4_NF4_DQ, LORA4_MXFP4, LORA4_NVFP4 = 1, 2, 3, 4
 FORMATS = {"nf4": LORA4_NF4, "nf4_dq": LORA4_NF4_DQ, "mxfp4": LORA4_MXFP4, "nvfp4": LORA4_NVFP4}
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
 BLOCK = {LORA4_NF4: 64, LORA4_NF4_DQ: 64, LORA4_MXFP4: 32, LORA4_NVFP4: 16}
 
 EXPORTS = ["lora4_forward", "lora4_forward_noalloc", "lora4_backward", "lora4_workspace_bytes", "lora4_packed_bytes",
            "lora4_forward_multi", "lora4_backward_multi", "lora4_workspace_bytes_multi", "quant_pack_nf4",
            "quant_pack_mxfp4", "quant_pack_nvfp4", "quant_pack_mxfp8", "lora4_workspace_bytes_mx", "lora4_forward_mx",
            "lora4_loftq_workspace_bytes", "lora4_loftq_init", "lora4_import_rowmajor",
+           "lora4_rmsnorm_workspace_bytes", "lora4_rmsnorm_forward", "lora4_rmsnorm_backward",
+           "lora4_gated_workspace_bytes", "lora4_gated_forward", "lora4_gated_backward",
+           "lora4_epilogue_workspace_bytes", "lora4_forward_epilogue", "lora4_backward_epilogue",
            "lora4_status_string", "lora4_timing_enable", "lora4_timing_collect", "lora4_version"]
 
 
@@ -94,6 +98,25 @@ def lib():
         L.lora4_loftq_init.restype = ctypes.c_int
         L.lora4_import_rowmajor.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp, vp]
         L.lora4_import_rowmajor.restype = ctypes.c_int
+        L.lora4_rmsnorm_workspace_bytes.argtypes = [i64, i64]
+        L.lora4_rmsnorm_workspace_bytes.restype = sz
+        L.lora4_rmsnorm_forward.argtypes = [vp, vp, vp, i64, i64, f32, vp, vp, vp, vp, vp]
+        L.lora4_rmsnorm_forward.restype = ctypes.c_int
+        L.lora4_rmsnorm_backward.argtypes = [vp, vp, vp, vp, i64, i64, f32, vp, vp, vp, sz, vp]
+        L.lora4_rmsnorm_backward.restype = ctypes.c_int
+        L.lora4_gated_workspace_bytes.argtypes = [ctypes.c_int, Wp, i64, i32]
+        L.lora4_gated_workspace_bytes.restype = sz
+        L.lora4_gated_forward.argtypes = [Wp, i32, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, sz, vp]
+        L.lora4_gated_forward.restype = ctypes.c_int
+        L.lora4_gated_backward.argtypes = [Wp, i32, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.lora4_gated_backward.restype = ctypes.c_int
+        L.lora4_epilogue_workspace_bytes.argtypes = [ctypes.c_int, Wp, i64, i32]
+        L.lora4_epilogue_workspace_bytes.restype = sz
+        L.lora4_forward_epilogue.argtypes = [Wp, i32, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.lora4_forward_epilogue.restype = ctypes.c_int
+        L.lora4_backward_epilogue.argtypes = [Wp, i32, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp,
+                                              sz, vp]
+        L.lora4_backward_epilogue.restype = ctypes.c_int
         L.lora4_status_string.argtypes = [ctypes.c_int]
         L.lora4_status_string.restype = ctypes.c_char_p
         L.lora4_timing_enable.argtypes = [ctypes.c_int]
@@ -195,6 +218,49 @@ def lora4_import_rowmajor(fmt, N, K, groups, codes_rm, scales_rm, codes, scales,
 
 def lora4_forward_mx(W, X, M, A, B, r, s, Y, Z, workspace, workspace_bytes, stream):
     return lib().lora4_forward_mx(ctypes.byref(W), X, M, A, B, r, s, Y, Z, workspace, workspace_bytes, stream)
+
+
+def lora4_rmsnorm_workspace_bytes(M, D):
+    return lib().lora4_rmsnorm_workspace_bytes(M, D)
+
+
+def lora4_rmsnorm_forward(X, R, weight, M, D, eps, H, Y, codes, scales_e8m0, stream):
+    return lib().lora4_rmsnorm_forward(X, R, weight, M, D, eps, H, Y, codes, scales_e8m0, stream)
+
+
+def lora4_rmsnorm_backward(dY, H, weight, dH, M, D, eps, dX, dW, workspace, workspace_bytes, stream):
+    return lib().lora4_rmsnorm_backward(dY, H, weight, dH, M, D, eps, dX, dW, workspace, workspace_bytes, stream)
+
+
+def lora4_gated_workspace_bytes(which, W, M, r):
+    return lib().lora4_gated_workspace_bytes(which, ctypes.byref(W), M, r)
+
+
+def lora4_gated_forward(W, activation, X, M, A, B, r, s, group_offsets, H, GU, Z, workspace, workspace_bytes, stream):
+    return lib().lora4_gated_forward(ctypes.byref(W), activation, X, M, A, B, r, s, group_offsets, H, GU, Z,
+                                     workspace, workspace_bytes, stream)
+
+
+def lora4_gated_backward(W, activation, X, dH, GU, M, A, B, r, s, group_offsets, Z, dX, dA, dB, workspace,
+                         workspace_bytes, stream):
+    return lib().lora4_gated_backward(ctypes.byref(W), activation, X, dH, GU, M, A, B, r, s, group_offsets, Z, dX,
+                                      dA, dB, workspace, workspace_bytes, stream)
+
+
+def lora4_epilogue_workspace_bytes(which, W, M, r):
+    return lib().lora4_epilogue_workspace_bytes(which, ctypes.byref(W), M, r)
+
+
+def lora4_forward_epilogue(W, activation, X, M, A, B, r, s, group_offsets, bias, residual, Y, P, Z, workspace,
+                           workspace_bytes, stream):
+    return lib().lora4_forward_epilogue(ctypes.byref(W), activation, X, M, A, B, r, s, group_offsets, bias, residual,
+                                        Y, P, Z, workspace, workspace_bytes, stream)
+
+
+def lora4_backward_epilogue(W, activation, X, dY, P, M, A, B, r, s, group_offsets, Z, dX, dA, dB, dbias, workspace,
+                            workspace_bytes, stream):
+    return lib().lora4_backward_epilogue(ctypes.byref(W), activation, X, dY, P, M, A, B, r, s, group_offsets, Z, dX,
+                                         dA, dB, dbias, workspace, workspace_bytes, stream)
 
 
 def timing_enable(on=True):
@@ -621,3 +687,290 @@ def loftq_init(W, r, iters=5, s=1.0, double_quant=False):
     _check(lora4_loftq_init(_ptr(W), N, K, r, iters, float(s), 1 if double_quant else 0, _ptr(codes), _ptr(scales),
                             _ptr(scales2), _ptr(A), _ptr(B), _ptr(ws), ws.numel(), _stream()), "lora4_loftq_init")
     return PackedBase(fmt, N, K, 1, codes, scales, scales2), A, B
+
+
+# ---------------------------------------------------------------------------
+# The feed-forward half of a block: RMS norm, gated projections, the linear
+# with an epilogue
+# ---------------------------------------------------------------------------
+
+def _on_device(dev):
+    """The device's current stream, with the device made current for the call
+    (kernels launch on the current device). Returns (stream, guard)."""
+    import contextlib
+    import torch
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {dev}")
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        return stream, contextlib.nullcontext()
+    return stream, torch.cuda.device(dev)
+
+
+def _workspace(n, what, dev):
+    import torch
+    if n == 0:
+        raise ValueError(f"invalid arguments for {what}")
+    return torch.empty((n,), dtype=torch.uint8, device=dev)
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _check_norm(X, weight, name="X"):
+    import torch
+    if X is None or X.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor [M, D]")
+    M, D = X.shape
+    _need(X, name, (M, D), torch.bfloat16)
+    _need(weight, "weight", (D,), torch.bfloat16, X.device)
+    return M, D
+
+
+def rmsnorm(X, weight, eps, residual=None, mx=False, want_y=True, out=None):
+    """RMS norm of bf16 X [M, D] (of X + residual where one is given) with
+    weight [D]: {"Y", "H", "codes", "scales"}, None for what was not asked for.
+    H is the bf16 sum X + residual; mx: Y as MXFP8 too, E4M3 codes [M, D] and
+    E8M0 scales [M, D / 32] (uint8), those of mxfp8(Y). `out` may hold
+    caller-allocated outputs under these keys; H may be X or the residual
+    itself."""
+    import torch
+    out = out or {}
+    M, D = _check_norm(X, weight)
+    dev = X.device
+    if residual is not None:
+        _need(residual, "residual", (M, D), torch.bfloat16, dev)
+    elif out.get("H") is not None:
+        raise ValueError("H is only an output with a residual")
+    for name, shape, dtype in (("Y", (M, D), torch.bfloat16), ("H", (M, D), torch.bfloat16),
+                               ("codes", (M, D), torch.uint8), ("scales", (M, D // 32), torch.uint8)):
+        if out.get(name) is not None:
+            _need(out[name], name, shape, dtype, dev)
+    mx = mx or out.get("codes") is not None or out.get("scales") is not None
+    if mx and D % 32 != 0:
+        raise ValueError("the MXFP8 output needs D % 32 == 0")
+    if not want_y and not mx:
+        raise ValueError("nothing to compute: want_y or mx")
+    Y = _out(out.get("Y"), (M, D), dev) if want_y or out.get("Y") is not None else None
+    H = _out(out.get("H"), (M, D), dev) if residual is not None else None
+    codes = scales = None
+    if mx:
+        codes, scales = out.get("codes"), out.get("scales")
+        if codes is None:
+            codes = torch.empty((M, D), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty((M, D // 32), dtype=torch.uint8, device=dev)
+    stream, guard = _on_device(dev)
+    with guard:
+        st = lora4_rmsnorm_forward(_ptr(X), _ptr(residual), _ptr(weight), M, D, float(eps), _ptr(H), _ptr(Y),
+                                   _ptr(codes), _ptr(scales), stream)
+    _check(st, "lora4_rmsnorm_forward")
+    return {"Y": Y, "H": H, "codes": codes, "scales": scales}
+
+
+def rmsnorm_workspace(M, D, device):
+    """Workspace of rmsnorm_backward with a weight gradient."""
+    return _workspace(lora4_rmsnorm_workspace_bytes(M, D), "lora4_rmsnorm_workspace_bytes", device)
+
+
+def rmsnorm_backward(dY, H, weight, eps, dH=None, want_dw=True, workspace=None, out=None):
+    """Backward of rmsnorm at H (its H output, or its X where there was no
+    residual): {"dX", "dW"}. dH: the gradient that reaches H past the norm;
+    dX is the gradient of X and of the residual, and may be dH itself (`out`).
+    want_dw False: a frozen weight."""
+    import torch
+    out = out or {}
+    M, D = _check_norm(H, weight, "H")
+    dev, bf = H.device, torch.bfloat16
+    _need(dY, "dY", (M, D), bf, dev)
+    if dH is not None:
+        _need(dH, "dH", (M, D), bf, dev)
+    for name, shape in (("dX", (M, D)), ("dW", (D,))):
+        if out.get(name) is not None:
+            _need(out[name], name, shape, bf, dev)
+    dX = _out(out.get("dX"), (M, D), dev)
+    dW = _out(out.get("dW"), (D,), dev) if want_dw or out.get("dW") is not None else None
+    if dW is not None:
+        need = lora4_rmsnorm_workspace_bytes(M, D)
+        if workspace is None:
+            workspace = _workspace(need, "lora4_rmsnorm_workspace_bytes", dev)
+        _check_workspace(workspace, need, dev)
+    stream, guard = _on_device(dev)
+    with guard:
+        st = lora4_rmsnorm_backward(_ptr(dY), _ptr(H), _ptr(weight), _ptr(dH), M, D, float(eps), _ptr(dX), _ptr(dW),
+                                    _ptr(workspace), 0 if workspace is None else workspace.numel(), stream)
+    _check(st, "lora4_rmsnorm_backward")
+    return {"dX": dX, "dW": dW}
+
+
+def check_gated_args(base, X, A, B, offsets=None, tensors=()):
+    """Validates the tensors of a gated call before any pointer reaches the
+    library: base with 2 E groups (gate and up of each expert), X [M, K],
+    A [2 E, r, K], B [2 E, N, r], offsets int64 [E + 1] for E > 1, and `tensors`,
+    (name, tensor, shape) triples of bf16 tensors that may be None. Returns
+    (M, r, E)."""
+    import torch
+    if base.groups % 2 != 0:
+        raise ValueError("a gated base has two groups per expert: the gate's, then the up projection's")
+    if A is None or A.dim() != 3:
+        raise ValueError(f"A must be [{base.groups}, r, K]")
+    M, r, _ = check_layer_args(PackedBase(base.fmt, base.N, base.K, 1, base.codes, base.scales, base.scales2), X,
+                               A[0], B[0] if B is not None and B.dim() == 3 else B)
+    bf, dev, E = torch.bfloat16, X.device, base.groups // 2
+    _need(A, "A", (2 * E, r, base.K), bf, dev)
+    _need(B, "B", (2 * E, base.N, r), bf, dev)
+    if E > 1:
+        _need(offsets, "group offsets", (E + 1,), torch.int64, dev)
+    elif offsets is not None:
+        raise ValueError("group offsets are only taken with several experts")
+    for name, t, shape in tensors:
+        if t is not None:
+            _need(t, name, shape, bf, dev)
+    return M, r, E
+
+
+def gated_workspace(which, base, M, r):
+    """Workspace of gated_forward (which = 0) or gated_backward (1)."""
+    return _workspace(lora4_gated_workspace_bytes(which, base.abi(), M, r), "lora4_gated_workspace_bytes",
+                      base.codes.device)
+
+
+def gated_forward(base, X, A, B, s, activation="silu", group_offsets=None, want_saved=True, workspace=None, out=None):
+    """H = act(G) * U with G, U the gate and up projections of bf16 X [M, K]:
+    {"H" [M, N], "GU" [M, 2 N], "Z" [M, 2 r]}; GU and Z, which the backward
+    takes, are None without want_saved. base: 2 E groups (pack_nf4 and its like
+    of W [2 E, N, K]: gate and up of each expert); A [2 E, r, K], B [2 E, N, r]."""
+    out = out or {}
+    act = _activation(activation)
+    M, N = (X.shape[0], base.N) if X is not None and X.dim() == 2 else (0, base.N)
+    r = A.shape[-2] if A is not None and A.dim() == 3 else 0
+    M, r, _ = check_gated_args(base, X, A, B, group_offsets, [
+        ("H", out.get("H"), (M, N)), ("GU", out.get("GU"), (M, 2 * N)), ("Z", out.get("Z"), (M, 2 * r))])
+    dev = X.device
+    H = _out(out.get("H"), (M, N), dev)
+    GU = _out(out.get("GU"), (M, 2 * N), dev) if want_saved or out.get("GU") is not None else None
+    Z = _out(out.get("Z"), (M, 2 * r), dev) if want_saved or out.get("Z") is not None else None
+    W = base.abi()
+    stream, guard = _on_device(dev)
+    with guard:
+        need = lora4_gated_workspace_bytes(0, W, M, r)
+        if workspace is None or need == 0:
+            workspace = _workspace(need, "lora4_gated_workspace_bytes", dev)
+        _check_workspace(workspace, need, dev)
+        st = lora4_gated_forward(W, act, _ptr(X), M, _ptr(A), _ptr(B), r, float(s), _ptr(group_offsets), _ptr(H),
+                                 _ptr(GU), _ptr(Z), _ptr(workspace), workspace.numel(), stream)
+    _check(st, "lora4_gated_forward")
+    return {"H": H, "GU": GU, "Z": Z}
+
+
+def gated_backward(base, X, dH, GU, A, B, s, activation="silu", Z=None, group_offsets=None, workspace=None, out=None):
+    """dX [M, K], dA [2 E, r, K], dB [2 E, N, r] of the gated projections for
+    dH [M, N] and gated_forward's GU (and Z, or None to recompute it)."""
+    import torch
+    out = out or {}
+    act = _activation(activation)
+    M, N = (X.shape[0], base.N) if X is not None and X.dim() == 2 else (0, base.N)
+    r = A.shape[-2] if A is not None and A.dim() == 3 else 0
+    if dH is None or GU is None:
+        raise ValueError("dH and GU are required")
+    M, r, _ = check_gated_args(base, X, A, B, group_offsets, [
+        ("dH", dH, (M, N)), ("GU", GU, (M, 2 * N)), ("Z", Z, (M, 2 * r)), ("dX", out.get("dX"), (M, base.K)),
+        ("dA", out.get("dA"), tuple(A.shape)), ("dB", out.get("dB"), None if B is None else tuple(B.shape))])
+    dev = X.device
+    dX = _out(out.get("dX"), (M, base.K), dev)
+    dA = out.get("dA") if out.get("dA") is not None else torch.empty_like(A)
+    dB = out.get("dB") if out.get("dB") is not None else torch.empty_like(B)
+    W = base.abi()
+    stream, guard = _on_device(dev)
+    with guard:
+        need = lora4_gated_workspace_bytes(1, W, M, r)
+        if workspace is None or need == 0:
+            workspace = _workspace(need, "lora4_gated_workspace_bytes", dev)
+        _check_workspace(workspace, need, dev)
+        st = lora4_gated_backward(W, act, _ptr(X), _ptr(dH), _ptr(GU), M, _ptr(A), _ptr(B), r, float(s),
+                                  _ptr(group_offsets), _ptr(Z), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(workspace),
+                                  workspace.numel(), stream)
+    _check(st, "lora4_gated_backward")
+    return {"dX": dX, "dA": dA, "dB": dB}
+
+
+def epilogue_workspace(which, base, M, r):
+    """Workspace of forward_epilogue (which = 0) or backward_epilogue (1)."""
+    return _workspace(lora4_epilogue_workspace_bytes(which, base.abi(), M, r), "lora4_epilogue_workspace_bytes",
+                      base.codes.device)
+
+
+def _bias_shape(base):
+    return (base.N,) if base.groups == 1 else (base.groups, base.N)
+
+
+def forward_epilogue(base, X, A, B, s, bias=None, activation="none", residual=None, group_offsets=None,
+                     want_saved=True, workspace=None, out=None):
+    """Y = act(P) + residual, P = X deq(W)^T + s (X A^T) B^T + bias: {"Y", "P",
+    "Z"}. P [M, N] (only with an activation) and Z [M, r], which the backward
+    takes, are None without want_saved. bias [N] ([E, N] with experts), residual
+    [M, N]; Y may be the residual itself (`out`)."""
+    import torch
+    out = out or {}
+    act = _activation(activation)
+    M, N = (X.shape[0], base.N) if X is not None and X.dim() == 2 else (0, base.N)
+    r = A.shape[-2] if A is not None and A.dim() >= 2 else 0
+    M, r, _ = check_layer_args(base, X, A, B, offsets=group_offsets, outputs=[
+        ("Y", out.get("Y"), (M, N)), ("P", out.get("P"), (M, N)), ("Z", out.get("Z"), (M, r)),
+        ("residual", residual, (M, N)), ("bias", bias, _bias_shape(base))])
+    dev = X.device
+    Y = _out(out.get("Y"), (M, N), dev)
+    P = _out(out.get("P"), (M, N), dev) if (want_saved and act) or out.get("P") is not None else None
+    Z = _out(out.get("Z"), (M, r), dev) if want_saved or out.get("Z") is not None else None
+    W = base.abi()
+    stream, guard = _on_device(dev)
+    with guard:
+        need = lora4_epilogue_workspace_bytes(0, W, M, r)
+        if workspace is None or need == 0:
+            workspace = _workspace(need, "lora4_epilogue_workspace_bytes", dev)
+        _check_workspace(workspace, need, dev)
+        st = lora4_forward_epilogue(W, act, _ptr(X), M, _ptr(A), _ptr(B), r, float(s), _ptr(group_offsets),
+                                    _ptr(bias), _ptr(residual), _ptr(Y), _ptr(P), _ptr(Z), _ptr(workspace),
+                                    workspace.numel(), stream)
+    _check(st, "lora4_forward_epilogue")
+    return {"Y": Y, "P": P, "Z": Z}
+
+
+def backward_epilogue(base, X, dY, A, B, s, P=None, activation="none", Z=None, want_dbias=False, group_offsets=None,
+                      workspace=None, out=None):
+    """dX, dA, dB and (want_dbias) dbias of forward_epilogue for dY; P is its
+    pre-activation (required with an activation), Z its Z or None to
+    recompute. The residual's gradient is dY."""
+    import torch
+    out = out or {}
+    act = _activation(activation)
+    if act and P is None:
+        raise ValueError("the pre-activation P is required with an activation")
+    M, N = (X.shape[0], base.N) if X is not None and X.dim() == 2 else (0, base.N)
+    if dY is None:
+        raise ValueError("dY is required")
+    M, r, _ = check_layer_args(base, X, A, B, dY=dY, Z=Z, offsets=group_offsets, outputs=[
+        ("P", P, (M, N)), ("dX", out.get("dX"), (M, base.K)),
+        ("dA", out.get("dA"), None if A is None else tuple(A.shape)),
+        ("dB", out.get("dB"), None if B is None else tuple(B.shape)), ("dbias", out.get("dbias"), _bias_shape(base))])
+    dev = X.device
+    dX = _out(out.get("dX"), (M, base.K), dev)
+    dA = out.get("dA") if out.get("dA") is not None else torch.empty_like(A)
+    dB = out.get("dB") if out.get("dB") is not None else torch.empty_like(B)
+    want_dbias = want_dbias or out.get("dbias") is not None
+    dbias = _out(out.get("dbias"), _bias_shape(base), dev) if want_dbias else None
+    W = base.abi()
+    stream, guard = _on_device(dev)
+    with guard:
+        need = lora4_epilogue_workspace_bytes(1, W, M, r)
+        if workspace is None or need == 0:
+            workspace = _workspace(need, "lora4_epilogue_workspace_bytes", dev)
+        _check_workspace(workspace, need, dev)
+        st = lora4_backward_epilogue(W, act, _ptr(X), _ptr(dY), _ptr(P), M, _ptr(A), _ptr(B), r, float(s),
+                                     _ptr(group_offsets), _ptr(Z), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(dbias),
+                                     _ptr(workspace), workspace.numel(), stream)
+    _check(st, "lora4_backward_epilogue")
+    return {"dX": dX, "dA": dA, "dB": dB, "dbias": dbias}

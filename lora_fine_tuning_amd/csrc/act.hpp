@@ -1,0 +1,78 @@
+// The activations of the feed-forward operators and their derivatives, in
+// fp32. exp and erf are the device library's; sigmoid and tanh are both taken
+// from one exponential, e^-|y| (never overflows), and one reciprocal:
+//   sigmoid(x) = 1 / (1 + e^-x),  (1 + tanh u) / 2 = sigmoid(2 u).
+#pragma once
+
+#include "common.hpp"
+
+namespace lora4 {
+
+enum Act : int { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3 };
+
+// 1 / (1 + e^-x): e^-|x| in (0, 1], so neither it nor the sum overflows. The
+// exponential and the reciprocal are the hardware's (about one unit in the
+// last place each, far below the bf16 rounding of what they feed).
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  const float e = __expf(-fabsf(x));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  return x >= 0.0f ? r : e * r;
+}
+
+constexpr float GELU_K = 0.7978845608028654f;    // sqrt(2 / pi)
+constexpr float GELU_C = 0.044715f;
+constexpr float SQRT_HALF = 0.7071067811865476f;
+constexpr float INV_SQRT_2PI = 0.3989422804014327f;
+
+// act(x). An infinite x gives the limit: x at +inf; at -inf 0 (the finite
+// factor is taken first, so no 0 * inf).
+__device__ __forceinline__ float act_value(float x, int act) {
+  if (act == ACT_NONE) return x;
+  float p;
+  if (act == ACT_SILU) p = sigmoid_f32(x);
+  else if (act == ACT_GELU) p = 0.5f * erfcf(-x * SQRT_HALF);
+  else p = sigmoid_f32(2.0f * GELU_K * (x + GELU_C * x * x * x));
+  return p == 0.0f ? 0.0f : x * p;
+}
+
+// Eight values at once; the choice of activation is outside the loop.
+__device__ __forceinline__ void act_value8(float (&v)[8], int act) {
+  if (act == ACT_SILU) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], ACT_SILU);
+  } else if (act == ACT_GELU) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], ACT_GELU);
+  } else if (act == ACT_GELU_TANH) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], ACT_GELU_TANH);
+  }
+}
+
+// act(x) and act'(x).
+__device__ __forceinline__ void act_value_slope(float x, int act, float &v, float &d) {
+  if (act == ACT_NONE) {
+    v = x;
+    d = 1.0f;
+    return;
+  }
+  float p, xdp;   // act(x) = x p(x); xdp = x p'(x)
+  if (act == ACT_SILU) {
+    p = sigmoid_f32(x);
+    const float q = p * sigmoid_f32(-x);   // p (1 - p), without cancellation
+    xdp = q == 0.0f ? 0.0f : x * q;
+  } else if (act == ACT_GELU) {
+    p = 0.5f * erfcf(-x * SQRT_HALF);
+    const float q = INV_SQRT_2PI * __expf(-0.5f * x * x);
+    xdp = q == 0.0f ? 0.0f : x * q;
+  } else {
+    const float u2 = 2.0f * GELU_K * (x + GELU_C * x * x * x);
+    p = sigmoid_f32(u2);
+    const float q = p * sigmoid_f32(-u2);
+    xdp = q == 0.0f ? 0.0f : x * q * (2.0f * GELU_K) * (1.0f + 3.0f * GELU_C * x * x);
+  }
+  v = p == 0.0f ? 0.0f : x * p;
+  d = p + xdp;
+}
+
+}  // namespace lora4

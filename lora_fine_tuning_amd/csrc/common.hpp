@@ -28,6 +28,10 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
+// 16 bytes in global memory at a 2-byte aligned address: rows of an odd number
+// of elements (amdhsa runs with unaligned global access).
+typedef uint32_t u32x4_a2_t __attribute__((ext_vector_type(4), aligned(2)));
+
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 
 // Two fp32 values -> one word of two bf16 (round to nearest even, the
@@ -107,6 +111,14 @@ __device__ __forceinline__ u32x4_t ldg_b128(const void *p) {
 __device__ __forceinline__ u32x4_t ldg_b128_cached(const void *p) {
   return *reinterpret_cast<const u32x4_t *>(p);
 }
+
+// bf16 matrix, row-major with leading dimension ld (elements); per-group
+// element offset gstride (0 when the operand is shared by all groups).
+struct Mat {
+  const uint16_t *p;
+  int64_t ld;
+  int64_t gstride;
+};
 
 // Row range of one row tile of a (possibly grouped) problem.
 struct RowTile {

@@ -1,0 +1,109 @@
+// Instantiations of the feed-forward operators' kernels (ffn.hpp).
+#include "ffn.hpp"
+
+namespace lora4 {
+namespace ffn {
+
+namespace {
+
+template <typename K>
+const void *addr(K *k) {
+  return reinterpret_cast<const void *>(k);
+}
+
+template <bool WAVE, int VPT>
+const void *norm_fwd(bool mx) {
+  return mx ? addr(norm::k_rmsnorm_fwd<WAVE, VPT, true>) : addr(norm::k_rmsnorm_fwd<WAVE, VPT, false>);
+}
+
+template <bool WAVE, int VPT>
+const void *norm_bwd(bool dw) {
+  return dw ? addr(norm::k_rmsnorm_bwd<WAVE, VPT, true>) : addr(norm::k_rmsnorm_bwd<WAVE, VPT, false>);
+}
+
+template <int FMT, int EPI>
+const void *tile(int rows, bool short_rows) {
+  constexpr int NJ_SMALL = EPI == fwd::EPI_GATED ? 2 : 1;
+  if (rows == 64) return addr(fwd::k_gemm_fwd_epi<FMT, EPI, 64, NJ_SMALL, false>);
+  if (rows == 128) return addr(fwd::k_gemm_fwd_epi<FMT, EPI, 128, NJ_SMALL, false>);
+  return short_rows ? addr(fwd::k_gemm_fwd_epi<FMT, EPI, 256, 2, true>)
+                    : addr(fwd::k_gemm_fwd_epi<FMT, EPI, 256, 2, false>);
+}
+
+template <int FMT, int EPI, int NW>
+const void *small_nw(int mt) {
+  switch (mt) {
+    case 1: return addr(small::k_small<FMT, EPI, 1, NW>);
+    case 2: return addr(small::k_small<FMT, EPI, 2, NW>);
+    default: return addr(small::k_small<FMT, EPI, 4, NW>);
+  }
+}
+
+template <int FMT>
+const void *tile_of(int epi, int rows, bool short_rows) {
+  return epi == fwd::EPI_GATED ? tile<FMT, fwd::EPI_GATED>(rows, short_rows)
+                               : tile<FMT, fwd::EPI_FUSED>(rows, short_rows);
+}
+
+template <int FMT>
+const void *small_of(int epi, int mt, int nw) {
+  if (epi == fwd::EPI_GATED)
+    return nw == 4 ? small_nw<FMT, fwd::EPI_GATED, 4>(mt) : small_nw<FMT, fwd::EPI_GATED, 8>(mt);
+  return nw == 4 ? small_nw<FMT, fwd::EPI_FUSED, 4>(mt) : small_nw<FMT, fwd::EPI_FUSED, 8>(mt);
+}
+
+}  // namespace
+
+// One wave per row up to 1024 elements; above, a block of as many waves as
+// hold the row at two vectors per thread.
+NormShape norm_shape(int D) {
+  const int nv = (D + 7) / 8;
+  if (nv <= 128) return {64, nv <= 64 ? 1 : 2};
+  return {64 * ((nv + 127) / 128), 2};
+}
+
+const void *norm_fwd_kernel(NormShape s, bool mx) {
+  if (s.threads == 64) return s.vpt == 1 ? norm_fwd<true, 1>(mx) : norm_fwd<true, 2>(mx);
+  return norm_fwd<false, 2>(mx);
+}
+
+const void *norm_bwd_kernel(NormShape s, bool dw) {
+  if (s.threads == 64) return s.vpt == 1 ? norm_bwd<true, 1>(dw) : norm_bwd<true, 2>(dw);
+  return norm_bwd<false, 2>(dw);
+}
+
+const void *col_sum_kernel() { return addr(norm::k_col_sum); }
+
+const void *tile_kernel(int fmt, int epi, int rows, bool short_rows) {
+  switch (fmt) {
+    case FMT_NF4: return tile_of<FMT_NF4>(epi, rows, short_rows);
+    case FMT_NF4_DQ: return tile_of<FMT_NF4_DQ>(epi, rows, short_rows);
+    case FMT_MXFP4: return tile_of<FMT_MXFP4>(epi, rows, short_rows);
+    default: return tile_of<FMT_NVFP4>(epi, rows, short_rows);
+  }
+}
+
+const void *small_kernel(int fmt, int epi, int mt, int nw) {
+  switch (fmt) {
+    case FMT_NF4: return small_of<FMT_NF4>(epi, mt, nw);
+    case FMT_NF4_DQ: return small_of<FMT_NF4_DQ>(epi, mt, nw);
+    case FMT_MXFP4: return small_of<FMT_MXFP4>(epi, mt, nw);
+    default: return small_of<FMT_NVFP4>(epi, mt, nw);
+  }
+}
+
+const void *small_z_kernel() { return addr(small::k_small_z); }
+
+const void *gated_bwd_kernel(int tj) {
+  switch (tj) {
+    case 1: return addr(actbwd::k_gated_bwd<1>);
+    case 2: return addr(actbwd::k_gated_bwd<2>);
+    case 4: return addr(actbwd::k_gated_bwd<4>);
+    default: return addr(actbwd::k_gated_bwd<8>);
+  }
+}
+
+const void *act_bwd_kernel() { return addr(actbwd::k_act_bwd); }
+
+}  // namespace ffn
+}  // namespace lora4

@@ -1,0 +1,473 @@
+// Host side of the feed-forward operators (included by lora4.hip behind its
+// planning and dispatch helpers): validation, workspace layout and launch
+// order of the RMS norm, the gated projections and the linear with an epilogue.
+//
+//   gated forward   : M <= SMALL_ROWS tokens per group: Z = X A^T (k_small_z),
+//                     then k_small; else the rank-r row pass (both projections'
+//                     A as one operand of 2 r rows), then the gated tiles
+//   gated backward  : [Z pass] -> k_gated_bwd (dG, dU, partial dZ) -> dX over
+//                     both projections as one reduction -> dA, dB
+//   fused forward   : as the gated, with one projection
+//   fused backward  : k_act_bwd (dP, column sums) -> dbias -> lora4_backward
+#pragma once
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Launch by kernel address (ffn.hpp)
+// ---------------------------------------------------------------------------
+
+template <typename... Args>
+lora4_status launch_fn(const char *name, const void *fn, int64_t blocks, int threads, size_t lds, hipStream_t st,
+                       Args... args) {
+  if (blocks <= 0) return LORA4_OK;
+  if (blocks > INT32_MAX) return LORA4_ERR_SHAPE;
+  if (lds > 64 * 1024) TRY(set_lds_limit(fn, lds));
+  void *argv[] = {(void *)&args...};
+  return launch_timed(name, st, [&] {
+    (void)hipLaunchKernel(fn, dim3((unsigned)blocks), dim3((unsigned)threads), argv, lds, st);
+  });
+}
+
+bool all_aligned16(std::initializer_list<const void *> ps) {
+  for (const void *p : ps)
+    if (p && !aligned16(p)) return false;
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// RMS norm
+// ---------------------------------------------------------------------------
+
+// Blocks of the norm's grids: enough for the chip to be full several times
+// over (rows beyond them are walked in steps of the grid).
+constexpr int64_t NORM_MAX_BLOCKS = 1 << 16;
+// Blocks with dW: each keeps a row of fp32 sums to be added up afterwards.
+constexpr int64_t NORM_DW_BLOCKS = 512;
+
+int norm_rows_per_block(ffn::NormShape s) { return s.threads == 64 ? norm::WAVE_ROWS : 1; }
+
+int64_t norm_dw_blocks(int64_t M, int64_t D) {
+  const ffn::NormShape s = ffn::norm_shape((int)D);
+  return std::min<int64_t>(NORM_DW_BLOCKS, ceil_div(M, norm_rows_per_block(s)));
+}
+
+size_t norm_ws_bytes(int64_t M, int64_t D) {
+  const ffn::NormShape s = ffn::norm_shape((int)D);
+  return align256((size_t)std::max<int64_t>(1, norm_dw_blocks(M, D)) * norm_rows_per_block(s) * D * 4);
+}
+
+lora4_status check_norm(int64_t M, int64_t D, float eps) {
+  if (M < 0 || M > (int64_t(1) << 31) || D < 1 || D > norm::MAX_D) return LORA4_ERR_SHAPE;
+  if (!std::isfinite(eps) || eps < 0.0f) return LORA4_ERR_SHAPE;
+  return LORA4_OK;
+}
+
+// dW of zero rows
+lora4_status fill_zero(uint16_t *p, int64_t n, hipStream_t st) {
+  return launch_args("fill_zero", k_fill_u16, dim3((unsigned)ceil_div(n, 256)), dim3(256), st, p, n, (uint16_t)0);
+}
+
+lora4_status norm_forward(const uint16_t *X, const uint16_t *R, const uint16_t *w, int64_t M, int64_t D, float eps,
+                          uint16_t *H, uint16_t *Y, uint8_t *codes, uint8_t *scales, hipStream_t st) {
+  TRY(check_norm(M, D, eps));
+  if (codes && D % 32 != 0) return LORA4_ERR_SHAPE;
+  if (!w || (M > 0 && !X) || (!codes) != (!scales) || (M > 0 && !Y && !codes) || (H && !R && M > 0))
+    return LORA4_ERR_NULL;
+  if (!all_aligned16({X, R, w, H, Y, codes, scales})) return LORA4_ERR_ALIGN;
+  if (M == 0) return LORA4_OK;
+  const norm::FwdParams p{X, R, w, M, (int)D, eps, H, Y, codes, scales};
+  const ffn::NormShape s = ffn::norm_shape((int)D);
+  const int64_t blocks = std::min(NORM_MAX_BLOCKS, ceil_div(M, norm_rows_per_block(s)));
+  return launch_fn("rmsnorm_fwd", ffn::norm_fwd_kernel(s, codes != nullptr), blocks,
+                   s.threads == 64 ? 64 * norm::WAVE_ROWS : s.threads, 0, st, p);
+}
+
+lora4_status norm_backward(const uint16_t *dY, const uint16_t *H, const uint16_t *w, const uint16_t *dH, int64_t M,
+                           int64_t D, float eps, uint16_t *dX, uint16_t *dW, void *ws, size_t ws_bytes,
+                           hipStream_t st) {
+  TRY(check_norm(M, D, eps));
+  if (!w || (M > 0 && (!dY || !H || !dX))) return LORA4_ERR_NULL;
+  if (!all_aligned16({dY, H, w, dH, dX, dW, ws})) return LORA4_ERR_ALIGN;
+  if (dW && M > 0 && (!ws || ws_bytes < norm_ws_bytes(M, D))) return LORA4_ERR_WORKSPACE;
+  if (M == 0) return dW ? fill_zero(dW, D, st) : LORA4_OK;
+  const ffn::NormShape s = ffn::norm_shape((int)D);
+  const int64_t per = norm_rows_per_block(s);
+  const int64_t blocks = dW ? norm_dw_blocks(M, D) : std::min(NORM_MAX_BLOCKS, ceil_div(M, per));
+  const norm::BwdParams p{dY, H, w, dH, M, (int)D, eps, dX, dW ? reinterpret_cast<float *>(ws) : nullptr};
+  TRY(launch_fn("rmsnorm_bwd", ffn::norm_bwd_kernel(s, dW != nullptr), blocks,
+                s.threads == 64 ? 64 * norm::WAVE_ROWS : s.threads, 0, st, p));
+  if (!dW) return LORA4_OK;
+  return launch_fn("rmsnorm_dw", ffn::col_sum_kernel(), ceil_div(D, 32), 1024, 0, st, (const float *)ws,
+                   (int)(blocks * per), (int)D, dW);
+}
+
+// ---------------------------------------------------------------------------
+// Gated and fused forward
+// ---------------------------------------------------------------------------
+
+// An operator's base: E row groups with P projections each (gated: 2, W's
+// groups 2 e and 2 e + 1).
+struct Ffn {
+  const lora4_W *W;
+  int epi;       // fwd::EPI_GATED or fwd::EPI_FUSED
+  int P;
+  int64_t E;
+  int64_t M;
+  int r;
+};
+
+// Tokens per group up to which the few-token kernels run.
+constexpr int64_t SMALL_ROWS = 64;
+
+// Forced schedule for tests and measurements (LORA4_FFN_ROWS): 16, 32 or 64
+// the few-token kernel with that many tokens per slot, 1064, 1128 or 1256 the
+// tiles of 64, 128 or 256 rows; anything else or unset: automatic.
+int ffn_policy() {
+  const char *e = std::getenv("LORA4_FFN_ROWS");
+  const int v = e ? std::atoi(e) : 0;
+  return v == 16 || v == 32 || v == 64 || v == 1064 || v == 1128 || v == 1256 ? v : 0;
+}
+
+struct FfnPlan {
+  bool small;
+  int mt, nw;           // small: 16 mt tokens per slot, nw waves
+  int rows;             // tiles: rows per tile
+  int64_t slots, cblocks;
+  SkSched zs;           // tiles: schedule of the rank-r row pass
+  bool z_tail;          // its range partials go to the tiles' tail
+  size_t off_sz, off_part, bytes;
+};
+
+FfnPlan ffn_plan(const Ffn &f) {
+  FfnPlan p{};
+  const int64_t M = std::max<int64_t>(f.M, 1), N = f.W->N;
+  const int64_t extra = f.E > 1 ? f.E : 0;   // slots cut short at the groups' ends
+  const int64_t cus = cu_count();
+  const int pol = ffn_policy();
+  const int64_t mean = ceil_div(M, f.E);
+  p.small = pol ? pol < 1000 : mean <= SMALL_ROWS;
+  if (p.small) {
+    p.mt = pol ? pol / 16 : mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
+    p.slots = ceil_div(M, 16 * p.mt) + extra;
+    p.cblocks = ceil_div(N, 16);
+    p.nw = std::min(p.slots, ceil_div(M, 16 * p.mt) + std::min(extra, M)) * p.cblocks < 2 * cus ? 8 : 4;
+  } else {
+    // the tile whose rounds over the chip cost least: time of a tile relative
+    // to one of 256 rows
+    struct Shape {
+      int rows, cols;
+      double cost;
+    };
+    static const Shape gated[] = {{256, 128, 1.0}, {128, 128, 0.58}, {64, 128, 0.40}};
+    static const Shape fused[] = {{256, 256, 1.0}, {128, 128, 0.34}, {64, 128, 0.24}};
+    double best = 0;
+    for (const Shape &s : f.epi == fwd::EPI_GATED ? gated : fused) {
+      if (pol && pol - 1000 != s.rows) continue;
+      const int64_t slots = ceil_div(M, s.rows) + extra, cb = ceil_div(N, s.cols);
+      // (a group's last tile runs the code of the rows it has)
+      const double cost = s.cost * (double)ceil_div(slots * cb, cus);
+      if (p.rows == 0 || cost < best) {
+        best = cost;
+        p.rows = s.rows;
+        p.slots = slots;
+        p.cblocks = cb;
+      }
+    }
+    p.zs = sk_sched(f.M, f.W->K, f.P * f.r, f.E, 0);
+    p.z_tail = p.zs.ranges > 1 && p.zs.ranges <= big::A2_MAX_PARTS;
+  }
+  p.off_sz = 0;
+  p.off_part = align256((size_t)M * f.P * f.r * 2);
+  p.bytes = p.off_part + (p.small ? 0 : sk_part_bytes_for(f.M, f.W->K, f.P * f.r, f.E, 0));
+  return p;
+}
+
+lora4_status check_ffn(const Ffn &f, int act, float s, const int64_t *offs) {
+  TRY(check_W(f.W));
+  if (f.P == 2 && f.W->groups % 2 != 0) return LORA4_ERR_SHAPE;
+  if (act < LORA4_ACT_NONE || act > LORA4_ACT_GELU_TANH) return LORA4_ERR_FORMAT;
+  if (f.M < 0 || f.M > (int64_t(1) << 31)) return LORA4_ERR_SHAPE;
+  if (f.r < 1 || f.r > 256 / f.P) return LORA4_ERR_SHAPE;
+  if (!std::isfinite(s)) return LORA4_ERR_SHAPE;
+  if (f.E > 1 && !offs) return LORA4_ERR_NULL;
+  if (f.E == 1 && offs) return LORA4_ERR_SHAPE;
+  // 32-bit buffer offsets within a group's base and a row tile
+  Base b{f.W, f.W->groups, false};
+  if (!big_fits(f.W->K, f.M, packed_of(b))) return LORA4_ERR_SHAPE;
+  return LORA4_OK;
+}
+
+struct FfnOut {
+  uint16_t *out, *pre, *Z;
+  const uint16_t *bias, *residual;
+};
+
+lora4_status ffn_forward(const Ffn &f, int act, const uint16_t *X, const uint16_t *A, const uint16_t *B, float s,
+                         const int64_t *offs, const FfnOut &o, void *ws, size_t ws_bytes, hipStream_t st) {
+  TRY(check_ffn(f, act, s, offs));
+  if (!A || !B || (f.M > 0 && (!X || !o.out))) return LORA4_ERR_NULL;
+  if (!all_aligned16({X, A, B, offs, o.out, o.pre, o.Z, o.bias, o.residual, ws})) return LORA4_ERR_ALIGN;
+  const FfnPlan pl = ffn_plan(f);
+  if (!ws || ws_bytes < pl.bytes) return LORA4_ERR_WORKSPACE;
+  if (f.M == 0) return LORA4_OK;
+  const lora4_W *W = f.W;
+  const PackedW pw = packed_of(Base{W, W->groups, false});
+  const int R = f.P * f.r;   // rank columns of a row group
+  uint16_t *sZ = ws_at<uint16_t>(ws, pl.off_sz);
+  if (pl.small) {
+    small::ZParams z{};
+    z.X = X;
+    z.A = A;
+    z.M = f.M;
+    z.K = W->K;
+    z.R = R;
+    z.s = s;
+    z.offsets = offs;
+    z.groups = (int)f.E;
+    z.sZ = sZ;
+    z.Z = o.Z;
+    z.jblocks = (int)ceil_div(R, 16);
+    const int64_t zslots = ceil_div(f.M, 16) + (f.E > 1 ? f.E : 0);
+    TRY(launch_fn("small_z", ffn::small_z_kernel(), zslots * z.jblocks, 64 * small::Z_WAVES, 0, st, z));
+    small::Params p{};
+    p.W = pw;
+    p.X = X;
+    p.M = f.M;
+    p.K = W->K;
+    p.N = W->N;
+    p.offsets = offs;
+    p.groups = (int)f.E;
+    p.r = f.r;
+    p.sZ = sZ;
+    p.B = B;
+    p.act = act;
+    p.out = o.out;
+    p.pre = o.pre;
+    p.bias = o.bias;
+    p.residual = o.residual;
+    p.nblocks = (int)pl.cblocks;
+    p.tab = nf4_table();
+    return launch_fn(f.P == 2 ? "small_gated" : "small_fused", ffn::small_kernel(W->format, f.epi, pl.mt, pl.nw),
+                     pl.slots * pl.cblocks, 64 * pl.nw, small::lds_bytes(f.P, pl.mt, pl.nw), st, p);
+  }
+  float *part = ws_at<float>(ws, pl.off_part);
+  uint16_t *z1 = o.Z ? o.Z : sZ, *z2 = o.Z ? sZ : nullptr;
+  TRY(rows_skinny(0, X, W->K, A, W->K, (int64_t)R * W->K, W->K, f.M, R, offs, f.E, z1, o.Z ? 1.0f : s, z2, s, part,
+                  pl.z_tail, st));
+  big::Params q = big_params(mat(X, W->K), pw, W->K, mat(sZ, R), mat(B, f.r, W->N * f.r), R, f.M, W->N, offs, f.E,
+                             o.out, W->N);
+  if (pl.z_tail) {
+    const TailParts tp{part, pl.zs.ranges, s, o.Z, 1.0f, nullptr, 0.0f};
+    apply_tail_parts(q, &tp);
+  }
+  q.act = act;
+  q.pre = o.pre;
+  q.bias = o.bias;
+  q.residual = o.residual;
+  q.tiles_n = (int)pl.cblocks;
+  q.nslots = (int)pl.slots;
+  if (pl.slots * pl.cblocks > INT32_MAX) return LORA4_ERR_SHAPE;
+  q.nblocks = (int)(pl.slots * pl.cblocks);
+  return launch_fn(f.P == 2 ? "gemm_gated" : "gemm_fused",
+                   ffn::tile_kernel(W->format, f.epi, pl.rows, pl.rows == 256 && f.E > 1), q.nblocks, fwd::THREADS,
+                   (size_t)fwd::lds_bytes(), st, q);
+}
+
+// ---------------------------------------------------------------------------
+// Gated backward
+// ---------------------------------------------------------------------------
+
+// The gate and the up base of a group as one base of 2 Np rows (Np: N rounded
+// up to whole row blocks; the padding rows dequantize to zero).
+PackedW halves_of(const lora4_W *W, int64_t Np) {
+  PackedW p = packed_of(Base{W, W->groups, false});
+  p.N = 2 * Np;
+  p.half = Np;
+  p.half_s2 = p.g_scales2;
+  p.g_codes *= 2;
+  p.g_scales *= 2;
+  p.g_scales2 *= 2;
+  return p;
+}
+
+constexpr int64_t GATED_BWD_BLOCKS = 1024;   // blocks wanted of k_gated_bwd
+constexpr int GATED_BWD_RANGES = 16;
+
+struct GatedBwdPlan {
+  int64_t Np;
+  PackedW pw;
+  lora4_W Wv;        // the joint base as make_plan sees it
+  Plan pl;           // its dgrad plan
+  int ranges, steps;
+  int rt, msplit_a, msplit_b;
+  int64_t tq_a, tq_b, ncnt;
+  size_t off_z, off_skpart, off_dz, off_dgu, off_dzpart, off_pa, off_pb, off_cnt, off_partx, bytes;
+};
+
+GatedBwdPlan gated_bwd_plan(const Ffn &f) {
+  GatedBwdPlan p{};
+  const lora4_W *W = f.W;
+  const int64_t M = std::max<int64_t>(f.M, 1), K = W->K, N = W->N, G = 2 * f.E;
+  p.Np = w_blocks(N) * 64;
+  p.pw = halves_of(W, p.Np);
+  p.Wv = *W;
+  p.Wv.N = 2 * p.Np;
+  p.Wv.groups = f.E;
+  p.pl = make_plan(1, Base{&p.Wv, f.E, false}, f.M, 2 * f.r);
+  const int64_t slots = ceil_div(M, 64) + (f.E > 1 ? f.E : 0), all = p.Np / 64;
+  int64_t want = std::min<int64_t>({ceil_div(GATED_BWD_BLOCKS, slots), GATED_BWD_RANGES, all});
+  p.steps = (int)ceil_div(all, std::max<int64_t>(1, want));
+  p.ranges = (int)ceil_div(all, p.steps);
+  p.rt = skinny_tile(f.r);
+  p.tq_a = ceil_div(K, TN_BQ);
+  p.tq_b = ceil_div(N, TN_BQ);
+  const int64_t rtiles = ceil_div(f.r, p.rt), mavg = std::max<int64_t>(1, M / f.E);
+  auto msplit = [&](int64_t qtiles) {
+    const int64_t tiles = rtiles * qtiles * G;
+    const int64_t w = ceil_div(TARGET_WG * 16 / p.rt, std::max<int64_t>(tiles, 1));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({w, std::max<int64_t>(1, mavg / 256), 65535 / G}));
+  };
+  p.msplit_a = msplit(p.tq_a);
+  p.msplit_b = msplit(p.tq_b);
+  p.ncnt = rtiles * (p.tq_a + p.tq_b) * G;
+  size_t off = 0;
+  auto take = [&](size_t b) {
+    const size_t o = off;
+    off += align256(b);
+    return o;
+  };
+  const size_t mr = (size_t)M * 2 * f.r;
+  p.off_z = take(mr * 2);
+  p.off_skpart = take(sk_part_bytes_for(f.M, K, 2 * f.r, f.E, 0));
+  p.off_dz = take(mr * 2);
+  p.off_dgu = take((size_t)M * 2 * p.Np * 2);
+  p.off_dzpart = take((size_t)p.ranges * mr * 4);
+  p.off_pa = take((size_t)p.msplit_a * G * f.r * K * 4);
+  p.off_pb = take((size_t)p.msplit_b * G * f.r * N * 4);
+  p.off_cnt = take((size_t)p.ncnt * 4);
+  p.off_partx = take(p.pl.lds_splits > 1 ? (size_t)p.pl.lds_splits * M * K * 4 : 0);
+  p.bytes = off;
+  return p;
+}
+
+lora4_status gated_backward(const Ffn &f, int act, const uint16_t *X, const uint16_t *dH, const uint16_t *GU,
+                            const uint16_t *A, const uint16_t *B, float s, const int64_t *offs, const uint16_t *Z,
+                            uint16_t *dX, uint16_t *dA, uint16_t *dB, void *ws, size_t ws_bytes, hipStream_t st) {
+  TRY(check_ffn(f, act, s, offs));
+  if (!A || !B || !dA || !dB || (f.M > 0 && (!X || !dH || !GU || !dX))) return LORA4_ERR_NULL;
+  if (!all_aligned16({X, dH, GU, A, B, offs, Z, dX, dA, dB, ws})) return LORA4_ERR_ALIGN;
+  const GatedBwdPlan p = gated_bwd_plan(f);
+  if (!ws || ws_bytes < p.bytes) return LORA4_ERR_WORKSPACE;
+  const lora4_W *W = f.W;
+  const int64_t K = W->K, N = W->N, G = 2 * f.E;
+  const int r = f.r, R = 2 * r;
+  if (f.M == 0) {
+    TRY(fill_zero(dA, G * r * K, st));
+    return fill_zero(dB, G * N * r, st);
+  }
+  const uint16_t *Zu = Z;
+  if (!Zu) {
+    uint16_t *Zw = ws_at<uint16_t>(ws, p.off_z);
+    TRY(rows_skinny(0, X, K, A, K, (int64_t)R * K, K, f.M, R, offs, f.E, Zw, 1.0f, nullptr, 0.0f,
+                    ws_at<float>(ws, p.off_skpart), false, st));
+    Zu = Zw;
+  }
+  // dG, dU and the partial sums of dZ; its first block clears the arrival
+  // counters of the dA / dB tiles
+  uint16_t *dGU = ws_at<uint16_t>(ws, p.off_dgu), *dZ = ws_at<uint16_t>(ws, p.off_dz);
+  float *zpart = ws_at<float>(ws, p.off_dzpart);
+  unsigned *cnt = ws_at<unsigned>(ws, p.off_cnt);
+  {
+    actbwd::GatedParams q{dH, GU, B, f.M, N, p.Np, r, act, offs, (int)f.E, dGU, p.steps, zpart, cnt, p.ncnt};
+    const int64_t slots = ceil_div(f.M, 64) + (f.E > 1 ? f.E : 0);
+    const void *fn = ffn::gated_bwd_kernel(r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8);
+    void *argv[] = {&q};
+    TRY(launch_timed("gated_bwd", st, [&] {
+      (void)hipLaunchKernel(fn, dim3((unsigned)slots, (unsigned)p.ranges), dim3(actbwd::THREADS), argv, 0, st);
+    }));
+  }
+  // dZ = s (..): by the dgrad's tail where it takes partial sums, else here
+  const bool tail = p.ranges <= big::A2_MAX_PARTS && dgrad_taken(2 * p.Np, 2 * p.Np, f.M, p.pw, K, f.E);
+  const TailParts tp{zpart, p.ranges, s, dZ, s, nullptr, 0.0f};
+  if (!tail)
+    TRY(reduce_bf16("reduce_dz", zpart, p.ranges, f.M * R, f.M * R, dZ, s, nullptr, 0.0f, st));
+  // dX = [dG dU] [deq(Wg); deq(Wu)] + dZ [Ag; Au]
+  {
+    NnParams q{};
+    q.A = mat(dGU, 2 * p.Np);
+    q.W = p.pw;
+    q.R = 2 * p.Np;
+    q.A2 = mat(dZ, R);
+    q.B2 = mat(A, K, (int64_t)R * K);
+    q.r2 = R;
+    q.M = f.M;
+    q.Nc = K;
+    q.offsets = offs;
+    q.groups = (int)f.E;
+    q.Rsplit = 2 * p.Np;
+    q.out = GemmOut{dX, K, nullptr, 0, 1.0f};
+    q.tab = nf4_table();
+    dim3 grid((unsigned)ceil_div(K, BN_MAIN), (unsigned)p.pl.row_slots, 1);
+    TRY(run_nn_main_fmt(W->format, q, grid, p.pl, ws_at<float>(ws, p.off_partx), tail ? &tp : nullptr, st));
+  }
+  // dA = dZ^T X and dB = s [dG dU]^T Z, per projection
+  TnParams pa{};
+  pa.U = mat(dZ, R);
+  pa.V = mat(X, K);
+  pa.P = r;
+  pa.Q = K;
+  pa.M = f.M;
+  pa.offsets = offs;
+  pa.groups = (int)G;
+  pa.splits = p.msplit_a;
+  pa.part = ws_at<float>(ws, p.off_pa);
+  pa.cnt = cnt;
+  pa.out = dA;
+  pa.alpha = 1.0f;
+  pa.transpose_out = 0;
+  pa.half_shift = 1;
+  pa.u_half = r;
+  pa.v_half = 0;
+  TnParams pb = pa;
+  pb.U = mat(Zu, R);
+  pb.V = mat(dGU, 2 * p.Np);
+  pb.Q = N;
+  pb.splits = p.msplit_b;
+  pb.part = ws_at<float>(ws, p.off_pb);
+  pb.cnt = cnt + ceil_div(r, p.rt) * p.tq_a * G;
+  pb.out = dB;
+  pb.alpha = s;
+  pb.transpose_out = 1;
+  pb.v_half = p.Np;
+  return run_tn2("gemm_tn_dA_dB", p.rt, pa, pb, (int)p.tq_a, (int)(p.msplit_a * G), (int)p.tq_b,
+                 (int)(p.msplit_b * G), st);
+}
+
+// ---------------------------------------------------------------------------
+// Backward of the linear with an epilogue
+// ---------------------------------------------------------------------------
+
+struct FusedBwdPlan {
+  int64_t xblocks;
+  int splits;          // row ranges of k_act_bwd per group
+  size_t off_dp, off_part, off_lin, lin_bytes, bytes;
+};
+
+FusedBwdPlan fused_bwd_plan(const Ffn &f, bool act, bool dbias) {
+  FusedBwdPlan p{};
+  const int64_t M = std::max<int64_t>(f.M, 1), N = f.W->N;
+  p.xblocks = ceil_div(N, actbwd::ACT_COLS);
+  // about 1024 blocks, of at least 16 rows each
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(1024, p.xblocks * f.E), ceil_div(M, 16 * f.E)));
+  p.off_dp = 0;
+  size_t off = act ? align256((size_t)M * N * 2) : 0;
+  p.off_part = off;
+  if (dbias) off += align256((size_t)f.E * p.splits * 4 * N * 4);
+  p.off_lin = off;
+  p.lin_bytes = make_plan(1, Base{f.W, f.E, false}, f.M, f.r).bytes;
+  p.bytes = off + p.lin_bytes;
+  return p;
+}
+
+}  // namespace

@@ -166,6 +166,11 @@ struct PackedW {
   int64_t g_scales;       // scale entries per group
   int64_t g_scales2;      // second-level entries per group
   int32_t shared;         // 1: one W for every row group (adapters over one base)
+  // Two projections of one group seen as one base of 2 `half` rows (half % 64
+  // == 0, each padded to whole row blocks): rows from `half` on are the second
+  // projection's, whose NF4-DQ second-level scales start half_s2 entries
+  // further and count from its own first row. 0: one base.
+  int64_t half, half_s2;
 };
 
 // group of W that row group g reads
@@ -183,8 +188,9 @@ __device__ __forceinline__ float block_scale(const PackedW &w, int g, int64_t n,
   } else if constexpr (FMT == FMT_NF4_DQ) {
     const uint8_t *s = reinterpret_cast<const uint8_t *>(w.scales) + g * w.g_scales;
     // the second-level groups run over the scales in row-major order
-    const int64_t idx = n * (w.K >> 6) + (k >> 6);
-    float c2 = w.scales2[g * w.g_scales2 + (idx >> 8)];
+    const bool second = w.half && n >= w.half;
+    const int64_t idx = (n - (second ? w.half : 0)) * (w.K >> 6) + (k >> 6);
+    float c2 = w.scales2[g * w.g_scales2 + (second ? w.half_s2 : 0) + (idx >> 8)];
     return e4m3_to_f32(s[w_scale64_idx(w.KB, n, k)]) * c2;
   } else if constexpr (FMT == FMT_NVFP4) {
     const uint8_t *s = reinterpret_cast<const uint8_t *>(w.scales) + g * w.g_scales;

@@ -35,14 +35,6 @@ constexpr int CPAD = 16;        // bf16 padding per LDS row of column-contiguous
 // Operand descriptions
 // --------------------------------------------------------------------------
 
-// bf16 matrix, row-major with leading dimension ld (elements); per-group
-// element offset gstride (0 when the operand is shared by all groups).
-struct Mat {
-  const uint16_t *p;
-  int64_t ld;
-  int64_t gstride;
-};
-
 struct GemmOut {
   uint16_t *C;        // bf16 output (or nullptr)
   int64_t ldc;
@@ -99,6 +91,11 @@ struct TnParams {
   uint16_t *out;
   float alpha;
   int transpose_out;
+  // 1: two products per row group (gate and up): product g covers the rows of
+  // group g / 2, and the odd ones take U and V u_half and v_half elements
+  // further on. 0: one product per row group.
+  int half_shift;
+  int64_t u_half, v_half;
 };
 
 // --------------------------------------------------------------------------
@@ -639,9 +636,10 @@ __device__ __forceinline__ void tn_tile(const TnParams &p, int bx, int by, int b
 
   int64_t ga = 0, gb = p.M;
   if (p.offsets) {
-    ga = p.offsets[g];
-    gb = p.offsets[g + 1];
+    ga = p.offsets[g >> p.half_shift];
+    gb = p.offsets[(g >> p.half_shift) + 1];
   }
+  const int64_t odd = g & p.half_shift;   // 1: a row group's second product
   const int64_t rows = gb - ga;
   const int64_t per = ((rows + p.splits - 1) / p.splits + BK - 1) / BK * BK;
   const int64_t m0 = ga + (int64_t)split * per;
@@ -657,15 +655,16 @@ __device__ __forceinline__ void tn_tile(const TnParams &p, int bx, int by, int b
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  const bool u_vec = (p.U.ld % 8) == 0;
-  const bool v_vec = (p.V.ld % 8) == 0;
+  const bool u_vec = (p.U.ld % 8) == 0 && (p.u_half % 8) == 0;
+  const bool v_vec = (p.V.ld % 8) == 0 && (p.v_half % 8) == 0;
+  const uint16_t *U = p.U.p + odd * p.u_half, *V = p.V.p + odd * p.v_half;
   ColSlabRegs<BP> ru;
   ColSlabRegs<BQ> rv;
 
   auto issue = [&](int s) {
     const int64_t r0 = m0 + (int64_t)s * BK;
-    load_colslab<BP>(ru, p.U.p, p.U.ld, r0, m1, p0, p.P, u_vec);
-    load_colslab<BQ>(rv, p.V.p, p.V.ld, r0, m1, q0, p.Q, v_vec);
+    load_colslab<BP>(ru, U, p.U.ld, r0, m1, p0, p.P, u_vec);
+    load_colslab<BQ>(rv, V, p.V.ld, r0, m1, q0, p.Q, v_vec);
   };
 
   if (steps > 0) issue(0);

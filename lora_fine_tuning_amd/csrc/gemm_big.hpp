@@ -70,6 +70,13 @@ struct Params {
   const uint8_t *X8;
   const uint8_t *X8s;
   int64_t ld8;
+  // forward with an epilogue (fwd::EPI_GATED, EPI_FUSED): the activation, the
+  // pre-activation output (or nullptr), bias [groups][Nc] and residual
+  // [M, Nc] (either may be null)
+  int act;
+  uint16_t *pre;
+  const uint16_t *bias;
+  const uint16_t *residual;
 };
 
 // Row tile of block slot: per group (experts), or over all M rows when the

@@ -76,8 +76,10 @@ struct WRaw {
   uint32_t c2;   // DQ second level (fp32 bits)
 };
 
-// SHARED: the row tiles ignore the groups (Params::shared_rows).
-template <int FMT, bool SHARED>
+// SHARED: the row tiles ignore the groups (Params::shared_rows). HALVES: the
+// reduction runs over two projections (PackedW::half), which only NF4-DQ's
+// second-level scales have to know.
+template <int FMT, bool SHARED, bool HALVES = false>
 __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
   const uint32_t sel = big::sel_base();
@@ -148,6 +150,21 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
                              ? big::make_rsrc(p.W.scales2 + gw * p.W.g_scales2, big::clamp_bytes(p.W.g_scales2 * 4))
                              : big::make_rsrc(p.W.codes, 0u);
 
+  // NF4-DQ: offset of the second-level scale of this thread's run of step s
+  auto s2_voff = [&](int s) -> uint32_t {
+    int64_t n = (int64_t)s * BKS;
+    int64_t skip = 0;
+    if constexpr (HALVES) {
+      // (a step's 64 rows lie in one half)
+      if (n >= p.W.half) {
+        n -= p.W.half;
+        skip = p.W.half_s2;
+      }
+    }
+    const int64_t idx = (n + lane) * sc_per_row + (kc >> 6);
+    return (uint32_t)(((idx >> 8) + skip) * 4);
+  };
+
   auto load_w = [&](int s, WRaw &w) {
     const int wo = (int)(w_step * s);
     w.c0 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(w_rsrc, w_voff0, wo, 0));
@@ -157,8 +174,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
       w.sc = __builtin_amdgcn_raw_buffer_load_b32(s_rsrc, s_voff, so, 0);
     } else if constexpr (FMT == FMT_NF4_DQ) {
       w.sc = __builtin_amdgcn_raw_buffer_load_b8(s_rsrc, s_voff, so, 0);
-      const int64_t idx = ((int64_t)s * BKS + lane) * sc_per_row + (kc >> 6);
-      w.c2 = __builtin_amdgcn_raw_buffer_load_b32(s2_rsrc, kc < p.Nc ? (uint32_t)((idx >> 8) * 4) : OOB, 0, 0);
+      w.c2 = __builtin_amdgcn_raw_buffer_load_b32(s2_rsrc, kc < p.Nc ? s2_voff(s) : OOB, 0, 0);
     } else if constexpr (FMT == FMT_NVFP4) {
       // two E4M3 codes per half of the run, loaded per half as for MXFP4
       const uint32_t e0 = __builtin_amdgcn_raw_buffer_load_b16(s_rsrc, s_voff, so, 0);
@@ -288,8 +304,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
       w.sc = __builtin_amdgcn_raw_buffer_load_b32(s_rsrc, s_voff, so, 0);
     } else if constexpr (FMT == FMT_NF4_DQ) {
       w.sc = __builtin_amdgcn_raw_buffer_load_b8(s_rsrc, s_voff, so, 0);
-      const int64_t idx = ((int64_t)s * BKS + lane) * sc_per_row + (kc >> 6);
-      w.c2 = __builtin_amdgcn_raw_buffer_load_b32(s2_rsrc, kc < p.Nc ? (uint32_t)((idx >> 8) * 4) : OOB, 0, 0);
+      w.c2 = __builtin_amdgcn_raw_buffer_load_b32(s2_rsrc, kc < p.Nc ? s2_voff(s) : OOB, 0, 0);
     } else if constexpr (FMT == FMT_NVFP4) {
       const uint32_t e0 = __builtin_amdgcn_raw_buffer_load_b16(s_rsrc, s_voff, so, 0);
       const uint32_t e1 = __builtin_amdgcn_raw_buffer_load_b16(s_rsrc, s_voff1, so, 0);

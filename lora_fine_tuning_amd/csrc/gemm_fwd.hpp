@@ -36,6 +36,9 @@
 // c = E4M3(code) * c2 first.
 #pragma once
 
+#include <type_traits>
+
+#include "act.hpp"
 #include "gemm_big.hpp"
 
 namespace lora4 {
@@ -70,6 +73,18 @@ struct WRaw {
   uint32_t c2[2];   // DQ second level (fp32 bits)
 };
 
+// What a tile does with its fp32 sums P = X deq(W)^T + (s Z) B^T:
+//  EPI_NONE  : Y = bf16(P)
+//  EPI_GATED : the tile's two 32-column blocks per wave are the same 32 columns
+//              of two projections, gate and up (groups 2 g and 2 g + 1 of W and
+//              B; the rank-r operand holds the gate's r2 / 2 columns, then the
+//              up's): H = bf16(act(G) U), and bf16 G, U to Params::pre [M][2 Nc]
+//              where it is given. Both factors of an element sit in the same
+//              lane's registers, so the product costs no exchange.
+//  EPI_FUSED : Y = bf16(act(P + bias) + residual), and bf16(P + bias) to
+//              Params::pre [M][Nc] where it is given.
+enum Epi : int { EPI_NONE = 0, EPI_GATED = 1, EPI_FUSED = 2 };
+
 // One output tile of TBM rows x 128 NJ columns: wave w owns the 32 NJ columns
 // from col0 + 32 NJ w (NJ 32-column blocks) for all TBM rows (TBM / 32 row
 // blocks). SPLIT (TBM 256, NJ 2 only): the block computes reduction range
@@ -77,12 +92,15 @@ struct WRaw {
 // the groups (Params::shared_rows). `tile` is the tile's index in the split
 // partials. rt: the tile's rows (from the slot's 256-row tile; a short last
 // tile of a group runs with TBM 64 or 128 over the same rows).
-template <int FMT, bool SPLIT, bool SHARED, int TBM, int NJ>
+template <int FMT, bool SPLIT, bool SHARED, int TBM, int NJ, int EPI = EPI_NONE>
 __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const RowTile &rt, int64_t col0, int tile,
                                          int split) {
   static_assert(!SPLIT || (TBM == BM && NJ == 2), "split partials are laid out for 256 x 256 tiles");
   constexpr int RB = TBM / 32;       // 32-row blocks: MFMA row blocks per wave, X chunks per step
-  constexpr int WN = 32 * NJ;        // columns per wave
+  static_assert(EPI == EPI_NONE || (!SPLIT && !SHARED), "the epilogues run on whole tiles of their own base");
+  static_assert(EPI != EPI_GATED || NJ == 2, "a gated tile has a gate and an up block per wave");
+  constexpr int WJ = EPI == EPI_GATED ? 0 : 32;     // output columns between a wave's blocks
+  constexpr int WN = EPI == EPI_GATED ? 32 : 32 * NJ;   // output columns per wave
   constexpr int CPS = 8 / RB;        // hand-dealt slices per MFMA row block (8 slices per sub-step)
   constexpr bool is_split = SPLIT;
   if (rt.group < 0) return;
@@ -131,26 +149,39 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
   const int64_t rb = wcol0 >> 6;
   const int i0 = (int)(wcol0 & 63);
   const bool rb_ok = rb < w_blocks(p.W.N);
-  const int gw = w_group(p.W, g);   // group of W
+  const int gw = EPI == EPI_GATED ? 2 * g : w_group(p.W, g);   // group of W (gated: of the gate)
   const uint8_t *codes_g = p.W.codes + gw * p.W.g_codes;
-  const rsrc_t w_rsrc = big::make_rsrc(rb_ok ? codes_g + rb * KB * 2048 : codes_g,
-                                       rb_ok ? big::clamp_bytes(KB * 2048) : 0u);
+  const rsrc_t w_rsrc0 = big::make_rsrc(rb_ok ? codes_g + rb * KB * 2048 : codes_g,
+                                        rb_ok ? big::clamp_bytes(KB * 2048) : 0u);
+  // gated: block 1's base is the next group's
+  const rsrc_t w_rsrc1 =
+      EPI == EPI_GATED ? big::make_rsrc(codes_g + p.W.g_codes + (rb_ok ? rb * KB * 2048 : 0),
+                                        rb_ok ? big::clamp_bytes(KB * 2048) : 0u)
+                       : w_rsrc0;
   constexpr int sc_bytes = FMT == FMT_NF4 ? 4 : 1;
   constexpr int sc_tile = FMT == FMT_MXFP4 ? 128 : FMT == FMT_NVFP4 ? 256 : 64 * sc_bytes;   // scale bytes per tile
   const uint8_t *sbase = reinterpret_cast<const uint8_t *>(p.W.scales) + (gw * p.W.g_scales) * sc_bytes;
-  const rsrc_t s_rsrc = big::make_rsrc(rb_ok ? sbase + rb * KB * sc_tile : sbase,
-                                       rb_ok ? big::clamp_bytes(KB * sc_tile) : 0u);
-  const rsrc_t s2_rsrc = FMT == FMT_NF4_DQ
-                             ? big::make_rsrc(p.W.scales2 + gw * p.W.g_scales2, big::clamp_bytes(p.W.g_scales2 * 4))
-                             : big::make_rsrc(p.W.codes, 0u);
+  const rsrc_t s_rsrc0 = big::make_rsrc(rb_ok ? sbase + rb * KB * sc_tile : sbase,
+                                        rb_ok ? big::clamp_bytes(KB * sc_tile) : 0u);
+  const rsrc_t s_rsrc1 =
+      EPI == EPI_GATED ? big::make_rsrc(sbase + p.W.g_scales * sc_bytes + (rb_ok ? rb * KB * sc_tile : 0),
+                                        rb_ok ? big::clamp_bytes(KB * sc_tile) : 0u)
+                       : s_rsrc0;
+  const rsrc_t s2_rsrc0 = FMT == FMT_NF4_DQ
+                              ? big::make_rsrc(p.W.scales2 + gw * p.W.g_scales2, big::clamp_bytes(p.W.g_scales2 * 4))
+                              : big::make_rsrc(p.W.codes, 0u);
+  const rsrc_t s2_rsrc1 =
+      EPI == EPI_GATED && FMT == FMT_NF4_DQ
+          ? big::make_rsrc(p.W.scales2 + (gw + 1) * p.W.g_scales2, big::clamp_bytes(p.W.g_scales2 * 4))
+          : s2_rsrc0;
   uint32_t w_voff[2], s_voff[2];
   int64_t s_idx0[2];   // DQ: row-major index of the row's first 64-run scale
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int i = i0 + j * 32 + l32;   // row inside the row block
+    const int i = i0 + j * WJ + l32;   // row inside the row block
     w_voff[j] = (uint32_t)(i * 32 + h * 16);
     s_voff[j] = (uint32_t)(FMT == FMT_MXFP4 ? i * 2 + h : FMT == FMT_NVFP4 ? i * 4 + h * 2 : i * sc_bytes);
-    s_idx0[j] = (wcol0 + j * 32 + l32) * (p.W.K >> 6);
+    s_idx0[j] = (wcol0 + j * WJ + l32) * (p.W.K >> 6);
   }
   // per-step offsets of tile (rb, k0 / 64)
   auto w_step_off = [](int k0) { return (int)((k0 >> 6) << 11); };
@@ -166,17 +197,17 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
     const bool half_ok = k0 + 32 * h < Ri;
     const int j = part;
     w.c[j] = __builtin_bit_cast(
-        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(w_rsrc, half_ok ? w_voff[j] : OOB, w_step_off(k0), 0));
+        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(j ? w_rsrc1 : w_rsrc0, half_ok ? w_voff[j] : OOB, w_step_off(k0), 0));
     if constexpr (FMT == FMT_NF4) {
-      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b32(s_rsrc, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
+      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b32(j ? s_rsrc1 : s_rsrc0, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
     } else if constexpr (FMT == FMT_NF4_DQ) {
-      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b8(s_rsrc, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
+      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b8(j ? s_rsrc1 : s_rsrc0, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
       const int64_t gi = (s_idx0[j] + (int64_t)(k0 >> 6)) >> 8;
-      w.c2[j] = __builtin_amdgcn_raw_buffer_load_b32(s2_rsrc, half_ok ? (uint32_t)(gi * 4) : OOB, 0, 0);
+      w.c2[j] = __builtin_amdgcn_raw_buffer_load_b32(j ? s2_rsrc1 : s2_rsrc0, half_ok ? (uint32_t)(gi * 4) : OOB, 0, 0);
     } else if constexpr (FMT == FMT_NVFP4) {   // the lane half's two E4M3 scales
-      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(s_rsrc, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
+      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(j ? s_rsrc1 : s_rsrc0, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
     } else {
-      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b8(s_rsrc, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
+      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b8(j ? s_rsrc1 : s_rsrc0, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
     }
   };
   // loads issued by load_w over a whole step, all in parts 0 .. NJ - 1
@@ -289,22 +320,22 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
     const int k0 = (s + sb) * BKS;
     const bool half_ok = k0 + 32 * h < Ri;
     if constexpr (FMT == FMT_NF4) {
-      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b32(s_rsrc, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
+      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b32(j ? s_rsrc1 : s_rsrc0, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
     } else if constexpr (FMT == FMT_NF4_DQ) {
-      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b8(s_rsrc, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
+      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b8(j ? s_rsrc1 : s_rsrc0, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
       const int64_t gi = (s_idx0[j] + (int64_t)(k0 >> 6)) >> 8;
-      w.c2[j] = __builtin_amdgcn_raw_buffer_load_b32(s2_rsrc, half_ok ? (uint32_t)(gi * 4) : OOB, 0, 0);
+      w.c2[j] = __builtin_amdgcn_raw_buffer_load_b32(j ? s2_rsrc1 : s2_rsrc0, half_ok ? (uint32_t)(gi * 4) : OOB, 0, 0);
     } else if constexpr (FMT == FMT_NVFP4) {   // the lane half's two E4M3 scales
-      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(s_rsrc, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
+      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b16(j ? s_rsrc1 : s_rsrc0, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
     } else {
-      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b8(s_rsrc, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
+      w.sc[j] = __builtin_amdgcn_raw_buffer_load_b8(j ? s_rsrc1 : s_rsrc0, half_ok ? s_voff[j] : OOB, s_step_off(k0), 0);
     }
   };
   auto load_w_codes = [&](int s, WRaw &w, int j) {
     const int k0 = (s + sb) * BKS;
     const bool half_ok = k0 + 32 * h < Ri;
     w.c[j] = __builtin_bit_cast(
-        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(w_rsrc, half_ok ? w_voff[j] : OOB, w_step_off(k0), 0));
+        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(j ? w_rsrc1 : w_rsrc0, half_ok ? w_voff[j] : OOB, w_step_off(k0), 0));
   };
   // slice i of decoding words q0, q0 + 1 of row j of w into f
   auto dec_slice = [&](int i, const WRaw &w, WFrag &f, const RunDec &d, int j, int q0, WordDec (&wd)[2]) {
@@ -483,7 +514,7 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
       WFrag bt;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const int64_t n = wcol0 + j * 32 + l32;
+        const int64_t n = wcol0 + j * WJ + l32;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const int kc = k0 + 32 * h + 8 * kk;
@@ -491,7 +522,24 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
           if constexpr (SHARED) gi = kc / tg.rp;
           const int64_t k = kc - gi * tg.rp;
           uint32_t w4[4] = {0u, 0u, 0u, 0u};
-          if (kk < nkk && n < p.Nc && kc < rc && k < p.r2) {
+          if constexpr (EPI == EPI_GATED) {
+            // block j's B rows fill the columns of its own half of the rank
+            // operand, zero elsewhere (a block-diagonal operand)
+            const int rj = p.r2 >> 1, kb = (int)k - j * rj;   // column within the half
+            if (kk < nkk && n < p.Nc && kb > -8 && kb < rj) {
+              const uint16_t *src = p.B2.p + (2 * g + j) * p.B2.gstride + n * p.B2.ld;
+              if (b_vec && (rj & 7) == 0) {   // (then 0 <= kb <= rj - 8)
+                const u32x4_t v = *reinterpret_cast<const u32x4_t *>(src + kb);
+                w4[0] = v[0];
+                w4[1] = v[1];
+                w4[2] = v[2];
+                w4[3] = v[3];
+              } else {
+                for (int e = 0; e < 8; ++e)
+                  if (kb + e >= 0 && kb + e < rj) w4[e >> 1] |= (uint32_t)src[kb + e] << (16 * (e & 1));
+              }
+            }
+          } else if (kk < nkk && n < p.Nc && kc < rc && k < p.r2) {
             const uint16_t *src = p.B2.p + (tg.g0 + gi) * p.B2.gstride + n * p.B2.ld + k;
             if (b_vec && k + 8 <= p.r2) {
               const u32x4_t v = *reinterpret_cast<const u32x4_t *>(src);
@@ -597,7 +645,7 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
   // segments of 16 NJ lanes per store instruction (element stores where a
   // row segment is cut by the output's edge or the rows are not 16-byte
   // aligned).
-  {
+  if constexpr (EPI == EPI_NONE) {
     constexpr int CH = 4 * NJ;           // 16-byte chunks per staged row
     constexpr int RPI = 64 / CH;         // rows per store instruction
     uint16_t *stg = smem + wave * (TBM * 64);
@@ -627,6 +675,110 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
         }
       }
     }
+  } else {
+    // The other epilogues stage fp32 sums, up to 128 rows at a time (32 KB per
+    // wave), and work on them in the order they are written out: 8 columns of
+    // a row per lane, so that bias, residual and every output move 16 bytes
+    // per lane, and the activation's code is not unrolled over the
+    // accumulators. 16-byte chunk c (4 columns; gated: 0 .. 7 the gate, 8 ..
+    // 15 the up projection) of row r at position c ^ (r % CF), free of bank
+    // conflicts when written (16 lanes: 16 rows, one chunk).
+    constexpr int CF = 8 * NJ;                        // chunks per staged row
+    constexpr int PB = RB < 4 ? RB : 4;               // row blocks per phase
+    constexpr int LPR = EPI == EPI_GATED ? 4 : 4 * NJ;   // lanes per row when written out
+    float *stf = reinterpret_cast<float *>(smem) + wave * (PB * 32 * CF * 4);
+    auto off = [](int row, int c) { return row * (CF * 4) + ((c ^ (row & (CF - 1))) << 2); };
+    const int c8 = lane % LPR;
+    const int64_t gcol = wcol0 + 8 * c8;
+    const int cols = (int)(p.Nc - gcol < 8 ? (p.Nc - gcol > 0 ? p.Nc - gcol : 0) : 8);   // of this lane
+    float bias[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      bias[e] = EPI == EPI_FUSED && p.bias && e < cols ? bf16_bits_to_f32(p.bias[g * p.Nc + gcol + e]) : 0.0f;
+    auto put = [&](uint16_t *dst0, int64_t ld, int64_t grow, const float (&v)[8]) {
+      uint16_t *dst = dst0 + grow * ld + gcol;
+      const u32x4_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7])};
+      if (cols == 8) {
+        *reinterpret_cast<u32x4_a2_t *>(dst) = w;
+      } else {
+        for (int e = 0; e < cols; ++e) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      }
+    };
+    auto take = [&](int row, int c, float (&v)[8]) {
+      const f32x4_t lo = *reinterpret_cast<const f32x4_t *>(stf + off(row, c));
+      const f32x4_t hi = *reinterpret_cast<const f32x4_t *>(stf + off(row, c + 1));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = lo[e];
+        v[4 + e] = hi[e];
+      }
+    };
+#pragma unroll
+    for (int ph = 0; ph < RB / PB; ++ph) {
+#pragma unroll
+      for (int ib = 0; ib < PB; ++ib)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int r4 = 0; r4 < 4; ++r4) {
+            const int i = ph * PB + ib;
+            *reinterpret_cast<f32x4_t *>(stf + off(ib * 32 + l32, 8 * j + 2 * r4 + h)) =
+                f32x4_t{acc[i][j][4 * r4], acc[i][j][4 * r4 + 1], acc[i][j][4 * r4 + 2], acc[i][j][4 * r4 + 3]};
+          }
+      // (the residual pieces of U rows per lane are loaded before the first is
+      // needed: one load's latency per U rows)
+      constexpr int U = EPI == EPI_FUSED ? 4 : 1;
+      constexpr int ITS = PB * 32 * LPR / 64;
+      static_assert(ITS % U == 0, "whole groups");
+#pragma unroll 1
+      for (int it0 = 0; it0 < ITS; it0 += U) {
+        u32x4_t rv[U];
+        if constexpr (EPI == EPI_FUSED) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int64_t grow = row0 + ph * PB * 32 + (it0 + u) * (64 / LPR) + lane / LPR;
+            rv[u] = u32x4_t{0u, 0u, 0u, 0u};
+            if (p.residual && grow < row_end && cols > 0) {
+              const uint16_t *src = p.residual + grow * p.ldc + gcol;
+              if (cols == 8) {
+                rv[u] = *reinterpret_cast<const u32x4_a2_t *>(src);
+              } else {
+                for (int e = 0; e < cols; ++e) rv[u][e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int row = (it0 + u) * (64 / LPR) + lane / LPR;
+          const int64_t grow = row0 + ph * PB * 32 + row;
+          float v[8];
+          take(row, 2 * c8, v);
+          if (grow >= row_end || cols == 0) continue;
+          if constexpr (EPI == EPI_GATED) {
+            float w[8];
+            take(row, 8 + 2 * c8, w);
+            if (p.pre) {
+              put(p.pre, 2 * p.Nc, grow, v);
+              put(p.pre + p.Nc, 2 * p.Nc, grow, w);
+            }
+            act_value8(v, p.act);
+            // (of the unrounded sums: H is rounded once)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= w[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += bias[e];
+            if (p.pre) put(p.pre, p.ldc, grow, v);
+            act_value8(v, p.act);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += bf16_bits_to_f32((rv[u][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+          }
+          put(p.C, p.ldc, grow, v);
+        }
+      }
+    }
   }
 }
 
@@ -643,6 +795,25 @@ __device__ __forceinline__ void fwd_whole_tile(const Params &p, uint16_t *smem, 
   if (SHORT && rows <= 64) fwd_tile<FMT, false, SHARED, 64, 2>(p, smem, rt, col0, tile, 0);
   else if (SHORT && rows <= 128) fwd_tile<FMT, false, SHARED, 128, 2>(p, smem, rt, col0, tile, 0);
   else fwd_tile<FMT, false, SHARED, BM, 2>(p, smem, rt, col0, tile, 0);
+}
+
+// A tile with one of the epilogues, TBM rows x 256 (NJ 2; gated: 128) or 128
+// (NJ 1) columns, in grouped tile order over p.nslots row slots of TBM rows.
+// SHORT (TBM 256): short last row tiles of a group run the shorter code.
+template <int FMT, int EPI, int TBM, int NJ, bool SHORT>
+__global__ __launch_bounds__(THREADS, 1) void k_gemm_fwd_epi(Params p) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  int b = blockIdx.x;
+  const int per = p.nblocks >> 3;
+  if (b < per * 8) b = (b & 7) * per + (b >> 3);
+  int slot, tn;
+  big::grouped_tile(b, p.tiles_n, p.nslots, slot, tn);
+  const RowTile rt = big::tile_rows<false>(p, slot, TBM);
+  const int64_t col0 = (int64_t)tn * (EPI == EPI_GATED ? 128 : 128 * NJ);
+  const int64_t rows = rt.row_end - rt.row0;
+  if (SHORT && rows <= 64) fwd_tile<FMT, false, false, 64, NJ, EPI>(p, smem, rt, col0, b, 0);
+  else if (SHORT && rows <= 128) fwd_tile<FMT, false, false, 128, NJ, EPI>(p, smem, rt, col0, b, 0);
+  else fwd_tile<FMT, false, false, TBM, NJ, EPI>(p, smem, rt, col0, b, 0);
 }
 
 // Full 256 x 256 tiles (blocks below p.nfull, in grouped tile order, each XCD
@@ -694,7 +865,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_fwd_small(Params p) {
 
 // C[tile rows][tile columns] = bf16(sum_k part[t][k][r][c]) for the split
 // tiles t; four columns per thread, splits summed in order.
-__global__ void k_reduce_tiles(Params p, int split_tiles) {
+static __global__ void k_reduce_tiles(Params p, int split_tiles) {
   const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t per_tile = (int64_t)BM * (BN / 4);
   if (idx >= (int64_t)split_tiles * per_tile) return;

@@ -22,6 +22,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -32,6 +33,7 @@
 #include "gemm_big.hpp"
 #include "gemm_fwd.hpp"
 #include "gemm_dgrad.hpp"
+#include "ffn.hpp"
 #include "mx.hpp"
 #include "loftq.hpp"
 #include "skinny.hpp"
@@ -586,6 +588,11 @@ lora4_status run_dgrad(const big::Params &p, hipStream_t st) {
   if (p.shared_rows)
     return launch_lds("gemm_nn_dgrad", dgrad::k_gemm_dgrad<FMT, true>, dim3((unsigned)p.nblocks),
                       dim3(dgrad::THREADS), (size_t)dgrad::lds_bytes(), p, st);
+  if constexpr (FMT == FMT_NF4_DQ) {
+    if (p.W.half)   // gate and up as one base
+      return launch_lds("gemm_nn_dgrad", dgrad::k_gemm_dgrad<FMT, false, true>, dim3((unsigned)p.nblocks),
+                        dim3(dgrad::THREADS), (size_t)dgrad::lds_bytes(), p, st);
+  }
   return launch_lds("gemm_nn_dgrad", dgrad::k_gemm_dgrad<FMT, false>, dim3((unsigned)p.nblocks),
                     dim3(dgrad::THREADS), (size_t)dgrad::lds_bytes(), p, st);
 }
@@ -1235,12 +1242,19 @@ dim3 pack_grid(int64_t N, int64_t K) {
 
 }  // namespace
 
+#include "ffn_host.hpp"
+
 // ===========================================================================
 // Exported C ABI
 // ===========================================================================
 
 #pragma GCC visibility push(default)
 extern "C" {
+
+static lora4_status backward_impl(const Base &bs, const uint16_t *X, const uint16_t *dY, int64_t M,
+                                  const uint16_t *A, const uint16_t *B, int32_t r, float s,
+                                  const int64_t *group_offsets, const uint16_t *Z, uint16_t *dX, uint16_t *dA,
+                                  uint16_t *dB, void *workspace, size_t workspace_bytes, void *stream);
 
 const char *lora4_version(void) { return "lora4 0.1 (gfx950)"; }
 
@@ -1784,5 +1798,124 @@ int lora4_timing_collect(lora4_kernel_time *out, int max) {
   return n;
 }
 
+// ---- the feed-forward operators (ffn_host.hpp) ------------------------------
+
+size_t lora4_rmsnorm_workspace_bytes(int64_t M, int64_t D) {
+  if (check_norm(M, D, 0.0f) != LORA4_OK) return 0;
+  return norm_ws_bytes(M, D);
+}
+
+lora4_status lora4_rmsnorm_forward(const uint16_t *X, const uint16_t *R, const uint16_t *weight, int64_t M, int64_t D,
+                                   float eps, uint16_t *H, uint16_t *Y, uint8_t *codes, uint8_t *scales_e8m0,
+                                   void *stream) {
+  return norm_forward(X, R, weight, M, D, eps, H, Y, codes, scales_e8m0, reinterpret_cast<hipStream_t>(stream));
+}
+
+lora4_status lora4_rmsnorm_backward(const uint16_t *dY, const uint16_t *H, const uint16_t *weight, const uint16_t *dH,
+                                    int64_t M, int64_t D, float eps, uint16_t *dX, uint16_t *dW, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+  return norm_backward(dY, H, weight, dH, M, D, eps, dX, dW, workspace, workspace_bytes,
+                       reinterpret_cast<hipStream_t>(stream));
+}
+
+static Ffn gated_of(const lora4_W *W, int64_t M, int32_t r) {
+  return Ffn{W, fwd::EPI_GATED, 2, std::max<int64_t>(1, W->groups / 2), M, r};
+}
+static Ffn fused_of(const lora4_W *W, int64_t M, int32_t r) {
+  return Ffn{W, fwd::EPI_FUSED, 1, W->groups, M, r};
+}
+
+size_t lora4_gated_workspace_bytes(int which, const lora4_W *W, int64_t M, int32_t r) {
+  if (!W || (which != 0 && which != 1)) return 0;
+  const Ffn f = gated_of(W, M, r);
+  const int64_t some = 0;   // (stands for the offsets, which the sizes do not depend on)
+  if (check_ffn(f, LORA4_ACT_NONE, 1.0f, f.E > 1 ? &some : nullptr) != LORA4_OK) return 0;
+  return which == 0 ? ffn_plan(f).bytes : gated_bwd_plan(f).bytes;
+}
+
+lora4_status lora4_gated_forward(const lora4_W *W, int32_t activation, const uint16_t *X, int64_t M,
+                                 const uint16_t *A, const uint16_t *B, int32_t r, float s,
+                                 const int64_t *group_offsets, uint16_t *H, uint16_t *GU, uint16_t *Z,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+  if (!W) return LORA4_ERR_NULL;
+  return ffn_forward(gated_of(W, M, r), activation, X, A, B, s, group_offsets, FfnOut{H, GU, Z, nullptr, nullptr},
+                     workspace, workspace_bytes, reinterpret_cast<hipStream_t>(stream));
+}
+
+lora4_status lora4_gated_backward(const lora4_W *W, int32_t activation, const uint16_t *X, const uint16_t *dH,
+                                  const uint16_t *GU, int64_t M, const uint16_t *A, const uint16_t *B, int32_t r,
+                                  float s, const int64_t *group_offsets, const uint16_t *Z, uint16_t *dX,
+                                  uint16_t *dA, uint16_t *dB, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+  if (!W) return LORA4_ERR_NULL;
+  return gated_backward(gated_of(W, M, r), activation, X, dH, GU, A, B, s, group_offsets, Z, dX, dA, dB, workspace,
+                        workspace_bytes, reinterpret_cast<hipStream_t>(stream));
+}
+
+size_t lora4_epilogue_workspace_bytes(int which, const lora4_W *W, int64_t M, int32_t r) {
+  if (!W || (which != 0 && which != 1)) return 0;
+  const Ffn f = fused_of(W, M, r);
+  const int64_t some = 0;
+  if (check_ffn(f, LORA4_ACT_NONE, 1.0f, f.E > 1 ? &some : nullptr) != LORA4_OK) return 0;
+  return which == 0 ? ffn_plan(f).bytes : fused_bwd_plan(f, true, true).bytes;
+}
+
+lora4_status lora4_forward_epilogue(const lora4_W *W, int32_t activation, const uint16_t *X, int64_t M,
+                                    const uint16_t *A, const uint16_t *B, int32_t r, float s,
+                                    const int64_t *group_offsets, const uint16_t *bias, const uint16_t *residual,
+                                    uint16_t *Y, uint16_t *P, uint16_t *Z, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+  if (!W) return LORA4_ERR_NULL;
+  return ffn_forward(fused_of(W, M, r), activation, X, A, B, s, group_offsets, FfnOut{Y, P, Z, bias, residual},
+                     workspace, workspace_bytes, reinterpret_cast<hipStream_t>(stream));
+}
+
+lora4_status lora4_backward_epilogue(const lora4_W *W, int32_t activation, const uint16_t *X, const uint16_t *dY,
+                                     const uint16_t *P, int64_t M, const uint16_t *A, const uint16_t *B, int32_t r,
+                                     float s, const int64_t *group_offsets, const uint16_t *Z, uint16_t *dX,
+                                     uint16_t *dA, uint16_t *dB, uint16_t *dbias, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
+  if (!W) return LORA4_ERR_NULL;
+  const Ffn f = fused_of(W, M, r);
+  TRY(check_ffn(f, activation, s, group_offsets));
+  const bool act = activation != LORA4_ACT_NONE;
+  if (!A || !B || !dA || !dB || (M > 0 && (!X || !dY || !dX || (act && !P)))) return LORA4_ERR_NULL;
+  if (!all_aligned16({X, dY, P, A, B, group_offsets, Z, dX, dA, dB, dbias, workspace})) return LORA4_ERR_ALIGN;
+  const FusedBwdPlan pl = fused_bwd_plan(f, act, dbias != nullptr);
+  if (!workspace || workspace_bytes < pl.bytes) return LORA4_ERR_WORKSPACE;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const int64_t N = W->N;
+  if (M == 0) {
+    if (dbias) TRY(fill_zero(dbias, f.E * N, st));
+  } else if (act || dbias) {
+    float *part = dbias ? ws_at<float>(workspace, pl.off_part) : nullptr;
+    uint16_t *dP = act ? ws_at<uint16_t>(workspace, pl.off_dp) : nullptr;
+    actbwd::ActParams q{dY, act ? P : nullptr, M, (int)N, activation, group_offsets, (int)f.E, dP, part};
+    const void *fn = ffn::act_bwd_kernel();
+    void *argv[] = {&q};
+    TRY(launch_timed("act_bwd", st, [&] {
+      (void)hipLaunchKernel(fn, dim3((unsigned)pl.xblocks, (unsigned)pl.splits, (unsigned)f.E), dim3(actbwd::THREADS),
+                            argv, 0, st);
+    }));
+    if (dbias) {
+      const int n = pl.splits * 4, D = (int)N;
+      void *sargv[] = {&part, (void *)&n, (void *)&D, &dbias};
+      const void *sum = ffn::col_sum_kernel();
+      TRY(launch_timed("dbias_sum", st, [&] {
+        (void)hipLaunchKernel(sum, dim3((unsigned)ceil_div(N, 32), (unsigned)f.E), dim3(1024), sargv, 0, st);
+      }));
+    }
+    if (act) dY = dP;
+  }
+  return backward_impl(Base{W, f.E, false}, X, dY, M, A, B, r, s, group_offsets, Z, dX, dA, dB,
+                       ws_at<char>(workspace, pl.off_lin), pl.lin_bytes, stream);
+}
+
 }  // extern "C"
 #pragma GCC visibility pop
+
+// The feed-forward kernels compile as a unit of their own (ffn.hip) where the
+// build asks for it, else here.
+#ifndef LORA4_FFN_SEPARATE
+#include "ffn.hip"
+#endif

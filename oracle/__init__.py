@@ -56,8 +56,10 @@ Parity status per function (what pins it is listed in ``tests/``):
                      values and NF4 LoftQ against plain NF4.
 * lora.*             pinned by finite differences, pure-Python loops, the
                      merge identity and the B = 0 / A = 0 special cases.
+* ffn.*              pinned by finite differences of every gradient, torch's
+                     own activations and closed forms of the norm.
 """
 
-from . import codecs, nf4, mxfp4, nvfp4, lora, mxfp8, loftq  # noqa: F401
+from . import codecs, nf4, mxfp4, nvfp4, lora, mxfp8, loftq, ffn  # noqa: F401
 
-__all__ = ["codecs", "nf4", "mxfp4", "nvfp4", "lora", "mxfp8", "loftq"]
+__all__ = ["codecs", "nf4", "mxfp4", "nvfp4", "lora", "mxfp8", "loftq", "ffn"]

@@ -1,0 +1,534 @@
+"""GPU tests of the feed-forward operators against the float64 oracle.
+
+Each float output passes two checks: relative Frobenius error at most TOL, and
+per element |gpu - ref| <= 1.01 u (|ref| + I) + 2^-9 rms(ref), u = 2^-8 the bf16
+unit roundoff (gpu_util.element_bound). I bounds what the bf16 intermediates
+carry into the output, each off by at most u of its own value: s Z in the
+forward; dG, dU, dP and dZ in the backward (every one a sum of absolute values,
+so no cancellation is assumed). The saved G, U, P and Z are inputs of the
+backward and enter the oracle as the bf16 values they are. Every output and
+workspace sits between guard bands.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import lora_fine_tuning_amd as L
+import synth
+from gpu_util import (DEV, compare_full, f64, guarded, oracle_dequant, oracle_pack, pack_gpu, print_case, to_dev,
+                      to_host)
+from oracle import ffn
+
+pytestmark = pytest.mark.gpu
+
+FMTS = [synth.NF4, synth.NF4_DQ, synth.MXFP4, synth.NVFP4]
+bf = torch.bfloat16
+
+
+def normal(rng, shape, std=1.0):
+    return synth.to_bf16((rng.standard_normal(shape) * std).astype(np.float32))
+
+
+# ---------------------------------------------------------------------------
+# RMS norm
+# ---------------------------------------------------------------------------
+
+NORM_SHAPES = [(1, 1), (1, 4096), (3, 7), (5, 64), (4, 513), (130, 1000), (7, 1024), (9, 1025), (33, 5003), (2, 8192),
+               (3, 16384), (17, 16383), (300, 96), (2100, 160)]
+
+
+@pytest.mark.parametrize("M,D", NORM_SHAPES)
+@pytest.mark.parametrize("res", [False, True])
+def test_rmsnorm_forward(M, D, res):
+    print_case("rmsnorm", M, D, res)
+    rng = np.random.default_rng(M * 31 + D)
+    X, w, R = normal(rng, (M, D), 2.0), normal(rng, (D,), 0.5), normal(rng, (M, D))
+    if M > 2:
+        X[1] = 0            # a row of zeros (with res: the residual's alone)
+    mx = D % 32 == 0
+    out = {}
+    checks = []
+    for name, shape, dt in [("Y", (M, D), bf)] + ([("H", (M, D), bf)] if res else []) + \
+            ([("codes", (M, D), torch.uint8), ("scales", (M, D // 32), torch.uint8)] if mx else []):
+        out[name], c = guarded(shape, dt)
+        checks.append((name, c))
+    o = L.rmsnorm(to_dev(X), to_dev(w), 1e-5, residual=to_dev(R) if res else None, out=out)
+    torch.cuda.synchronize()
+    for name, c in checks:
+        c(name)
+    ref = ffn.rmsnorm(f64(X), f64(w), 1e-5, f64(R) if res else None)
+    compare_full("Y", to_host(o["Y"]), ref["Y"])
+    if res:
+        compare_full("H", to_host(o["H"]), ref["H"])
+    else:
+        assert o["H"] is None
+    if mx:
+        codes, scales = L.mxfp8(o["Y"].contiguous())
+        assert torch.equal(codes, o["codes"]) and torch.equal(scales, o["scales"])
+
+
+@pytest.mark.parametrize("M,D", NORM_SHAPES)
+@pytest.mark.parametrize("dh,dw", [(False, True), (True, True), (True, False)])
+def test_rmsnorm_backward(M, D, dh, dw):
+    print_case("rmsnorm bwd", M, D, dh, dw)
+    rng = np.random.default_rng(M * 37 + D)
+    H, w, dY, dH = normal(rng, (M, D), 2.0), normal(rng, (D,), 0.5), normal(rng, (M, D)), normal(rng, (M, D))
+    out = {}
+    out["dX"], c1 = guarded((M, D))
+    if dw:
+        out["dW"], c2 = guarded((D,))
+    ws, c3 = guarded((L.lora4_rmsnorm_workspace_bytes(M, D),), torch.uint8)
+    o = L.rmsnorm_backward(to_dev(dY), to_dev(H), to_dev(w), 1e-5, dH=to_dev(dH) if dh else None, want_dw=dw,
+                           workspace=ws, out=out)
+    torch.cuda.synchronize()
+    c1("dX")
+    c3("workspace")
+    ref = ffn.rmsnorm_backward(f64(dY), f64(H), f64(w), 1e-5, f64(dH) if dh else None)
+    # (one element: t - n mean(t n) cancels to eps of t, so the rounding of t itself
+    # in fp32, 2^-24 |rstd t|, is added to the reference's scale)
+    if D == 1 and not dh:
+        t = np.abs(f64(dY) * f64(w)) / np.maximum(np.abs(f64(H)), 1e-30)
+        assert np.all(np.abs(f64(to_host(o["dX"])) - ref["dX"]) <= 2.0 ** -21 * t + 2.0 ** -8 * np.abs(ref["dX"]))
+    else:
+        compare_full("dX", to_host(o["dX"]), ref["dX"])
+    if dw:
+        c2("dW")
+        compare_full("dW", to_host(o["dW"]), ref["dW"])
+    else:
+        assert o["dW"] is None
+
+
+def test_rmsnorm_in_place_and_special_rows():
+    M, D = 9, 1056
+    rng = np.random.default_rng(4)
+    X, R, w = normal(rng, (M, D)), normal(rng, (M, D)), normal(rng, (D,))
+    X[2, 5] = 0x7F80          # +inf
+    X[4, 7] = 0x7FC0          # NaN
+    x, r, wd = to_dev(X), to_dev(R), to_dev(w)
+    plain = L.rmsnorm(x, wd, 1e-6, residual=r, mx=True)
+    for alias in ("x", "r"):
+        a, b = x.clone(), r.clone()
+        got = L.rmsnorm(a, wd, 1e-6, residual=b, mx=True, out={"H": a if alias == "x" else b})
+        assert got["H"].data_ptr() == (a if alias == "x" else b).data_ptr()
+        for k in ("Y", "H"):
+            assert torch.equal(got[k].view(torch.int16), plain[k].view(torch.int16)), (alias, k)
+        assert torch.equal(got["codes"], plain["codes"])
+    y = f64(to_host(plain["Y"]))
+    good = [i for i in range(M) if i not in (2, 4)]
+    with np.errstate(all="ignore"):
+        ref = ffn.rmsnorm(f64(X)[good], f64(w), 1e-6, f64(R)[good])["Y"]
+    compare_full("Y", y[good], ref)
+    assert not np.all(np.isfinite(y[2])) and np.all(np.isnan(y[4]))
+    # the gradient in place of the one that comes past the norm
+    h, dy, dh = plain["H"][good].contiguous(), to_dev(normal(rng, (7, D))), to_dev(normal(rng, (7, D)))
+    want = L.rmsnorm_backward(dy, h, wd, 1e-6, dH=dh, want_dw=False)["dX"]
+    got = L.rmsnorm_backward(dy, h, wd, 1e-6, dH=dh, want_dw=False, out={"dX": dh})["dX"]
+    assert torch.equal(got, want)
+    assert L.rmsnorm_backward(dy[:0], h[:0], wd, 1e-6)["dW"].abs().sum().item() == 0
+
+
+# ---------------------------------------------------------------------------
+# Gated projections and the linear with an epilogue
+# ---------------------------------------------------------------------------
+
+class Case:
+    """Seeded inputs of one layer: P projections per expert, their dequantized
+    bases (float64, the oracle's) and the packed base (the library's)."""
+
+    def __init__(self, M, K, N, r, fmt, P, offsets=None, seed=0):
+        rng = np.random.default_rng(1000 * seed + M + 7 * K + 13 * N + r)
+        self.E = 1 if offsets is None else len(offsets) - 1
+        G = self.E * P
+        self.M, self.K, self.N, self.r, self.P, self.fmt = M, K, N, r, P, fmt
+        self.offs = [0, M] if offsets is None else list(offsets)
+        self.s = 1.5
+        W = normal(rng, (G, N, K), 0.05)
+        self.base = pack_gpu(W if G > 1 else W[0], fmt)
+        self.Wd = [f64(oracle_dequant(oracle_pack(W[g], fmt), fmt)) for g in range(G)]
+        self.X, self.A, self.B = normal(rng, (M, K)), normal(rng, (G, r, K), K ** -0.5), normal(rng, (G, N, r), 0.3)
+        self.dY, self.bias, self.R = normal(rng, (M, N)), normal(rng, (self.E, N)), normal(rng, (M, N), 2.0)
+        self.offsets = None if offsets is None else torch.tensor(self.offs, dtype=torch.int64, device=DEV)
+
+    def rows(self):
+        for e in range(self.E):
+            yield e, slice(self.offs[e], self.offs[e + 1])
+
+    def dev(self, *names):
+        t = []
+        for n in names:
+            a = getattr(self, n)
+            if n in ("A", "B") and self.P == 1 and self.E == 1 or n == "bias" and self.E == 1:
+                a = a[0]
+            t.append(to_dev(a))
+        return t
+
+
+def abs_mm(a, b):
+    return np.abs(a) @ np.abs(b)
+
+
+def run_gated(c, act, save=True):
+    X, A, B = c.dev("X", "A", "B")
+    out, checks = {}, []
+    for name, shape in [("H", (c.M, c.N))] + ([("GU", (c.M, 2 * c.N)), ("Z", (c.M, 2 * c.r))] if save else []):
+        out[name], chk = guarded(shape)
+        checks.append((name, chk))
+    ws, chk = guarded((L.lora4_gated_workspace_bytes(0, c.base.abi(), c.M, c.r),), torch.uint8)
+    checks.append(("workspace", chk))
+    o = L.gated_forward(c.base, X, A, B, c.s, activation=act, group_offsets=c.offsets, want_saved=save, workspace=ws,
+                        out=out)
+    torch.cuda.synchronize()
+    for name, chk in checks:
+        chk(name)
+    return o
+
+
+def check_gated(c, act, o):
+    H, GU, Z, IH, IGU = [np.zeros((c.M, n)) for n in (c.N, 2 * c.N, 2 * c.r, c.N, 2 * c.N)]
+    for e, sl in c.rows():
+        x, A, B = f64(c.X[sl]), f64(c.A[2 * e:2 * e + 2]), f64(c.B[2 * e:2 * e + 2])
+        f = ffn.gated_forward(x, c.Wd[2 * e], c.Wd[2 * e + 1], A, B, c.s, act)
+        H[sl], Z[sl] = f["H"], f["Z"]
+        GU[sl] = np.concatenate([f["G"], f["U"]], 1)
+        ig = c.s * abs_mm(f["Z"][:, :c.r], B[0].T)
+        iu = c.s * abs_mm(f["Z"][:, c.r:], B[1].T)
+        v, d = ffn.act(f["G"], act)
+        IGU[sl] = np.concatenate([ig, iu], 1)
+        IH[sl] = np.abs(d * f["U"]) * ig + np.abs(v) * iu
+    compare_full("H", to_host(o["H"]), H, IH)
+    if o["GU"] is not None:
+        compare_full("GU", to_host(o["GU"]), GU, IGU)
+        compare_full("Z", to_host(o["Z"]), Z)
+
+
+def run_epilogue(c, act, bias, res, save=True):
+    X, A, B, bv, R = c.dev("X", "A", "B", "bias", "R")
+    out, checks = {}, []
+    names = [("Y", (c.M, c.N))] + ([("Z", (c.M, c.r))] if save else []) + \
+        ([("P", (c.M, c.N))] if save and act != "none" else [])
+    for name, shape in names:
+        out[name], chk = guarded(shape)
+        checks.append((name, chk))
+    ws, chk = guarded((L.lora4_epilogue_workspace_bytes(0, c.base.abi(), c.M, c.r),), torch.uint8)
+    checks.append(("workspace", chk))
+    o = L.forward_epilogue(c.base, X, A, B, c.s, bias=bv if bias else None, activation=act,
+                           residual=R if res else None, group_offsets=c.offsets, want_saved=save, workspace=ws,
+                           out=out)
+    torch.cuda.synchronize()
+    for name, chk in checks:
+        chk(name)
+    return o
+
+
+def check_epilogue(c, act, bias, res, o):
+    Y, P, Z, IY, IP = [np.zeros((c.M, n)) for n in (c.N, c.N, c.r, c.N, c.N)]
+    for e, sl in c.rows():
+        B = f64(c.B[e])
+        f = ffn.epilogue_forward(f64(c.X[sl]), c.Wd[e], f64(c.A[e]), B, c.s, act, f64(c.bias[e]) if bias else None,
+                                 f64(c.R[sl]) if res else None)
+        Y[sl], P[sl], Z[sl] = f["Y"], f["P"], f["Z"]
+        IP[sl] = c.s * abs_mm(f["Z"], B.T)
+        IY[sl] = np.abs(ffn.act(f["P"], act)[1]) * IP[sl]
+    compare_full("Y", to_host(o["Y"]), Y, IY)
+    if o["Z"] is not None:
+        compare_full("Z", to_host(o["Z"]), Z)
+    if o["P"] is not None:
+        compare_full("P", to_host(o["P"]), P, IP)
+
+
+# the schedules: the library's own choice, the few-token kernel with 16, 32 and
+# 64 tokens per slot, tiles of 64, 128 and 256 rows
+POLICIES = ["", "16", "32", "64", "1064", "1128", "1256"]
+SHAPES = [(1, 256, 96, 16), (5, 320, 200, 8), (17, 512, 257, 4), (64, 1024, 64, 1), (130, 640, 384, 24),
+          (300, 192, 515, 128)]
+MX_SHAPES = [(1, 96, 33, 3), (40, 352, 131, 12)]    # K % 64 == 32, odd N and r
+
+
+def _shapes(fmt):
+    return SHAPES + (MX_SHAPES if fmt in (synth.MXFP4, synth.NVFP4) else [])
+
+
+GRID = [(fmt, shape, pol) for fmt in FMTS for shape in _shapes(fmt) for pol in POLICIES
+        if not (pol in ("16", "32") and shape[0] > 130)]
+
+
+@pytest.mark.parametrize("fmt,shape,policy", GRID)
+def test_gated_forward(fmt, shape, policy, monkeypatch):
+    print_case("gated", fmt, shape, policy)
+    monkeypatch.setenv("LORA4_FFN_ROWS", policy)
+    c = Case(*shape, fmt, 2)
+    act = ["silu", "gelu", "gelu_tanh", "none"][(shape[0] + len(policy)) % 4]
+    check_gated(c, act, run_gated(c, act, save=shape[0] != 5))
+
+
+@pytest.mark.parametrize("fmt,shape,policy", GRID)
+def test_forward_epilogue(fmt, shape, policy, monkeypatch):
+    print_case("epilogue", fmt, shape, policy)
+    monkeypatch.setenv("LORA4_FFN_ROWS", policy)
+    c = Case(*shape, fmt, 1, seed=1)
+    k = shape[0] + len(policy)
+    act = ["none", "gelu", "gelu_tanh", "silu"][k % 4]
+    bias, res = k % 3 != 0, k % 2 == 0
+    check_epilogue(c, act, bias, res, run_epilogue(c, act, bias, res, save=shape[0] != 5))
+
+
+OFFSETS = [[0, 0, 37, 100], [0, 150, 150, 151, 460], [0, 3, 4, 5, 5, 6]]
+MANY = [0] * 20 + list(range(0, 9)) + [8] * 62 + [11]     # 90 experts, 9 with rows
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("offsets", OFFSETS + [MANY])
+@pytest.mark.parametrize("policy", POLICIES)
+def test_experts_forward(fmt, offsets, policy, monkeypatch):
+    if len(offsets) > 10 and fmt != synth.MXFP4:
+        pytest.skip("one format is enough for many experts")
+    print_case("experts", fmt, len(offsets) - 1, policy)
+    monkeypatch.setenv("LORA4_FFN_ROWS", policy)
+    c = Case(offsets[-1], 192, 100, 8, fmt, 2, offsets)
+    check_gated(c, "silu", run_gated(c, "silu"))
+    c = Case(offsets[-1], 192, 100, 12, fmt, 1, offsets, seed=1)
+    check_epilogue(c, "gelu", True, True, run_epilogue(c, "gelu", True, True))
+
+
+BWD = [((1, 256, 96, 16), None), ((70, 320, 200, 8), None), ((130, 640, 257, 4), None), ((300, 192, 515, 128), None),
+       ((600, 512, 640, 40), None), ((100, 256, 130, 8), [0, 0, 37, 100]), ((460, 192, 200, 12), [0, 150, 150, 460])]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("shape,offsets", BWD)
+@pytest.mark.parametrize("big", ["", "1", "0"])
+def test_gated_backward(fmt, shape, offsets, big, monkeypatch):
+    print_case("gated bwd", fmt, shape, offsets, big)
+    if big:
+        monkeypatch.setenv("LORA4_BIG", big)
+    c = Case(*shape, fmt, 2, offsets, seed=2)
+    act = ["silu", "gelu", "gelu_tanh", "none"][(shape[0] + len(big)) % 4]
+    with_z = shape[0] != 70
+    rng = np.random.default_rng(9)
+    GU, Zs = normal(rng, (c.M, 2 * c.N)), normal(rng, (c.M, 2 * c.r))
+    X, A, B, dH = c.dev("X", "A", "B", "dY")
+    out, checks = {}, []
+    for name, shp in [("dX", (c.M, c.K)), ("dA", c.A.shape), ("dB", c.B.shape)]:
+        out[name], chk = guarded(shp)
+        checks.append((name, chk))
+    ws, chk = guarded((L.lora4_gated_workspace_bytes(1, c.base.abi(), c.M, c.r),), torch.uint8)
+    checks.append(("workspace", chk))
+    o = L.gated_backward(c.base, X, dH, to_dev(GU), A, B, c.s, activation=act, Z=to_dev(Zs) if with_z else None,
+                         group_offsets=c.offsets, workspace=ws, out=out)
+    torch.cuda.synchronize()
+    for name, chk in checks:
+        chk(name)
+    dX, IX = np.zeros((c.M, c.K)), np.zeros((c.M, c.K))
+    dA, dB, IA, IB = [np.zeros(t.shape) for t in (c.A, c.B, c.A, c.B)]
+    for e, sl in c.rows():
+        x, W = f64(c.X[sl]), c.Wd[2 * e:2 * e + 2]
+        As, Bs = f64(c.A[2 * e:2 * e + 2]), f64(c.B[2 * e:2 * e + 2])
+        g, u = f64(GU[sl, :c.N]), f64(GU[sl, c.N:])
+        z = f64(Zs[sl]) if with_z else np.concatenate([x @ As[0].T, x @ As[1].T], 1)
+        b = ffn.gated_backward(x, W[0], W[1], As, Bs, c.s, act, f64(c.dY[sl]), g, u, z)
+        dX[sl], dA[2 * e:2 * e + 2], dB[2 * e:2 * e + 2] = b["dX"], b["dA"], b["dB"]
+        for j, d in ((0, b["dG"]), (1, b["dU"])):
+            dz = b["dZ"][:, j * c.r:(j + 1) * c.r]
+            iz = np.abs(dz) + c.s * abs_mm(d, Bs[j])          # dZ: its own rounding and that of dG (dU)
+            IX[sl] += abs_mm(d, W[j]) + iz @ np.abs(As[j])
+            IA[2 * e + j] = iz.T @ np.abs(x)
+            zj = z[:, j * c.r:(j + 1) * c.r]
+            IB[2 * e + j] = c.s * abs_mm(d.T, zj) * (1 if with_z else 2)   # (a recomputed Z is rounded too)
+    compare_full("dX", to_host(o["dX"]), dX, IX)
+    compare_full("dA", to_host(o["dA"]), dA, IA)
+    compare_full("dB", to_host(o["dB"]), dB, IB)
+
+
+@pytest.mark.parametrize("fmt", [synth.NF4, synth.NVFP4])
+@pytest.mark.parametrize("shape,offsets", BWD)
+def test_backward_epilogue(fmt, shape, offsets):
+    print_case("epilogue bwd", fmt, shape, offsets)
+    c = Case(*shape, fmt, 1, offsets, seed=3)
+    act = ["none", "gelu", "gelu_tanh", "silu"][shape[0] % 4]
+    want_dbias = shape[0] != 70
+    rng = np.random.default_rng(9)
+    Ps, Zs = normal(rng, (c.M, c.N)), normal(rng, (c.M, c.r))
+    X, A, B, dY = c.dev("X", "A", "B", "dY")
+    out, checks = {}, []
+    names = [("dX", (c.M, c.K)), ("dA", tuple(A.shape)), ("dB", tuple(B.shape))]
+    if want_dbias:
+        names.append(("dbias", (c.N,) if c.E == 1 else (c.E, c.N)))
+    for name, shp in names:
+        out[name], chk = guarded(shp)
+        checks.append((name, chk))
+    ws, chk = guarded((L.lora4_epilogue_workspace_bytes(1, c.base.abi(), c.M, c.r),), torch.uint8)
+    checks.append(("workspace", chk))
+    o = L.backward_epilogue(c.base, X, dY, A, B, c.s, P=to_dev(Ps) if act != "none" else None, activation=act,
+                            Z=to_dev(Zs), group_offsets=c.offsets, workspace=ws, out=out)
+    torch.cuda.synchronize()
+    for name, chk in checks:
+        chk(name)
+    dX, IX = np.zeros((c.M, c.K)), np.zeros((c.M, c.K))
+    dA, dB, IA, IB = [np.zeros(t.shape) for t in (c.A, c.B, c.A, c.B)]
+    db, idb = np.zeros((c.E, c.N)), np.zeros((c.E, c.N))
+    k = 0 if act == "none" else 1            # dP is rounded only with an activation
+    for e, sl in c.rows():
+        x, As, Bs = f64(c.X[sl]), f64(c.A[e]), f64(c.B[e])
+        b = ffn.epilogue_backward(x, c.Wd[e], As, Bs, c.s, act, f64(c.dY[sl]), f64(Ps[sl]), f64(Zs[sl]))
+        dX[sl], dA[e], dB[e], db[e] = b["dX"], b["dA"], b["dB"], b["dbias"]
+        iz = np.abs(b["dZ"]) + k * c.s * abs_mm(b["dP"], Bs)
+        IX[sl] = k * abs_mm(b["dP"], c.Wd[e]) + iz @ np.abs(As)
+        IA[e] = iz.T @ np.abs(x)
+        IB[e] = k * c.s * abs_mm(b["dP"].T, f64(Zs[sl]))
+        # fp32 sums of the terms over the rows: 2^-24 per addition, 12 levels and the serial part
+        idb[e] = 2.0 ** -13 * np.abs(b["dP"]).sum(0)
+    compare_full("dX", to_host(o["dX"]), dX, IX)
+    compare_full("dA", to_host(o["dA"]).reshape(dA.shape), dA, IA)
+    compare_full("dB", to_host(o["dB"]).reshape(dB.shape), dB, IB)
+    if want_dbias:
+        compare_full("dbias", to_host(o["dbias"]).reshape(db.shape), db, idb)
+
+
+def test_no_rows():
+    c = Case(4, 128, 96, 8, synth.NF4, 2)
+    X, A, B = c.dev("X", "A", "B")
+    o = L.gated_forward(c.base, X[:0], A, B, c.s)
+    assert o["H"].shape == (0, 96) and o["GU"].shape == (0, 192)
+    g = L.gated_backward(c.base, X[:0], o["H"], o["GU"], A, B, c.s)
+    assert g["dA"].abs().sum().item() == 0 and g["dB"].abs().sum().item() == 0
+    c = Case(4, 128, 96, 8, synth.NF4, 1)
+    X, A, B = c.dev("X", "A", "B")
+    assert L.forward_epilogue(c.base, X[:0], A, B, c.s)["Y"].shape == (0, 96)
+    g = L.backward_epilogue(c.base, X[:0], X.new_empty((0, 96)), A, B, c.s, want_dbias=True)
+    assert all(g[k].abs().sum().item() == 0 for k in ("dA", "dB", "dbias"))
+
+
+@pytest.mark.parametrize("M", [3, 40, 200])
+def test_non_finite_rows_stay_apart(M):
+    """A token with infinities and NaNs leaves the other tokens' outputs as they were."""
+    c = Case(M, 320, 100, 8, synth.MXFP4, 2)
+    X, A, B = c.dev("X", "A", "B")
+    want = L.gated_forward(c.base, X, A, B, c.s)
+    X2 = X.clone()
+    X2[1, 5], X2[1, 300] = float("inf"), float("nan")
+    got = L.gated_forward(c.base, X2, A, B, c.s)
+    keep = [i for i in range(M) if i != 1]
+    for k in ("H", "GU", "Z"):
+        assert torch.equal(got[k][keep], want[k][keep]), k
+    assert not torch.isfinite(got["GU"][1]).all()
+
+
+def test_residual_in_place():
+    for M in (4, 300):
+        c = Case(M, 256, 203, 8, synth.NF4, 1)
+        X, A, B, R = c.dev("X", "A", "B", "R")
+        want = L.forward_epilogue(c.base, X, A, B, c.s, residual=R)["Y"]
+        got = L.forward_epilogue(c.base, X, A, B, c.s, residual=R, out={"Y": R})["Y"]
+        assert got.data_ptr() == R.data_ptr() and torch.equal(got, want)
+
+
+# ---------------------------------------------------------------------------
+# The operators together
+# ---------------------------------------------------------------------------
+
+class Block:
+    """The feed-forward half of a block: norm (of the residual's sum) -> gated
+    projections -> down projection with the residual added -> norm."""
+
+    def __init__(self, D, F, r, fmt, seed):
+        rng = np.random.default_rng(seed)
+        self.up, self.down = Case(1, D, F, r, fmt, 2, seed=seed), Case(1, F, D, r, fmt, 1, seed=seed + 1)
+        self.w1, self.w2 = to_dev(normal(rng, (D,), 0.3)), to_dev(normal(rng, (D,), 0.3))
+        self.ga = self.up.dev("A", "B")
+        self.da = self.down.dev("A", "B")
+        self.s = 0.5
+
+    def forward(self, X, R):
+        n1 = L.rmsnorm(X, self.w1, 1e-5, residual=R)
+        g = L.gated_forward(self.up.base, n1["Y"], *self.ga, self.s)
+        d = L.forward_epilogue(self.down.base, g["H"], *self.da, self.s, residual=n1["H"])
+        n2 = L.rmsnorm(d["Y"], self.w2, 1e-5, mx=True)
+        return n1, g, d, n2
+
+    def backward(self, saved, dY):
+        n1, g, d, _ = saved
+        b2 = L.rmsnorm_backward(dY, d["Y"], self.w2, 1e-5)
+        bd = L.backward_epilogue(self.down.base, g["H"], b2["dX"], *self.da, self.s, Z=d["Z"])
+        bg = L.gated_backward(self.up.base, n1["Y"], bd["dX"], g["GU"], *self.ga, self.s, Z=g["Z"])
+        b1 = L.rmsnorm_backward(bg["dX"], n1["H"], self.w1, 1e-5, dH=b2["dX"])
+        return b2, bd, bg, b1
+
+
+@pytest.mark.parametrize("M", [1, 33, 260])
+def test_block_run(M):
+    """Every stage of the run against the oracle on that stage's own inputs."""
+    D, F, r = 320, 576, 8
+    b = Block(D, F, r, synth.NF4, 11)
+    rng = np.random.default_rng(M)
+    X, R, dY = (to_dev(normal(rng, (M, D))) for _ in range(3))
+    saved = b.forward(X, R)
+    grads = b.backward(saved, dY)
+    torch.cuda.synchronize()
+    n1, g, d, n2 = saved
+    h = lambda t: f64(to_host(t))
+    ref = ffn.rmsnorm(h(X), h(b.w1), 1e-5, h(R))
+    compare_full("H1", to_host(n1["H"]), ref["H"])
+    compare_full("Y1", to_host(n1["Y"]), ref["Y"])
+    A, B = (f64(t) for t in (b.up.A, b.up.B))
+    f = ffn.gated_forward(h(n1["Y"]), b.up.Wd[0], b.up.Wd[1], A, B, b.s, "silu")
+    ig, iu = (b.s * abs_mm(f["Z"][:, j * r:(j + 1) * r], B[j].T) for j in (0, 1))
+    v, sl = ffn.act(f["G"], "silu")
+    compare_full("H", to_host(g["H"]), f["H"], np.abs(sl * f["U"]) * ig + np.abs(v) * iu)
+    Ad, Bd = f64(b.down.A[0]), f64(b.down.B[0])
+    e = ffn.epilogue_forward(h(g["H"]), b.down.Wd[0], Ad, Bd, b.s, "none", None, h(n1["H"]))
+    compare_full("Yd", to_host(d["Y"]), e["Y"], b.s * abs_mm(e["Z"], Bd.T))
+    compare_full("Y2", to_host(n2["Y"]), ffn.rmsnorm(h(d["Y"]), h(b.w2), 1e-5)["Y"])
+    b2, bd, bg, b1 = grads
+    ref = ffn.rmsnorm_backward(h(dY), h(d["Y"]), h(b.w2), 1e-5)
+    compare_full("dX2", to_host(b2["dX"]), ref["dX"])
+    compare_full("dW2", to_host(b2["dW"]), ref["dW"])
+    ref = ffn.epilogue_backward(h(g["H"]), b.down.Wd[0], Ad, Bd, b.s, "none", h(b2["dX"]), None, h(d["Z"]))
+    compare_full("dHd", to_host(bd["dX"]), ref["dX"], np.abs(ref["dZ"]) @ np.abs(Ad))
+    ref = ffn.gated_backward(h(n1["Y"]), b.up.Wd[0], b.up.Wd[1], A, B, b.s, "silu", h(bd["dX"]), h(g["GU"])[:, :F],
+                             h(g["GU"])[:, F:], h(g["Z"]))
+    I = 0
+    for j, dd in ((0, ref["dG"]), (1, ref["dU"])):
+        I = I + abs_mm(dd, b.up.Wd[j]) + (np.abs(ref["dZ"][:, j * r:(j + 1) * r]) + b.s * abs_mm(dd, B[j])) @ np.abs(A[j])
+    compare_full("dX", to_host(bg["dX"]), ref["dX"], I)
+    ref = ffn.rmsnorm_backward(h(bg["dX"]), h(n1["H"]), h(b.w1), 1e-5, h(b2["dX"]))
+    compare_full("dX1", to_host(b1["dX"]), ref["dX"])
+    compare_full("dW1", to_host(b1["dW"]), ref["dW"])
+
+
+def _all(saved, grads):
+    return [t for d in saved + grads for t in d.values() if t is not None]
+
+
+@pytest.mark.parametrize("M", [1, 48, 300])
+def test_block_in_a_graph_and_on_another_stream(M):
+    """The run captured once and replayed, with eager work between the replays,
+    and the run on a side stream give the eager bits."""
+    D, F, r = 384, 640, 16
+    b = Block(D, F, r, synth.MXFP4, 21)
+    rng = np.random.default_rng(M)
+    X, R, dY = (to_dev(normal(rng, (M, D))) for _ in range(3))
+    saved = b.forward(X, R)
+    want = _all(saved, b.backward(saved, dY))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        s2 = b.forward(X, R)
+        got = _all(s2, b.backward(s2, dY))
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s3 = b.forward(X, R)
+        got = _all(s3, b.backward(s3, dY))
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)

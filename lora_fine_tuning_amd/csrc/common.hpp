@@ -158,4 +158,47 @@ __device__ __forceinline__ RowTile map_row_tile(int slot, int BM, const int64_t 
   return t;
 }
 
+// As map_row_tile, with the 64 lanes of a wave looking through 64 groups at a
+// time (a grid of few-token slots runs over every expert).
+// The result is uniform, and in scalar registers (buffer descriptors made
+// from vector registers cost a loop around every load).
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  return ((int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+}
+__device__ __forceinline__ RowTile map_row_tile_wave(int slot, int BM, const int64_t *offsets, int groups,
+                                                     int64_t M) {
+  if (offsets == nullptr) return map_row_tile(slot, BM, nullptr, 1, M);
+  RowTile t{-1, 0, 0};
+  const int lane = threadIdx.x & 63;
+  int64_t base = 0;   // slots of the groups before e0
+  for (int e0 = 0; e0 < groups; e0 += 64) {
+    const int e = e0 + lane;
+    int64_t a = 0, b = 0;
+    if (e < groups) {
+      a = offsets[e];
+      b = offsets[e + 1];
+    }
+    const int nt = (int)((b - a + BM - 1) / BM);
+    int incl = nt;   // inclusive prefix sum over the lanes
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int64_t first = base + incl - nt;
+    const unsigned long long hit = __ballot(slot >= first && slot < first + nt);
+    if (hit) {
+      const int src = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
+      t.group = e0 + src;
+      const int s = __shfl((int)(slot - first), src);
+      t.row0 = uniform64(__shfl((long long)a, src) + (int64_t)s * BM);
+      t.row_end = uniform64(__shfl((long long)b, src));
+      return t;
+    }
+    base += __shfl(incl, 63);
+  }
+  return t;
+}
+
 }  // namespace lora4

@@ -30,13 +30,23 @@ const void *tile(int rows, bool short_rows) {
                     : addr(fwd::k_gemm_fwd_epi<FMT, EPI, 256, 2, false>);
 }
 
-template <int FMT, int EPI, int NW>
-const void *small_nw(int mt) {
-  switch (mt) {
-    case 1: return addr(small::k_small<FMT, EPI, 1, NW>);
-    case 2: return addr(small::k_small<FMT, EPI, 2, NW>);
-    default: return addr(small::k_small<FMT, EPI, 4, NW>);
-  }
+template <int FMT, int EPI>
+const void *split(int rows) {
+  return rows == 32   ? addr(fwd::k_gemm_fwd_split<FMT, EPI, 32>)
+         : rows == 64 ? addr(fwd::k_gemm_fwd_split<FMT, EPI, 64>)
+                      : addr(fwd::k_gemm_fwd_split<FMT, EPI, 128>);
+}
+
+template <int FMT>
+const void *split_of(int epi, int rows) {
+  return epi == fwd::EPI_GATED ? split<FMT, fwd::EPI_GATED>(rows) : split<FMT, fwd::EPI_FUSED>(rows);
+}
+
+template <int FMT, int EPI, int XT>
+const void *small_xt(int nw) {
+  return nw == 4   ? addr(small::k_small<FMT, EPI, XT, 4>)
+         : nw == 8 ? addr(small::k_small<FMT, EPI, XT, 8>)
+                   : addr(small::k_small<FMT, EPI, XT, 16>);
 }
 
 template <int FMT>
@@ -46,10 +56,10 @@ const void *tile_of(int epi, int rows, bool short_rows) {
 }
 
 template <int FMT>
-const void *small_of(int epi, int mt, int nw) {
+const void *small_of(int epi, int xt, int nw) {
   if (epi == fwd::EPI_GATED)
-    return nw == 4 ? small_nw<FMT, fwd::EPI_GATED, 4>(mt) : small_nw<FMT, fwd::EPI_GATED, 8>(mt);
-  return nw == 4 ? small_nw<FMT, fwd::EPI_FUSED, 4>(mt) : small_nw<FMT, fwd::EPI_FUSED, 8>(mt);
+    return xt == 4 ? small_xt<FMT, fwd::EPI_GATED, 4>(nw) : small_xt<FMT, fwd::EPI_GATED, 8>(nw);
+  return xt == 4 ? small_xt<FMT, fwd::EPI_FUSED, 4>(nw) : small_xt<FMT, fwd::EPI_FUSED, 8>(nw);
 }
 
 }  // namespace
@@ -83,12 +93,25 @@ const void *tile_kernel(int fmt, int epi, int rows, bool short_rows) {
   }
 }
 
-const void *small_kernel(int fmt, int epi, int mt, int nw) {
+const void *split_kernel(int fmt, int epi, int rows) {
   switch (fmt) {
-    case FMT_NF4: return small_of<FMT_NF4>(epi, mt, nw);
-    case FMT_NF4_DQ: return small_of<FMT_NF4_DQ>(epi, mt, nw);
-    case FMT_MXFP4: return small_of<FMT_MXFP4>(epi, mt, nw);
-    default: return small_of<FMT_NVFP4>(epi, mt, nw);
+    case FMT_NF4: return split_of<FMT_NF4>(epi, rows);
+    case FMT_NF4_DQ: return split_of<FMT_NF4_DQ>(epi, rows);
+    case FMT_MXFP4: return split_of<FMT_MXFP4>(epi, rows);
+    default: return split_of<FMT_NVFP4>(epi, rows);
+  }
+}
+
+const void *epi_reduce_kernel(int epi) {
+  return epi == fwd::EPI_GATED ? addr(fwd::k_epi_reduce<fwd::EPI_GATED>) : addr(fwd::k_epi_reduce<fwd::EPI_FUSED>);
+}
+
+const void *small_kernel(int fmt, int epi, int xt, int nw) {
+  switch (fmt) {
+    case FMT_NF4: return small_of<FMT_NF4>(epi, xt, nw);
+    case FMT_NF4_DQ: return small_of<FMT_NF4_DQ>(epi, xt, nw);
+    case FMT_MXFP4: return small_of<FMT_MXFP4>(epi, xt, nw);
+    default: return small_of<FMT_NVFP4>(epi, xt, nw);
   }
 }
 

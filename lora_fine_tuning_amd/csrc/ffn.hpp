@@ -28,8 +28,13 @@ const void *col_sum_kernel();
 // of a group (rows 256 only).
 const void *tile_kernel(int fmt, int epi, int rows, bool short_rows);
 
-// Few tokens: up to 16 mt (1, 2, 4) tokens of a group, nw (4, 8) waves.
-const void *small_kernel(int fmt, int epi, int mt, int nw);
+// The same with the reduction split over blocks (rows 32, 64 or 128; 128
+// columns of both projections or 256), and the sum of their partials.
+const void *split_kernel(int fmt, int epi, int rows);
+const void *epi_reduce_kernel(int epi);
+
+// Few tokens: up to xt (4, 8) tokens of a group, nw (4, 8, 16) waves.
+const void *small_kernel(int fmt, int epi, int xt, int nw);
 const void *small_z_kernel();
 
 const void *gated_bwd_kernel(int tj);   // tj: 16-column blocks of the rank, 1, 2, 4 or 8

@@ -2,9 +2,9 @@
 // planning and dispatch helpers): validation, workspace layout and launch
 // order of the RMS norm, the gated projections and the linear with an epilogue.
 //
-//   gated forward   : M <= SMALL_ROWS tokens per group: Z = X A^T (k_small_z),
-//                     then k_small; else the rank-r row pass (both projections'
-//                     A as one operand of 2 r rows), then the gated tiles
+//   gated forward   : Z = X A^T, both projections' A as one operand of 2 r rows
+//                     (k_small_z, or the rank-r row pass for many rows), then
+//                     k_small, or the gated tiles, whole or split and summed
 //   gated backward  : [Z pass] -> k_gated_bwd (dG, dU, partial dZ) -> dX over
 //                     both projections as one reduction -> dA, dB
 //   fused forward   : as the gated, with one projection
@@ -117,69 +117,147 @@ struct Ffn {
   int r;
 };
 
-// Tokens per group up to which the few-token kernels run.
-constexpr int64_t SMALL_ROWS = 64;
+// Tokens per group up to which the few-token kernel runs: one slot of it, and
+// two for one projection (14336 -> 4096, NF4, 16 tokens: 25 us against 35 with
+// the split tiles; gated, 4096 -> 14336: 39 against 36, 8192 -> 28672 MXFP4: 99
+// against 78).
+constexpr int64_t SMALL_ROWS = 8;
 
-// Forced schedule for tests and measurements (LORA4_FFN_ROWS): 16, 32 or 64
-// the few-token kernel with that many tokens per slot, 1064, 1128 or 1256 the
-// tiles of 64, 128 or 256 rows; anything else or unset: automatic.
+// Forced schedule for tests and measurements (LORA4_FFN_ROWS): 4 or 8 the
+// few-token kernel with that many tokens per slot; 1064, 1128 or 1256 the
+// tiles of 64, 128 or 256 rows; 2032, 2064 or 2128 the tiles of that many rows
+// with their reduction split; anything else or unset: automatic.
 int ffn_policy() {
   const char *e = std::getenv("LORA4_FFN_ROWS");
-  const int v = e ? std::atoi(e) : 0;
-  return v == 16 || v == 32 || v == 64 || v == 1064 || v == 1128 || v == 1256 ? v : 0;
+  if (!e) return 0;
+  const int v = std::atoi(e);
+  for (int ok : {4, 8, 1064, 1128, 1256, 2032, 2064, 2128})
+    if (v == ok) return v;
+  return 0;
 }
 
 struct FfnPlan {
   bool small;
-  int mt, nw;           // small: 16 mt tokens per slot, nw waves
+  int xt, nw;           // small: tokens per slot, waves
   int rows;             // tiles: rows per tile
+  bool split;           // tiles: their reduction in ksplit ranges of split_steps 64-deep steps
+  int ksplit, split_steps;
   int64_t slots, cblocks;
-  SkSched zs;           // tiles: schedule of the rank-r row pass
-  bool z_tail;          // its range partials go to the tiles' tail
-  size_t off_sz, off_part, bytes;
+  bool z_small;         // Z by k_small_z (z_splits ranges of z_per chunks), else by the rank-r row pass
+  int z_splits;
+  int64_t z_per;
+  SkSched zs;           // the rank-r row pass's schedule
+  bool z_tail;          // the tiles' tail adds up Z's range partials
+  size_t off_sz, off_zpart, off_part, bytes;
 };
+
+// The tiles and split of the reduction with the least estimated time. Measured
+// (gated, NF4 and MXFP4 bases of 4096 x 14336 and 8192 x 28672, 16 experts of
+// 7168 x 2048, fused 14336 -> 4096): a 64-deep step of a tile takes about
+// `alone` us on a CU of its own, and `shared` us of the CU where several share
+// one (`occ` at a time); starting a tile and writing it out about 4 us; a split
+// reduction another launch of about 6 us and its partial sums' way through
+// memory. Shapes a few percent apart in this estimate are as close in time.
+struct TileShape {
+  int rows, cols;      // per tile (gated: columns of each projection)
+  bool split;
+  int occ;
+  double alone, shared;
+};
+constexpr TileShape GATED_TILES[] = {
+    {64, 128, false, 2, 0.75, 0.65},  {128, 128, false, 1, 0.95, 0.95}, {256, 128, false, 1, 1.7, 1.7},
+    {32, 128, true, 3, 0.75, 0.65},   {64, 128, true, 2, 0.75, 0.65},   {128, 128, true, 1, 0.95, 0.95},
+};
+constexpr TileShape FUSED_TILES[] = {
+    {64, 128, false, 3, 0.48, 0.38},  {128, 128, false, 2, 0.62, 0.6},  {256, 256, false, 1, 1.7, 1.7},
+    {32, 256, true, 3, 0.75, 0.65},   {64, 256, true, 2, 0.75, 0.65},   {128, 256, true, 1, 0.95, 0.95},
+};
+
+void choose_tiles(const Ffn &f, int64_t M, int pol, int64_t cus, FfnPlan &p) {
+  const int64_t N = f.W->N, steps = ceil_div(f.W->K, fwd::BKS), extra = f.E > 1 ? std::min(f.E, M) : 0;
+  double best = 0;
+  for (const TileShape &s : f.epi == fwd::EPI_GATED ? GATED_TILES : FUSED_TILES) {
+    if (pol && pol != (s.split ? 2000 : 1000) + s.rows) continue;
+    const int64_t slots = ceil_div(M, s.rows) + extra, cb = ceil_div(N, s.cols);
+    // tiles with rows: a group's last one is half full on average
+    const double tiles = (double)cb * (f.E > 1 ? (double)M / s.rows + 0.5 * (double)extra : (double)ceil_div(M, s.rows));
+    // a split: as many ranges (of at least four steps) as keep the chip full once
+    int64_t per = steps, ks = 1;
+    if (s.split) {
+      const int64_t want = std::min<int64_t>((int64_t)((double)(s.occ * cus) / tiles), steps / 4);
+      if (want < 2 && !pol) continue;
+      per = ceil_div(steps, std::max<int64_t>(1, want));
+      ks = ceil_div(steps, per);
+    }
+    const double blocks = tiles * (double)ks;
+    const double rounds = std::ceil(blocks / (double)(s.occ * cus));
+    const double each = std::max(1.0, blocks / (rounds * (double)cus));   // blocks on a CU at a time
+    const double step = s.occ == 1 ? s.alone : std::max(s.alone, each * s.shared);
+    double t = rounds * (step * (double)per + 4.0);
+    if (s.split) t += 6.0 + blocks * s.rows * (4 * 64 * 4) * 2 / 4.0e6;
+    if (p.rows == 0 || t < best) {
+      best = t;
+      p.rows = s.rows;
+      p.slots = slots;
+      p.cblocks = cb;
+      p.split = s.split;
+      p.ksplit = (int)ks;
+      p.split_steps = s.split ? (int)per : 1 << 30;
+    }
+  }
+}
+
+// Rows up to which k_small_z makes the Z of the tiles.
+constexpr int64_t Z_SMALL_ROWS = 1024;
 
 FfnPlan ffn_plan(const Ffn &f) {
   FfnPlan p{};
-  const int64_t M = std::max<int64_t>(f.M, 1), N = f.W->N;
-  const int64_t extra = f.E > 1 ? f.E : 0;   // slots cut short at the groups' ends
+  const int64_t M = std::max<int64_t>(f.M, 1), N = f.W->N, K = f.W->K;
+  const int64_t extra = f.E > 1 ? std::min(f.E, M) : 0;   // slots cut short at the ends of groups with rows
   const int64_t cus = cu_count();
   const int pol = ffn_policy();
+  const int R = f.P * f.r;
   const int64_t mean = ceil_div(M, f.E);
-  p.small = pol ? pol < 1000 : mean <= SMALL_ROWS;
+  p.ksplit = 1;
+  p.split_steps = 1 << 30;
+  p.small = pol ? pol < 1000 : mean <= (f.P == 1 ? 2 : 1) * SMALL_ROWS;
+  int64_t max_zsplits = big::A2_MAX_PARTS;
   if (p.small) {
-    p.mt = pol ? pol / 16 : mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
-    p.slots = ceil_div(M, 16 * p.mt) + extra;
+    p.xt = pol ? pol : mean <= 4 ? 4 : 8;
+    p.slots = ceil_div(M, p.xt) + extra;
     p.cblocks = ceil_div(N, 16);
-    p.nw = std::min(p.slots, ceil_div(M, 16 * p.mt) + std::min(extra, M)) * p.cblocks < 2 * cus ? 8 : 4;
+    // about 14 waves per CU
+    const int64_t groups = p.slots * p.cblocks;
+    p.nw = groups >= 3 * cus ? 4 : groups >= 3 * cus / 2 ? 8 : 16;
+    // (every workgroup of the base product reads the ranges' partials of its
+    // tokens: at most 16 KB)
+    max_zsplits = std::max<int64_t>(1, std::min<int64_t>(16, 4096 / (std::min<int64_t>(M, p.xt) * R)));
   } else {
-    // the tile whose rounds over the chip cost least: time of a tile relative
-    // to one of 256 rows
-    struct Shape {
-      int rows, cols;
-      double cost;
-    };
-    static const Shape gated[] = {{256, 128, 1.0}, {128, 128, 0.58}, {64, 128, 0.40}};
-    static const Shape fused[] = {{256, 256, 1.0}, {128, 128, 0.34}, {64, 128, 0.24}};
-    double best = 0;
-    for (const Shape &s : f.epi == fwd::EPI_GATED ? gated : fused) {
-      if (pol && pol - 1000 != s.rows) continue;
-      const int64_t slots = ceil_div(M, s.rows) + extra, cb = ceil_div(N, s.cols);
-      // (a group's last tile runs the code of the rows it has)
-      const double cost = s.cost * (double)ceil_div(slots * cb, cus);
-      if (p.rows == 0 || cost < best) {
-        best = cost;
-        p.rows = s.rows;
-        p.slots = slots;
-        p.cblocks = cb;
-      }
-    }
-    p.zs = sk_sched(f.M, f.W->K, f.P * f.r, f.E, 0);
-    p.z_tail = p.zs.ranges > 1 && p.zs.ranges <= big::A2_MAX_PARTS;
+    choose_tiles(f, M, pol, cus, p);
   }
-  p.off_sz = 0;
-  p.off_part = align256((size_t)M * f.P * f.r * 2);
-  p.bytes = p.off_part + (p.small ? 0 : sk_part_bytes_for(f.M, f.W->K, f.P * f.r, f.E, 0));
+  p.z_small = p.small || f.M <= Z_SMALL_ROWS;
+  size_t off = 0;
+  auto take = [&](size_t b) {
+    const size_t o = off;
+    off += align256(b);
+    return o;
+  };
+  if (p.z_small) {
+    const int64_t chunks = K / 32;
+    p.z_splits =
+        (int)std::max<int64_t>(1, std::min(ceil_div(chunks, small::Z_WAVES * small::Z_CHUNKS), max_zsplits));
+    p.z_per = ceil_div(chunks, p.z_splits);
+    p.z_splits = (int)ceil_div(chunks, p.z_per);
+    p.off_zpart = take((size_t)p.z_splits * M * R * 4);
+  } else {
+    p.zs = sk_sched(f.M, K, R, f.E, 0);
+    p.z_tail = p.zs.ranges > 1 && p.zs.ranges <= big::A2_MAX_PARTS;
+    p.off_sz = take((size_t)M * R * 2);
+    p.off_zpart = take(sk_part_bytes_for(f.M, K, R, f.E, 0));
+  }
+  if (p.split)
+    p.off_part = take((size_t)p.slots * p.cblocks * p.ksplit * 4 * p.rows * 64 * 4);
+  p.bytes = std::max<size_t>(off, 256);
   return p;
 }
 
@@ -214,22 +292,24 @@ lora4_status ffn_forward(const Ffn &f, int act, const uint16_t *X, const uint16_
   const lora4_W *W = f.W;
   const PackedW pw = packed_of(Base{W, W->groups, false});
   const int R = f.P * f.r;   // rank columns of a row group
-  uint16_t *sZ = ws_at<uint16_t>(ws, pl.off_sz);
-  if (pl.small) {
+  float *zpart = ws_at<float>(ws, pl.off_zpart);
+  if (pl.z_small) {
     small::ZParams z{};
     z.X = X;
     z.A = A;
     z.M = f.M;
     z.K = W->K;
     z.R = R;
-    z.s = s;
     z.offsets = offs;
     z.groups = (int)f.E;
-    z.sZ = sZ;
-    z.Z = o.Z;
+    z.part = zpart;
     z.jblocks = (int)ceil_div(R, 16);
-    const int64_t zslots = ceil_div(f.M, 16) + (f.E > 1 ? f.E : 0);
-    TRY(launch_fn("small_z", ffn::small_z_kernel(), zslots * z.jblocks, 64 * small::Z_WAVES, 0, st, z));
+    z.splits = pl.z_splits;
+    z.per = pl.z_per;
+    const int64_t zslots = ceil_div(f.M, 16) + (f.E > 1 ? std::min(f.E, f.M) : 0);
+    TRY(launch_fn("small_z", ffn::small_z_kernel(), zslots * z.jblocks * z.splits, 64 * small::Z_WAVES, 0, st, z));
+  }
+  if (pl.small) {
     small::Params p{};
     p.W = pw;
     p.X = X;
@@ -239,7 +319,10 @@ lora4_status ffn_forward(const Ffn &f, int act, const uint16_t *X, const uint16_
     p.offsets = offs;
     p.groups = (int)f.E;
     p.r = f.r;
-    p.sZ = sZ;
+    p.zpart = zpart;
+    p.zsplits = pl.z_splits;
+    p.s = s;
+    p.Z = o.Z;
     p.B = B;
     p.act = act;
     p.out = o.out;
@@ -248,18 +331,23 @@ lora4_status ffn_forward(const Ffn &f, int act, const uint16_t *X, const uint16_
     p.residual = o.residual;
     p.nblocks = (int)pl.cblocks;
     p.tab = nf4_table();
-    return launch_fn(f.P == 2 ? "small_gated" : "small_fused", ffn::small_kernel(W->format, f.epi, pl.mt, pl.nw),
-                     pl.slots * pl.cblocks, 64 * pl.nw, small::lds_bytes(f.P, pl.mt, pl.nw), st, p);
+    return launch_fn(f.P == 2 ? "small_gated" : "small_fused", ffn::small_kernel(W->format, f.epi, pl.xt, pl.nw),
+                     pl.slots * pl.cblocks, 64 * pl.nw, small::lds_bytes(f.P, pl.xt, pl.nw), st, p);
   }
-  float *part = ws_at<float>(ws, pl.off_part);
-  uint16_t *z1 = o.Z ? o.Z : sZ, *z2 = o.Z ? sZ : nullptr;
-  TRY(rows_skinny(0, X, W->K, A, W->K, (int64_t)R * W->K, W->K, f.M, R, offs, f.E, z1, o.Z ? 1.0f : s, z2, s, part,
-                  pl.z_tail, st));
+  uint16_t *sZ = ws_at<uint16_t>(ws, pl.off_sz);
   big::Params q = big_params(mat(X, W->K), pw, W->K, mat(sZ, R), mat(B, f.r, W->N * f.r), R, f.M, W->N, offs, f.E,
                              o.out, W->N);
-  if (pl.z_tail) {
-    const TailParts tp{part, pl.zs.ranges, s, o.Z, 1.0f, nullptr, 0.0f};
+  if (pl.z_small) {
+    const TailParts tp{zpart, pl.z_splits, s, o.Z, 1.0f, nullptr, 0.0f};
     apply_tail_parts(q, &tp);
+  } else {
+    uint16_t *z1 = o.Z ? o.Z : sZ, *z2 = o.Z ? sZ : nullptr;
+    TRY(rows_skinny(0, X, W->K, A, W->K, (int64_t)R * W->K, W->K, f.M, R, offs, f.E, z1, o.Z ? 1.0f : s, z2, s, zpart,
+                    pl.z_tail, st));
+    if (pl.z_tail) {
+      const TailParts tp{zpart, pl.zs.ranges, s, o.Z, 1.0f, nullptr, 0.0f};
+      apply_tail_parts(q, &tp);
+    }
   }
   q.act = act;
   q.pre = o.pre;
@@ -267,11 +355,22 @@ lora4_status ffn_forward(const Ffn &f, int act, const uint16_t *X, const uint16_
   q.residual = o.residual;
   q.tiles_n = (int)pl.cblocks;
   q.nslots = (int)pl.slots;
-  if (pl.slots * pl.cblocks > INT32_MAX) return LORA4_ERR_SHAPE;
-  q.nblocks = (int)(pl.slots * pl.cblocks);
-  return launch_fn(f.P == 2 ? "gemm_gated" : "gemm_fused",
-                   ffn::tile_kernel(W->format, f.epi, pl.rows, pl.rows == 256 && f.E > 1), q.nblocks, fwd::THREADS,
-                   (size_t)fwd::lds_bytes(), st, q);
+  const int64_t blocks = pl.slots * pl.cblocks * pl.ksplit;
+  if (blocks > INT32_MAX) return LORA4_ERR_SHAPE;
+  q.nblocks = (int)blocks;
+  const char *name = f.P == 2 ? "gemm_gated" : "gemm_fused";
+  if (pl.split) {
+    q.ksplit = pl.ksplit;
+    q.split_steps = pl.split_steps;
+    q.Cpart = ws_at<float>(ws, pl.off_part);
+    TRY(launch_fn(name, ffn::split_kernel(W->format, f.epi, pl.rows), blocks, fwd::THREADS,
+                  (size_t)fwd::epi_lds_bytes(pl.rows, 2, true), st, q));
+    const int64_t pieces = pl.slots * pl.cblocks * 4 * pl.rows * (f.P == 2 ? 4 : 8);
+    return launch_fn("epilogue", ffn::epi_reduce_kernel(f.epi), ceil_div(pieces, 256), 256, 0, st, q, pl.rows);
+  }
+  const int nj = f.P == 2 || pl.rows == 256 ? 2 : 1;
+  return launch_fn(name, ffn::tile_kernel(W->format, f.epi, pl.rows, pl.rows == 256 && f.E > 1), blocks, fwd::THREADS,
+                   (size_t)fwd::epi_lds_bytes(pl.rows, nj, false), st, q);
 }
 
 // ---------------------------------------------------------------------------

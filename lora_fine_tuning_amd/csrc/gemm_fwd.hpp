@@ -95,9 +95,12 @@ enum Epi : int { EPI_NONE = 0, EPI_GATED = 1, EPI_FUSED = 2 };
 template <int FMT, bool SPLIT, bool SHARED, int TBM, int NJ, int EPI = EPI_NONE>
 __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const RowTile &rt, int64_t col0, int tile,
                                          int split) {
-  static_assert(!SPLIT || (TBM == BM && NJ == 2), "split partials are laid out for 256 x 256 tiles");
+  static_assert(!SPLIT || ((TBM == BM || EPI != EPI_NONE) && NJ == 2), "split partials are laid out for 256 x 256 tiles");
   constexpr int RB = TBM / 32;       // 32-row blocks: MFMA row blocks per wave, X chunks per step
-  static_assert(EPI == EPI_NONE || (!SPLIT && !SHARED), "the epilogues run on whole tiles of their own base");
+  static_assert(EPI == EPI_NONE || !SHARED, "the epilogues run on tiles of their own base");
+  // one X stage: the tiles with an epilogue take the LDS of their rows only,
+  // so that several short ones share a CU
+  constexpr int STG = EPI == EPI_NONE ? TILE : TBM * BKS;
   static_assert(EPI != EPI_GATED || NJ == 2, "a gated tile has a gate and an up block per wave");
   constexpr int WJ = EPI == EPI_GATED ? 0 : 32;     // output columns between a wave's blocks
   constexpr int WN = EPI == EPI_GATED ? 32 : 32 * NJ;   // output columns per wave
@@ -479,7 +482,7 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
   WFrag f0, f1;
   u32x4_t x[RB];
   // ring of five stages; step s uses stage s % 5
-  auto stage = [&](int i) -> uint16_t * { return smem + (i >= STAGES ? i - STAGES : i) * TILE; };
+  auto stage = [&](int i) -> uint16_t * { return smem + (i >= STAGES ? i - STAGES : i) * STG; };
 #pragma unroll
   for (int part = 0; part < 4; ++part) {
     issue_a(0, stage(0), part);
@@ -621,7 +624,21 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
 
   // ---- epilogue: register e of acc[i][j] holds
   // Y[32 i + lane % 32][64 wave + 32 j + 8 (e / 4) + 4 (lane / 32) + e % 4]
-  if constexpr (SPLIT) {
+  if constexpr (SPLIT && EPI != EPI_NONE) {
+    // fp32 partial of this range: [tile][split][wave][TBM rows][64], a wave's
+    // 64 sums of a row (gated: 32 of the gate, 32 of the up projection)
+    // together; k_epi_reduce adds them up and works the epilogue
+    float *pt = p.Cpart + ((((int64_t)tile * p.ksplit + split) * 4 + wave) * TBM) * 64;
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4)
+          *reinterpret_cast<f32x4_t *>(pt + (i * 32 + l32) * 64 + j * 32 + r4 * 8 + h * 4) =
+              f32x4_t{acc[i][j][4 * r4], acc[i][j][4 * r4 + 1], acc[i][j][4 * r4 + 2], acc[i][j][4 * r4 + 3]};
+    return;
+  } else if constexpr (SPLIT) {
     // fp32 partial of this range, tile-local [256][256] (rows and columns past
     // the output are written too and ignored by the reduction)
     float *pt = p.Cpart + ((int64_t)tile * p.ksplit + split) * (BM * BN);
@@ -804,16 +821,115 @@ template <int FMT, int EPI, int TBM, int NJ, bool SHORT>
 __global__ __launch_bounds__(THREADS, 1) void k_gemm_fwd_epi(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
   int b = blockIdx.x;
-  const int per = p.nblocks >> 3;
+  // each XCD walks a contiguous range of the tiles. Not with groups: their
+  // slots past the last tile (the grid is made for the most there can be) would
+  // leave the last XCDs idle (16 experts of 128 rows: 205 against 150 us).
+  const int per = p.offsets ? 0 : p.nblocks >> 3;
   if (b < per * 8) b = (b & 7) * per + (b >> 3);
   int slot, tn;
   big::grouped_tile(b, p.tiles_n, p.nslots, slot, tn);
-  const RowTile rt = big::tile_rows<false>(p, slot, TBM);
+  const RowTile rt = map_row_tile_wave(slot, TBM, p.offsets, p.groups, p.M);
   const int64_t col0 = (int64_t)tn * (EPI == EPI_GATED ? 128 : 128 * NJ);
   const int64_t rows = rt.row_end - rt.row0;
   if (SHORT && rows <= 64) fwd_tile<FMT, false, false, 64, NJ, EPI>(p, smem, rt, col0, b, 0);
   else if (SHORT && rows <= 128) fwd_tile<FMT, false, false, 128, NJ, EPI>(p, smem, rt, col0, b, 0);
   else fwd_tile<FMT, false, false, TBM, NJ, EPI>(p, smem, rt, col0, b, 0);
+}
+
+// LDS of an epilogue tile: its X stages, or the fp32 sums it stages (whole
+// tiles; up to 128 rows of 64 floats per wave).
+__host__ __device__ constexpr int epi_lds_bytes(int tbm, int nj, bool split) {
+  const int x = STAGES * tbm * BKS * 2, e = split ? 0 : 4 * (tbm < 128 ? tbm : 128) * 32 * nj * 4;
+  return x > e ? x : e;
+}
+
+// The same products with the reduction of every tile split over p.ksplit
+// blocks: for few rows, where the tiles alone would leave most
+// of the chip idle. Block b: range b % ksplit of tile b / ksplit.
+template <int FMT, int EPI, int TBM>
+__global__ __launch_bounds__(THREADS, 1) void k_gemm_fwd_split(Params p) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  const int tile = blockIdx.x / p.ksplit;
+  const RowTile rt = map_row_tile_wave(tile / p.tiles_n, TBM, p.offsets, p.groups, p.M);
+  fwd_tile<FMT, true, false, TBM, 2, EPI>(p, smem, rt, (int64_t)(tile % p.tiles_n) * (EPI == EPI_GATED ? 128 : 256),
+                                          tile, blockIdx.x % p.ksplit);
+}
+
+// Adds the partial sums of k_gemm_fwd_split in range order and works the
+// epilogue: 8 columns of a row per thread.
+template <int EPI>
+__global__ __launch_bounds__(256) void k_epi_reduce(Params p, int tbm) {
+  constexpr int PC = EPI == EPI_GATED ? 4 : 8;   // 8-column pieces per wave row
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int piece = (int)(idx % PC);
+  const int row = (int)(idx / PC % tbm), wave = (int)(idx / (PC * tbm) % 4);
+  const int64_t tile = idx / (PC * 4 * (int64_t)tbm);
+  if (tile >= (int64_t)p.tiles_n * p.nslots) return;
+  // (a tile is at least 256 threads' pieces: its row range is uniform here)
+  const RowTile rt = map_row_tile_wave((int)(tile / p.tiles_n), tbm, p.offsets, p.groups, p.M);
+  if (rt.group < 0) return;
+  const int64_t grow = rt.row0 + row;
+  const int64_t gcol = tile % p.tiles_n * (EPI == EPI_GATED ? 128 : 256) + wave * (8 * PC) + 8 * piece;
+  if (grow >= rt.row_end || gcol >= p.Nc) return;
+  const int64_t stride = (int64_t)4 * tbm * 64;   // one range's partials of a tile
+  const float *src = p.Cpart + tile * p.ksplit * stride + ((int64_t)wave * tbm + row) * 64 + 8 * piece;
+  constexpr int V = EPI == EPI_GATED ? 4 : 2;     // float4s per range
+  f32x4_t a[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) a[v] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < p.ksplit; k0 += 4) {
+    f32x4_t q[4][V];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k0 + u < p.ksplit)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          q[u][v] = *reinterpret_cast<const f32x4_t *>(src + (k0 + u) * stride + (v >> 1) * 32 + (v & 1) * 4);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k0 + u < p.ksplit)
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] += q[u][v];
+  }
+  const int cols = (int)min(p.Nc - gcol, (int64_t)8);
+  auto put = [&](uint16_t *dst, const float (&v)[8]) {
+    const u32x4_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7])};
+    if (cols == 8) {
+      *reinterpret_cast<u32x4_a2_t *>(dst) = w;
+    } else {
+      for (int e = 0; e < cols; ++e) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  };
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = a[e >> 2][e & 3];
+  if constexpr (EPI == EPI_GATED) {
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = a[2 + (e >> 2)][e & 3];
+    if (p.pre) {
+      put(p.pre + grow * 2 * p.Nc + gcol, v);
+      put(p.pre + grow * 2 * p.Nc + p.Nc + gcol, w);
+    }
+    act_value8(v, p.act);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= w[e];
+  } else {
+    if (p.bias) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < cols) v[e] += bf16_bits_to_f32(p.bias[rt.group * p.Nc + gcol + e]);
+    }
+    if (p.pre) put(p.pre + grow * p.ldc + gcol, v);
+    act_value8(v, p.act);
+    if (p.residual) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < cols) v[e] += bf16_bits_to_f32(p.residual[grow * p.ldc + gcol + e]);
+    }
+  }
+  put(p.C + grow * p.ldc + gcol, v);
 }
 
 // Full 256 x 256 tiles (blocks below p.nfull, in grouped tile order, each XCD

@@ -1,12 +1,13 @@
 // The base product for few tokens (single-token decoding, small serving
-// batches, experts with a handful of rows each):
+// batches, experts with a few rows each):
 //
-//   P = X deq(W)^T + (s Z) B^T for up to 16 MT tokens of a group,
+//   P = X deq(W)^T + (s Z) B^T for up to XT (4 or 8) tokens of a group,
 //   with the gated or the fused epilogue (fwd::Epi).
 //
 // Bound: reading the packed base once (about half a byte per element; at one
-// token 2 flops per element). A workgroup owns 16 columns (gated: the same 16
-// of gate and up) and all its NW waves split the reduction among them, so that
+// token 2 flops per element), and for NF4 the decode (3.5 VALU instructions
+// per element and lane). A workgroup owns 16 columns (gated: the same 16 of
+// gate and up) and all its NW waves split the reduction among them, so that
 // the base's bytes are spread over thousands of waves, each with several
 // 16-byte loads per lane in flight, and no partial sums leave the workgroup
 // (the waves' sums are joined in LDS). A wave takes chunks of 128 elements
@@ -19,7 +20,13 @@
 //    share a run, hence half an NF4 table each (big::make_table_pair);
 //  * the codes decode straight into MFMA operands: the 32 elements are four
 //    operands of v_mfma_f32_16x16x32_bf16 in the reduction order 8 kk + ..
-//    of every lane, and the tokens' X (second operand) is read in that order.
+//    of every lane;
+//  * the chunk of X, XT rows of 256 bytes, takes XT / 4 load instructions of
+//    one 16-byte piece per lane, and goes through the wave's own LDS into the
+//    operand layout. (Loading each lane's operand straight from memory takes
+//    four instructions of duplicates and 16 registers per chunk in flight;
+//    with these 4 to 8, a wave needs at most 128 registers and four of them
+//    share a SIMD.)
 //
 // PF register sets of a chunk's codes, scales and X are in flight. Token rows
 // past the group's last repeat its last row (their results are not stored).
@@ -40,7 +47,10 @@ struct Params {
   const int64_t *offsets;
   int groups;             // row groups
   int r;
-  const uint16_t *sZ;     // [M, P r] bf16, s Z
+  const float *zpart;     // [zsplits][M, P r] partial sums of Z
+  int zsplits;
+  float s;
+  uint16_t *Z;            // [M, P r] bf16 output (of the blocks of columns 0 ..), or nullptr
   const uint16_t *B;      // [groups P][N, r]
   int act;
   uint16_t *out;          // [M, N]
@@ -51,46 +61,11 @@ struct Params {
   Nf4Table tab;
 };
 
-// As map_row_tile, with the 64 lanes of a wave looking through 64 groups at a
-// time (a grid of few-token slots runs over every expert).
-__device__ __forceinline__ RowTile map_row_tile_wave(int slot, int BM, const int64_t *offsets, int groups,
-                                                     int64_t M) {
-  if (offsets == nullptr) return map_row_tile(slot, BM, nullptr, 1, M);
-  RowTile t{-1, 0, 0};
-  const int lane = threadIdx.x & 63;
-  int64_t base = 0;   // slots of the groups before e0
-  for (int e0 = 0; e0 < groups; e0 += 64) {
-    const int e = e0 + lane;
-    int64_t a = 0, b = 0;
-    if (e < groups) {
-      a = offsets[e];
-      b = offsets[e + 1];
-    }
-    const int nt = (int)((b - a + BM - 1) / BM);
-    int incl = nt;   // inclusive prefix sum over the lanes
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o);
-      if (lane >= o) incl += v;
-    }
-    const int64_t first = base + incl - nt;
-    const unsigned long long hit = __ballot(slot >= first && slot < first + nt);
-    if (hit) {
-      const int src = __ffsll(hit) - 1;
-      t.group = e0 + src;
-      const int s = __shfl((int)(slot - first), src);
-      t.row0 = __shfl((long long)a, src) + (int64_t)s * BM;
-      t.row_end = __shfl((long long)b, src);
-      return t;
-    }
-    base += __shfl(incl, 63);
-  }
-  return t;
-}
-
 // ---------------------------------------------------------------------------
-// Z = X A^T for few tokens: one workgroup per 16 tokens x 16 rank columns, its
-// 16 waves taking 32-wide chunks of the reduction in turn, joined in LDS.
+// Z = X A^T for few tokens: one workgroup per 16 tokens x 16 rank columns x
+// one of `splits` ranges of the reduction, its four waves taking 32-wide chunks
+// in turn, joined in LDS. The consumer adds the ranges' fp32 sums up, so a long
+// reduction costs one pass of loads instead of many in a row.
 // ---------------------------------------------------------------------------
 
 struct ZParams {
@@ -98,52 +73,42 @@ struct ZParams {
   const uint16_t *A;      // [groups][R, K]
   int64_t M, K;
   int R;                  // rank columns (P r)
-  float s;
   const int64_t *offsets;
   int groups;
-  uint16_t *sZ;           // [M, R] bf16(s Z)
-  uint16_t *Z;            // [M, R] bf16(Z) or nullptr
-  int jblocks;            // blocks of 16 rank columns; block b: slot b / jblocks
+  float *part;            // [splits][M, R]
+  int jblocks, splits;    // block b: range b % splits, rank block b / splits % jblocks, then the slot
+  int64_t per;            // chunks per range
 };
 
-constexpr int Z_WAVES = 16;
+constexpr int Z_WAVES = 4;
+constexpr int Z_CHUNKS = 8;   // chunks a wave has in flight
 
 static __global__ __launch_bounds__(64 * Z_WAVES) void k_small_z(ZParams p) {
   __shared__ f32x4_t red[Z_WAVES][64];
-  const RowTile rt = map_row_tile_wave(blockIdx.x / p.jblocks, 16, p.offsets, p.groups, p.M);
+  const int split = blockIdx.x % p.splits, rest = blockIdx.x / p.splits;
+  const RowTile rt = map_row_tile_wave(rest / p.jblocks, 16, p.offsets, p.groups, p.M);
   if (rt.group < 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane & 15, q = lane >> 4;
-  const int j0 = (blockIdx.x % p.jblocks) * 16;
+  const int j0 = (rest % p.jblocks) * 16;
   const int64_t last = min(rt.row0 + 16, rt.row_end) - 1;
   const int64_t tok = min(rt.row0 + lr, last);
   const uint16_t *x = p.X + tok * p.K + 8 * q;
   const uint16_t *a = p.A + ((int64_t)rt.group * p.R + min(j0 + lr, p.R - 1)) * p.K + 8 * q;
-  const int64_t chunks = p.K >> 5;   // (K % 32 == 0)
+  const int64_t all = p.K >> 5;   // (K % 32 == 0)
+  const int64_t end = min((split + 1) * p.per, all);
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  constexpr int U = 8;
-  int64_t c = wave;
-  for (; c + (U - 1) * Z_WAVES < chunks; c += U * Z_WAVES) {
-    u32x4_t av[U], xv[U];
+  for (int64_t c = split * p.per + wave; c < end; c += Z_CHUNKS * Z_WAVES) {
+    u32x4_t av[Z_CHUNKS], xv[Z_CHUNKS];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      av[u] = *reinterpret_cast<const u32x4_t *>(a + (c + u * Z_WAVES) * 32);
-      xv[u] = *reinterpret_cast<const u32x4_t *>(x + (c + u * Z_WAVES) * 32);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) acc = mfma_16x16x32(av[u], xv[u], acc);
-  }
-  {
-    u32x4_t av[U], xv[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c + u * Z_WAVES < chunks) {
+    for (int u = 0; u < Z_CHUNKS; ++u)
+      if (c + u * Z_WAVES < end) {
         av[u] = *reinterpret_cast<const u32x4_t *>(a + (c + u * Z_WAVES) * 32);
         xv[u] = *reinterpret_cast<const u32x4_t *>(x + (c + u * Z_WAVES) * 32);
       }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c + u * Z_WAVES < chunks) acc = mfma_16x16x32(av[u], xv[u], acc);
+    for (int u = 0; u < Z_CHUNKS; ++u)
+      if (c + u * Z_WAVES < end) acc = mfma_16x16x32(av[u], xv[u], acc);
   }
   red[wave][lane] = acc;
   __syncthreads();
@@ -153,14 +118,10 @@ static __global__ __launch_bounds__(64 * Z_WAVES) void k_small_z(ZParams p) {
     for (int w = 1; w < Z_WAVES; ++w) z += red[w][lane];
     // lane: rank columns j0 + 4 q + e of token lr
     if (rt.row0 + lr <= last) {
+      float *dst = p.part + ((int64_t)split * p.M + rt.row0 + lr) * p.R;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + 4 * q + e;
-        if (j < p.R) {
-          p.sZ[(rt.row0 + lr) * p.R + j] = to_bf16(z[e] * p.s);
-          if (p.Z) p.Z[(rt.row0 + lr) * p.R + j] = to_bf16(z[e]);
-        }
-      }
+      for (int e = 0; e < 4; ++e)
+        if (j0 + 4 * q + e < p.R) dst[j0 + 4 * q + e] = z[e];
     }
   }
 }
@@ -169,20 +130,27 @@ static __global__ __launch_bounds__(64 * Z_WAVES) void k_small_z(ZParams p) {
 // The base product
 // ---------------------------------------------------------------------------
 
-__host__ __device__ constexpr int lds_bytes(int P, int MT, int NW) { return NW * P * MT * 64 * 16; }
+__host__ __device__ constexpr int lds_bytes(int P, int XT, int NW) { return NW * (P * 64 * 16 + XT * 256); }
 
-template <int FMT, int EPI, int MT, int NW>
-__global__ __launch_bounds__(64 * NW) void k_small(Params p) {
+template <int FMT, int EPI, int XT, int NW>
+__global__ __launch_bounds__(64 * NW, 4) void k_small(Params p) {
   constexpr int P = EPI == fwd::EPI_GATED ? 2 : 1;
-  constexpr int PF = MT == 1 ? 4 : MT == 2 ? 3 : 2;   // chunks in flight
-  extern __shared__ __attribute__((aligned(16))) f32x4_t red[];   // [NW][P][MT][64]
-  const RowTile rt = map_row_tile_wave(blockIdx.x / p.nblocks, 16 * MT, p.offsets, p.groups, p.M);
+    constexpr int PF = P == 2 ? 3 : 4;   // chunks in flight (one more or fewer: within 3%)
+  constexpr int XL = XT / 4;   // X loads per chunk
+  extern __shared__ __attribute__((aligned(16))) f32x4_t lds[];   // [NW][P][64] sums, then [NW][XT][16] X pieces
+  // Blocks go to the XCDs in turn: the four column blocks of one 64-row block
+  // of the storage are taken by blocks of one XCD, so that the lines of scales
+  // they share (and the codes' memory pages) are fetched by one L2.
+  int b = blockIdx.x;
+  const int whole = (int)(gridDim.x & ~31u);
+  if (b < whole) b = (b & ~31) + ((b & 7) << 2) + ((b >> 3) & 3);
+  const RowTile rt = map_row_tile_wave(b / p.nblocks, XT, p.offsets, p.groups, p.M);
   if (rt.group < 0) return;
   const int g = rt.group;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int lr = lane & 15, q = lane >> 4;
-  const int64_t n0 = (int64_t)(blockIdx.x % p.nblocks) * 16;
-  const int rows = (int)min(rt.row_end - rt.row0, (int64_t)16 * MT);
+  const int64_t n0 = (int64_t)(b % p.nblocks) * 16;
+  const int rows = (int)min(rt.row_end - rt.row0, (int64_t)XT);
   const int64_t KB = p.W.KB;
   const int K = (int)p.K;
 
@@ -213,14 +181,25 @@ __global__ __launch_bounds__(64 * NW) void k_small(Params p) {
 
   // ---- tokens -----------------------------------------------------------------
   const rsrc_t x_rs = big::make_rsrc(p.X + rt.row0 * p.K, big::clamp_bytes((int64_t)rows * p.K * 2));
-  uint32_t x_off[MT];
+  // piece (kk, token, q) of the chunk is the 16 bytes at element 64 (q % 2) +
+  // 32 (q / 2) + 8 kk of the token: load u of lane l takes piece number
+  // 64 u + l = (kk XT + token) 4 + q, and so it lies in LDS
+  uint32_t x_off[XL];
+  int x_k[XL];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) x_off[m] = (uint32_t)((min(16 * m + lr, rows - 1) * p.K + k_lane) * 2);
+  for (int u = 0; u < XL; ++u) {
+    const int id = 64 * u + lane, pq = id & 3, tok = (id >> 2) % XT, kk = id / (4 * XT);
+    x_k[u] = 64 * (pq & 1) + 32 * (pq >> 1) + 8 * kk;
+    x_off[u] = (uint32_t)((min(tok, rows - 1) * p.K + x_k[u]) * 2);
+  }
+  f32x4_t *red = lds;
+  u32x4_t *xs = reinterpret_cast<u32x4_t *>(lds + NW * P * 64) + wave * (XT * 16);
+  const u32x4_t *x_rd = xs + (lr < XT ? lr : XT - 1) * 4 + q;   // operand kk at x_rd[kk * 4 XT]
 
   struct Set {
     u32x4_t c[P];
     uint32_t sc[P], c2[P];
-    u32x4_t x[MT][4];
+    u32x4_t x[XL];
   };
   // (a lane whose 32 elements lie past K loads zeros, base and tokens)
   auto load = [&](Set &s, int chunk) {
@@ -242,24 +221,26 @@ __global__ __launch_bounds__(64 * NW) void k_small(Params p) {
             s2_rs[j], in ? (uint32_t)(((s2_row + 2 * chunk) >> 8) * 4) : OOB, 0, 0);
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        s.x[m][kk] = __builtin_bit_cast(
-            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(x_rs, in ? x_off[m] + 16 * kk : OOB, chunk * 256, 0));
+    for (int u = 0; u < XL; ++u)
+      s.x[u] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                               x_rs, chunk * 128 + x_k[u] < K ? x_off[u] : OOB, chunk * 256, 0));
   };
 
   const uint32_t sel = big::sel_base();
   float qh[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) qh[i] = (lane >> 5) ? p.tab.q[8 + i] : p.tab.q[i];
-  f32x4_t acc[P][MT];
+  f32x4_t acc[P];
 #pragma unroll
-  for (int j = 0; j < P; ++j)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[j][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < P; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   auto compute = [&](const Set &s) {
+    // (a wave's LDS accesses run in order: the last chunk's reads are done)
+#pragma unroll
+    for (int u = 0; u < XL; ++u) xs[64 * u + lane] = s.x[u];
+    u32x4_t x[4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) x[kk] = x_rd[kk * 4 * XT];
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       u32x4_t w[4];
@@ -280,69 +261,104 @@ __global__ __launch_bounds__(64 * NW) void k_small(Params p) {
         for (int kk = 0; kk < 4; ++kk) w[kk] = big::decode8_nf4(T, s.c[j][kk]);
       }
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[j][m] = mfma_16x16x32(w[kk], s.x[m][kk], acc[j][m]);
+      for (int kk = 0; kk < 4; ++kk) acc[j] = mfma_16x16x32(w[kk], x[kk], acc[j]);
     }
   };
+
+  // ---- rank-r product: 32 rank columns per step, the steps dealt to the waves.
+  // (Before the base's loads are issued: among them it costs 30 registers
+  // more than there are, and its own latency is hidden by the other waves.)
+  for (int j0 = 32 * wave; j0 < p.r; j0 += 32 * NW) {
+    const int jr = j0 + 8 * q;
+    const bool vec = (p.r & 7) == 0;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int64_t n = n0 + lr;
+      u32x4_t b = {0u, 0u, 0u, 0u};
+      if (n < p.N && jr < p.r) {
+        const uint16_t *src = p.B + (((int64_t)g * P + j) * p.N + n) * p.r + jr;
+        if (vec) {
+          b = *reinterpret_cast<const u32x4_t *>(src);
+        } else {
+          for (int e = 0; e < 8; ++e)
+            if (jr + e < p.r) b[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+        }
+      }
+      // eight columns of this lane's token: the ranges added up in order
+      const int64_t row = rt.row0 + min(lr, rows - 1);
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = 0.0f;
+      if (jr < p.r) {
+        const float *src = p.zpart + row * (P * p.r) + j * p.r + jr;
+        const int64_t stride = p.M * (P * p.r);
+        if (vec) {
+#pragma unroll 4
+          for (int k = 0; k < p.zsplits; ++k) {
+            const f32x4_t lo = *reinterpret_cast<const f32x4_t *>(src + k * stride);
+            const f32x4_t hi = *reinterpret_cast<const f32x4_t *>(src + k * stride + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              z[e] += lo[e];
+              z[4 + e] += hi[e];
+            }
+          }
+        } else {
+          for (int k = 0; k < p.zsplits; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (jr + e < p.r) z[e] += src[k * stride + e];
+        }
+        if (p.Z && n0 == 0 && lr < rows) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (jr + e < p.r) p.Z[row * (P * p.r) + j * p.r + jr + e] = to_bf16(z[e]);
+        }
+      }
+      acc[j] = mfma_16x16x32(b, big::pack_scaled8(z, p.s), acc[j]);
+    }
+  }
+  asm volatile("" ::: "memory");
 
   const int chunks = (K + 127) >> 7;
   const int n_own = chunks > wave ? (chunks - wave + NW - 1) / NW : 0;   // chunks wave, wave + NW, ..
   Set set[PF];
 #pragma unroll
-  for (int u = 0; u < PF; ++u) load(set[u], wave + u * NW);
-  for (int i = 0; i < n_own; i += PF) {
+  for (int u = 0; u < PF; ++u) {
+    load(set[u], wave + u * NW);
+    __builtin_amdgcn_sched_barrier(0);   // (the waits count loads in this order)
+  }
+  // (the groups of PF chunks run without conditions, so that every wait in
+  // them counts exactly the loads behind it; loads past the last chunk are out
+  // of range and return zeros)
+  int i = 0;
+  for (; i + PF <= n_own; i += PF) {
 #pragma unroll
     for (int u = 0; u < PF; ++u) {
-      if (i + u < n_own) {
-        compute(set[u]);
-        load(set[u], wave + (i + u + PF) * NW);
-      }
+      compute(set[u]);
+      load(set[u], wave + (i + u + PF) * NW);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+#pragma unroll
+  for (int u = 0; u < PF; ++u)
+    if (i + u < n_own) compute(set[u]);
 
-  // ---- rank-r product, 32 rank columns per step, the steps dealt to the waves
-  for (int j0 = 32 * wave; j0 < p.r; j0 += 32 * NW) {
-    const int jr = j0 + 8 * q;
-    const bool vec = (p.r & 7) == 0;
-    auto rank8 = [&](const uint16_t *src, bool ok) -> u32x4_t {   // src[0 .. 7], zero past r
-      uint32_t w4[4] = {0u, 0u, 0u, 0u};
-      if (ok && jr < p.r) {
-        if (vec) return *reinterpret_cast<const u32x4_t *>(src);
-        for (int e = 0; e < 8; ++e)
-          if (jr + e < p.r) w4[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
-      }
-      return u32x4_t{w4[0], w4[1], w4[2], w4[3]};
-    };
+  // ---- join the waves; a thread has 4 consecutive columns of one token ---------
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const int64_t n = n0 + lr;
-      const u32x4_t b = rank8(p.B + (((int64_t)g * P + j) * p.N + n) * p.r + jr, n < p.N);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int64_t row = rt.row0 + min(16 * m + lr, rows - 1);
-        acc[j][m] = mfma_16x16x32(b, rank8(p.sZ + row * (P * p.r) + j * p.r + jr, true), acc[j][m]);
-      }
-    }
-  }
-
-  // ---- join the waves; each item is 4 consecutive columns of one token --------
-#pragma unroll
-  for (int j = 0; j < P; ++j)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) red[((wave * P + j) * MT + m) * 64 + lane] = acc[j][m];
+  for (int j = 0; j < P; ++j) red[(wave * P + j) * 64 + lane] = acc[j];
   __syncthreads();
-  for (int it = threadIdx.x; it < MT * 64; it += 64 * NW) {
+  if (threadIdx.x < 64) {
     f32x4_t v[P];
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      v[j] = red[j * MT * 64 + it];
+      v[j] = red[j * 64 + lane];
 #pragma unroll
-      for (int w = 1; w < NW; ++w) v[j] += red[(w * P + j) * MT * 64 + it];
+      for (int w = 1; w < NW; ++w) v[j] += red[(w * P + j) * 64 + lane];
     }
-    const int tok = 16 * (it >> 6) + (it & 15);
-    const int64_t n = n0 + 4 * ((it >> 4) & 3);
-    if (tok >= rows || n >= p.N) continue;
+    const int tok = lr;
+    const int64_t n = n0 + 4 * q;
+    if (tok >= rows || n >= p.N) return;
     const int64_t row = rt.row0 + tok;
     const bool vec = (p.N & 3) == 0;   // then the four columns are whole and 8-byte aligned
     auto put = [&](uint16_t *dst, const float (&o)[4]) {

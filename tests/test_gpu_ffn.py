@@ -237,9 +237,10 @@ def check_epilogue(c, act, bias, res, o):
         compare_full("P", to_host(o["P"]), P, IP)
 
 
-# the schedules: the library's own choice, the few-token kernel with 16, 32 and
-# 64 tokens per slot, tiles of 64, 128 and 256 rows
-POLICIES = ["", "16", "32", "64", "1064", "1128", "1256"]
+# the schedules: the library's own choice, the few-token kernel with 4 and 8
+# tokens per slot, tiles of 64, 128 and 256 rows, whole, and of 32, 64 and 128
+# rows with their reduction split
+POLICIES = ["", "4", "8", "1064", "1128", "1256", "2032", "2064", "2128"]
 SHAPES = [(1, 256, 96, 16), (5, 320, 200, 8), (17, 512, 257, 4), (64, 1024, 64, 1), (130, 640, 384, 24),
           (300, 192, 515, 128)]
 MX_SHAPES = [(1, 96, 33, 3), (40, 352, 131, 12)]    # K % 64 == 32, odd N and r
@@ -250,7 +251,7 @@ def _shapes(fmt):
 
 
 GRID = [(fmt, shape, pol) for fmt in FMTS for shape in _shapes(fmt) for pol in POLICIES
-        if not (pol in ("16", "32") and shape[0] > 130)]
+        if not (pol in ("4", "8") and shape[0] > 130)]
 
 
 @pytest.mark.parametrize("fmt,shape,policy", GRID)

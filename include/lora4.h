@@ -380,7 +380,8 @@ typedef enum {
 
 /* RMS norm: h = X + R (h = X if R is NULL), Y = h rstd weight with
  * rstd = 1 / sqrt(mean(h^2) + eps) of each row.
- *  X, R    : bf16 [M, D]; R may be NULL. 1 <= D <= 16384, any D.
+ *  X, R    : bf16 [M, D]; R may be NULL. 1 <= D <= 16384 (16376 unless a
+ *            multiple of 8).
  *  weight  : bf16 [D]. eps: finite, >= 0.
  *  H       : bf16 [M, D] output bf16(h), may be NULL (must be without R). May
  *            be X or R itself; no other overlap is allowed.

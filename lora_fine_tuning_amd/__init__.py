@@ -694,17 +694,55 @@ def loftq_init(W, r, iters=5, s=1.0, double_quant=False):
 # with an epilogue
 # ---------------------------------------------------------------------------
 
+class _NoGuard:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        return None
+
+
+_NO_GUARD = _NoGuard()
+
+
 def _on_device(dev):
-    """The device's current stream, with the device made current for the call
-    (kernels launch on the current device). Returns (stream, guard)."""
-    import contextlib
+    """The device's current stream (a handle), and a guard that makes the device
+    current for the call (kernels launch on the current device)."""
     import torch
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {dev}")
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        return stream, contextlib.nullcontext()
-    return stream, torch.cuda.device(dev)
+    # the handle without the Stream object around it: 0.1 us of 2
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    stream = raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+    return stream, _NO_GUARD if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _like(t, ref):
+    """The caller's output t, or a new tensor like ref."""
+    import torch
+    return torch.empty_like(ref) if t is None else t
+
+
+def _bf16_on(t, name, shape, dev):
+    """_need for a bf16 tensor, with one test where nothing is wrong."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and t.is_contiguous()
+            and t.device == dev):
+        _need(t, name, shape, torch.bfloat16, dev)
+
+
+def _given(ws, dev):
+    """Checks a caller's workspace tensor; whether it is large enough the
+    library says (LORA4_ERR_WORKSPACE)."""
+    import torch
+    if ws.dtype is not torch.uint8 or ws.dim() != 1 or not ws.is_contiguous() or ws.device != dev:
+        raise ValueError("workspace must be a contiguous 1-D uint8 tensor on the layer's device")
+
+
+def _check_ws_status(st, what):
+    if st == -5:
+        raise ValueError(f"{what}: the workspace is too small")
+    _check(st, what)
 
 
 def _workspace(n, what, dev):
@@ -721,12 +759,11 @@ def _activation(name):
 
 
 def _check_norm(X, weight, name="X"):
-    import torch
     if X is None or X.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor [M, D]")
     M, D = X.shape
-    _need(X, name, (M, D), torch.bfloat16)
-    _need(weight, "weight", (D,), torch.bfloat16, X.device)
+    _bf16_on(X, name, (M, D), X.device)
+    _bf16_on(weight, "weight", (D,), X.device)
     return M, D
 
 
@@ -742,20 +779,21 @@ def rmsnorm(X, weight, eps, residual=None, mx=False, want_y=True, out=None):
     M, D = _check_norm(X, weight)
     dev = X.device
     if residual is not None:
-        _need(residual, "residual", (M, D), torch.bfloat16, dev)
+        _bf16_on(residual, "residual", (M, D), dev)
     elif out.get("H") is not None:
         raise ValueError("H is only an output with a residual")
-    for name, shape, dtype in (("Y", (M, D), torch.bfloat16), ("H", (M, D), torch.bfloat16),
-                               ("codes", (M, D), torch.uint8), ("scales", (M, D // 32), torch.uint8)):
-        if out.get(name) is not None:
-            _need(out[name], name, shape, dtype, dev)
+    if out:
+        for name, shape, dtype in (("Y", (M, D), torch.bfloat16), ("H", (M, D), torch.bfloat16),
+                                   ("codes", (M, D), torch.uint8), ("scales", (M, D // 32), torch.uint8)):
+            if out.get(name) is not None:
+                _need(out[name], name, shape, dtype, dev)
     mx = mx or out.get("codes") is not None or out.get("scales") is not None
     if mx and D % 32 != 0:
         raise ValueError("the MXFP8 output needs D % 32 == 0")
     if not want_y and not mx:
         raise ValueError("nothing to compute: want_y or mx")
-    Y = _out(out.get("Y"), (M, D), dev) if want_y or out.get("Y") is not None else None
-    H = _out(out.get("H"), (M, D), dev) if residual is not None else None
+    Y = _like(out.get("Y"), X) if want_y or out.get("Y") is not None else None
+    H = _like(out.get("H"), X) if residual is not None else None
     codes = scales = None
     if mx:
         codes, scales = out.get("codes"), out.get("scales")
@@ -785,24 +823,23 @@ def rmsnorm_backward(dY, H, weight, eps, dH=None, want_dw=True, workspace=None, 
     out = out or {}
     M, D = _check_norm(H, weight, "H")
     dev, bf = H.device, torch.bfloat16
-    _need(dY, "dY", (M, D), bf, dev)
+    _bf16_on(dY, "dY", (M, D), dev)
     if dH is not None:
-        _need(dH, "dH", (M, D), bf, dev)
+        _bf16_on(dH, "dH", (M, D), dev)
     for name, shape in (("dX", (M, D)), ("dW", (D,))):
         if out.get(name) is not None:
             _need(out[name], name, shape, bf, dev)
-    dX = _out(out.get("dX"), (M, D), dev)
-    dW = _out(out.get("dW"), (D,), dev) if want_dw or out.get("dW") is not None else None
-    if dW is not None:
-        need = lora4_rmsnorm_workspace_bytes(M, D)
-        if workspace is None:
-            workspace = _workspace(need, "lora4_rmsnorm_workspace_bytes", dev)
-        _check_workspace(workspace, need, dev)
+    dX = _like(out.get("dX"), H)
+    dW = _like(out.get("dW"), weight) if want_dw or out.get("dW") is not None else None
     stream, guard = _on_device(dev)
     with guard:
+        if workspace is not None:
+            _given(workspace, dev)
+        elif dW is not None:
+            workspace = _workspace(lora4_rmsnorm_workspace_bytes(M, D), "lora4_rmsnorm_workspace_bytes", dev)
         st = lora4_rmsnorm_backward(_ptr(dY), _ptr(H), _ptr(weight), _ptr(dH), M, D, float(eps), _ptr(dX), _ptr(dW),
                                     _ptr(workspace), 0 if workspace is None else workspace.numel(), stream)
-    _check(st, "lora4_rmsnorm_backward")
+    _check_ws_status(st, "lora4_rmsnorm_backward")
     return {"dX": dX, "dW": dW}
 
 
@@ -815,21 +852,58 @@ def check_gated_args(base, X, A, B, offsets=None, tensors=()):
     import torch
     if base.groups % 2 != 0:
         raise ValueError("a gated base has two groups per expert: the gate's, then the up projection's")
-    if A is None or A.dim() != 3:
+    if not isinstance(A, torch.Tensor) or A.dim() != 3:
         raise ValueError(f"A must be [{base.groups}, r, K]")
-    M, r, _ = check_layer_args(PackedBase(base.fmt, base.N, base.K, 1, base.codes, base.scales, base.scales2), X,
-                               A[0], B[0] if B is not None and B.dim() == 3 else B)
-    bf, dev, E = torch.bfloat16, X.device, base.groups // 2
-    _need(A, "A", (2 * E, r, base.K), bf, dev)
-    _need(B, "B", (2 * E, base.N, r), bf, dev)
-    if E > 1:
-        _need(offsets, "group offsets", (E + 1,), torch.int64, dev)
-    elif offsets is not None:
-        raise ValueError("group offsets are only taken with several experts")
+    E, N = base.groups // 2, base.N
+    M, r = _check_x(base, X), A.shape[1]
+    dev = X.device
+    _bf16_on(A, "A", (2 * E, r, base.K), dev)
+    _bf16_on(B, "B", (2 * E, N, r), dev)
+    _check_offsets(offsets, E, dev)
     for name, t, shape in tensors:
         if t is not None:
-            _need(t, name, shape, bf, dev)
+            _bf16_on(t, name, shape, dev)
     return M, r, E
+
+
+def _check_x(base, X):
+    """M of X [M, K], with the base on X's device."""
+    import torch
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be a 2-D tensor [M, K]")
+    M, dev = X.shape[0], X.device
+    _bf16_on(X, "X", (M, base.K), dev)
+    for t in (base.codes, base.scales, base.scales2):
+        if t is not None and (t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"the base's tensors must be contiguous on {dev}")
+    return M
+
+
+def _check_offsets(offsets, groups, dev):
+    import torch
+    if groups > 1:
+        _need(offsets, "group offsets", (groups + 1,), torch.int64, dev)
+    elif offsets is not None:
+        raise ValueError("group offsets are only taken with several groups")
+
+
+def _check_linear(base, X, A, B, offsets, tensors):
+    """Validates the tensors of a linear with an epilogue; `tensors`: (name,
+    tensor, shape) triples that may be None. Returns (M, r)."""
+    import torch
+    G = base.groups
+    if not isinstance(A, torch.Tensor) or A.dim() not in (2, 3) or (A.dim() == 2 and G != 1):
+        raise ValueError(f"A must be [r, K] or [groups={G}, r, K]")
+    M, r = _check_x(base, X), A.shape[-2]
+    dev = X.device
+    lead = () if A.dim() == 2 else (G,)
+    _bf16_on(A, "A", lead + (r, base.K), dev)
+    _bf16_on(B, "B", lead + (base.N, r), dev)
+    _check_offsets(offsets, G, dev)
+    for name, t, shape in tensors:
+        if t is not None:
+            _bf16_on(t, name, shape, dev)
+    return M, r
 
 
 def gated_workspace(which, base, M, r):
@@ -856,13 +930,13 @@ def gated_forward(base, X, A, B, s, activation="silu", group_offsets=None, want_
     W = base.abi()
     stream, guard = _on_device(dev)
     with guard:
-        need = lora4_gated_workspace_bytes(0, W, M, r)
-        if workspace is None or need == 0:
-            workspace = _workspace(need, "lora4_gated_workspace_bytes", dev)
-        _check_workspace(workspace, need, dev)
+        if workspace is None:
+            workspace = _workspace(lora4_gated_workspace_bytes(0, W, M, r), "lora4_gated_workspace_bytes", dev)
+        else:
+            _given(workspace, dev)
         st = lora4_gated_forward(W, act, _ptr(X), M, _ptr(A), _ptr(B), r, float(s), _ptr(group_offsets), _ptr(H),
                                  _ptr(GU), _ptr(Z), _ptr(workspace), workspace.numel(), stream)
-    _check(st, "lora4_gated_forward")
+    _check_ws_status(st, "lora4_gated_forward")
     return {"H": H, "GU": GU, "Z": Z}
 
 
@@ -886,14 +960,14 @@ def gated_backward(base, X, dH, GU, A, B, s, activation="silu", Z=None, group_of
     W = base.abi()
     stream, guard = _on_device(dev)
     with guard:
-        need = lora4_gated_workspace_bytes(1, W, M, r)
-        if workspace is None or need == 0:
-            workspace = _workspace(need, "lora4_gated_workspace_bytes", dev)
-        _check_workspace(workspace, need, dev)
+        if workspace is None:
+            workspace = _workspace(lora4_gated_workspace_bytes(1, W, M, r), "lora4_gated_workspace_bytes", dev)
+        else:
+            _given(workspace, dev)
         st = lora4_gated_backward(W, act, _ptr(X), _ptr(dH), _ptr(GU), M, _ptr(A), _ptr(B), r, float(s),
                                   _ptr(group_offsets), _ptr(Z), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(workspace),
                                   workspace.numel(), stream)
-    _check(st, "lora4_gated_backward")
+    _check_ws_status(st, "lora4_gated_backward")
     return {"dX": dX, "dA": dA, "dB": dB}
 
 
@@ -918,7 +992,7 @@ def forward_epilogue(base, X, A, B, s, bias=None, activation="none", residual=No
     act = _activation(activation)
     M, N = (X.shape[0], base.N) if X is not None and X.dim() == 2 else (0, base.N)
     r = A.shape[-2] if A is not None and A.dim() >= 2 else 0
-    M, r, _ = check_layer_args(base, X, A, B, offsets=group_offsets, outputs=[
+    M, r = _check_linear(base, X, A, B, group_offsets, [
         ("Y", out.get("Y"), (M, N)), ("P", out.get("P"), (M, N)), ("Z", out.get("Z"), (M, r)),
         ("residual", residual, (M, N)), ("bias", bias, _bias_shape(base))])
     dev = X.device
@@ -928,14 +1002,14 @@ def forward_epilogue(base, X, A, B, s, bias=None, activation="none", residual=No
     W = base.abi()
     stream, guard = _on_device(dev)
     with guard:
-        need = lora4_epilogue_workspace_bytes(0, W, M, r)
-        if workspace is None or need == 0:
-            workspace = _workspace(need, "lora4_epilogue_workspace_bytes", dev)
-        _check_workspace(workspace, need, dev)
+        if workspace is None:
+            workspace = _workspace(lora4_epilogue_workspace_bytes(0, W, M, r), "lora4_epilogue_workspace_bytes", dev)
+        else:
+            _given(workspace, dev)
         st = lora4_forward_epilogue(W, act, _ptr(X), M, _ptr(A), _ptr(B), r, float(s), _ptr(group_offsets),
                                     _ptr(bias), _ptr(residual), _ptr(Y), _ptr(P), _ptr(Z), _ptr(workspace),
                                     workspace.numel(), stream)
-    _check(st, "lora4_forward_epilogue")
+    _check_ws_status(st, "lora4_forward_epilogue")
     return {"Y": Y, "P": P, "Z": Z}
 
 
@@ -952,8 +1026,9 @@ def backward_epilogue(base, X, dY, A, B, s, P=None, activation="none", Z=None, w
     M, N = (X.shape[0], base.N) if X is not None and X.dim() == 2 else (0, base.N)
     if dY is None:
         raise ValueError("dY is required")
-    M, r, _ = check_layer_args(base, X, A, B, dY=dY, Z=Z, offsets=group_offsets, outputs=[
-        ("P", P, (M, N)), ("dX", out.get("dX"), (M, base.K)),
+    r = A.shape[-2] if A is not None and A.dim() >= 2 else 0
+    M, r = _check_linear(base, X, A, B, group_offsets, [
+        ("dY", dY, (M, N)), ("Z", Z, (M, r)), ("P", P, (M, N)), ("dX", out.get("dX"), (M, base.K)),
         ("dA", out.get("dA"), None if A is None else tuple(A.shape)),
         ("dB", out.get("dB"), None if B is None else tuple(B.shape)), ("dbias", out.get("dbias"), _bias_shape(base))])
     dev = X.device
@@ -965,12 +1040,12 @@ def backward_epilogue(base, X, dY, A, B, s, P=None, activation="none", Z=None, w
     W = base.abi()
     stream, guard = _on_device(dev)
     with guard:
-        need = lora4_epilogue_workspace_bytes(1, W, M, r)
-        if workspace is None or need == 0:
-            workspace = _workspace(need, "lora4_epilogue_workspace_bytes", dev)
-        _check_workspace(workspace, need, dev)
+        if workspace is None:
+            workspace = _workspace(lora4_epilogue_workspace_bytes(1, W, M, r), "lora4_epilogue_workspace_bytes", dev)
+        else:
+            _given(workspace, dev)
         st = lora4_backward_epilogue(W, act, _ptr(X), _ptr(dY), _ptr(P), M, _ptr(A), _ptr(B), r, float(s),
                                      _ptr(group_offsets), _ptr(Z), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(dbias),
                                      _ptr(workspace), workspace.numel(), stream)
-    _check(st, "lora4_backward_epilogue")
+    _check_ws_status(st, "lora4_backward_epilogue")
     return {"dX": dX, "dA": dA, "dB": dB, "dbias": dbias}

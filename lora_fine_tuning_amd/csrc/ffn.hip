@@ -16,9 +16,13 @@ const void *norm_fwd(bool mx) {
   return mx ? addr(norm::k_rmsnorm_fwd<WAVE, VPT, true>) : addr(norm::k_rmsnorm_fwd<WAVE, VPT, false>);
 }
 
-template <bool WAVE, int VPT>
-const void *norm_bwd(bool dw) {
-  return dw ? addr(norm::k_rmsnorm_bwd<WAVE, VPT, true>) : addr(norm::k_rmsnorm_bwd<WAVE, VPT, false>);
+template <bool WAVE, int VPT, int MAXW>
+const void *norm_bwd(bool dw, bool edge) {
+  if (edge)
+    return dw ? addr(norm::k_rmsnorm_bwd<WAVE, VPT, true, MAXW, true>)
+              : addr(norm::k_rmsnorm_bwd<WAVE, VPT, false, MAXW, true>);
+  return dw ? addr(norm::k_rmsnorm_bwd<WAVE, VPT, true, MAXW, false>)
+            : addr(norm::k_rmsnorm_bwd<WAVE, VPT, false, MAXW, false>);
 }
 
 template <int FMT, int EPI>
@@ -67,7 +71,8 @@ const void *small_of(int epi, int xt, int nw) {
 // One wave per row up to 1024 elements; above, a block of as many waves as
 // hold the row at two vectors per thread.
 NormShape norm_shape(int D) {
-  const int nv = (D + 7) / 8;
+  // (the backward's aligned vectors of a row: one more where rows are unaligned)
+  const int nv = D % 8 == 0 ? D / 8 : (D + 14) / 8;
   if (nv <= 128) return {64, nv <= 64 ? 1 : 2};
   return {64 * ((nv + 127) / 128), 2};
 }
@@ -77,9 +82,11 @@ const void *norm_fwd_kernel(NormShape s, bool mx) {
   return norm_fwd<false, 2>(mx);
 }
 
-const void *norm_bwd_kernel(NormShape s, bool dw) {
-  if (s.threads == 64) return s.vpt == 1 ? norm_bwd<true, 1>(dw) : norm_bwd<true, 2>(dw);
-  return norm_bwd<false, 2>(dw);
+const void *norm_bwd_kernel(NormShape s, bool dw, bool edge) {
+  if (s.threads == 64) return s.vpt == 1 ? norm_bwd<true, 1, 4>(dw, edge) : norm_bwd<true, 2, 4>(dw, edge);
+  return s.threads <= 256   ? norm_bwd<false, 2, 4>(dw, edge)
+         : s.threads <= 512 ? norm_bwd<false, 2, 8>(dw, edge)
+                            : norm_bwd<false, 2, 16>(dw, edge);
 }
 
 const void *col_sum_kernel() { return addr(norm::k_col_sum); }
@@ -117,16 +124,35 @@ const void *small_kernel(int fmt, int epi, int xt, int nw) {
 
 const void *small_z_kernel() { return addr(small::k_small_z); }
 
-const void *gated_bwd_kernel(int tj) {
+const void *act_dz_kernel(int projections, int tj) {
+  if (projections == 2) {
+    switch (tj) {
+      case 1: return addr(actbwd::k_act_dz<2, 1>);
+      case 2: return addr(actbwd::k_act_dz<2, 2>);
+      case 4: return addr(actbwd::k_act_dz<2, 4>);
+      default: return addr(actbwd::k_act_dz<2, 8>);
+    }
+  }
   switch (tj) {
-    case 1: return addr(actbwd::k_gated_bwd<1>);
-    case 2: return addr(actbwd::k_gated_bwd<2>);
-    case 4: return addr(actbwd::k_gated_bwd<4>);
-    default: return addr(actbwd::k_gated_bwd<8>);
+    case 1: return addr(actbwd::k_act_dz<1, 1>);
+    case 2: return addr(actbwd::k_act_dz<1, 2>);
+    case 4: return addr(actbwd::k_act_dz<1, 4>);
+    case 8: return addr(actbwd::k_act_dz<1, 8>);
+    default: return addr(actbwd::k_act_dz<1, 16>);
   }
 }
 
-const void *act_bwd_kernel() { return addr(actbwd::k_act_bwd); }
+const void *col_part_kernel() { return addr(actbwd::k_col_part); }
+const void *col_sum_slots_kernel() { return addr(actbwd::k_col_sum_slots); }
+
+const void *dgrad_split_kernel(int fmt) {
+  switch (fmt) {
+    case FMT_NF4: return addr(dgrad::k_gemm_dgrad<FMT_NF4, false, false, true>);
+    case FMT_NF4_DQ: return addr(dgrad::k_gemm_dgrad<FMT_NF4_DQ, false, true, true>);
+    case FMT_MXFP4: return addr(dgrad::k_gemm_dgrad<FMT_MXFP4, false, false, true>);
+    default: return addr(dgrad::k_gemm_dgrad<FMT_NVFP4, false, false, true>);
+  }
+}
 
 }  // namespace ffn
 }  // namespace lora4

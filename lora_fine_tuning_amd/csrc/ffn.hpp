@@ -5,6 +5,7 @@
 #pragma once
 
 #include "act_bwd.hpp"
+#include "gemm_dgrad.hpp"
 #include "gemm_fwd.hpp"
 #include "norm.hpp"
 #include "small.hpp"
@@ -19,7 +20,7 @@ struct NormShape {
 };
 NormShape norm_shape(int D);
 const void *norm_fwd_kernel(NormShape s, bool mx);
-const void *norm_bwd_kernel(NormShape s, bool dw);
+const void *norm_bwd_kernel(NormShape s, bool dw, bool edge);   // edge: D % 8 != 0
 const void *col_sum_kernel();
 
 // Forward tiles with an epilogue (epi: fwd::EPI_GATED, fwd::EPI_FUSED).
@@ -37,8 +38,14 @@ const void *epi_reduce_kernel(int epi);
 const void *small_kernel(int fmt, int epi, int xt, int nw);
 const void *small_z_kernel();
 
-const void *gated_bwd_kernel(int tj);   // tj: 16-column blocks of the rank, 1, 2, 4 or 8
-const void *act_bwd_kernel();
+// Gradient of the activation and dZ: projections 1 or 2; tj: 16-column blocks of
+// the rank, 1, 2, 4, 8 or 16 (16 with one projection only).
+const void *act_dz_kernel(int projections, int tj);
+const void *col_part_kernel();
+const void *col_sum_slots_kernel();
+
+// The 256 x 256 dgrad with its reduction split over blocks.
+const void *dgrad_split_kernel(int fmt);
 
 }  // namespace ffn
 }  // namespace lora4

@@ -5,10 +5,11 @@
 //   gated forward   : Z = X A^T, both projections' A as one operand of 2 r rows
 //                     (k_small_z, or the rank-r row pass for many rows), then
 //                     k_small, or the gated tiles, whole or split and summed
-//   gated backward  : [Z pass] -> k_gated_bwd (dG, dU, partial dZ) -> dX over
+//   gated backward  : [Z pass] -> k_act_dz (dG, dU, partial dZ) -> dX over
 //                     both projections as one reduction -> dA, dB
 //   fused forward   : as the gated, with one projection
-//   fused backward  : k_act_bwd (dP, column sums) -> dbias -> lora4_backward
+//   fused backward  : with an activation as the gated, with one projection and
+//                     dbias; else dbias and the plain layer's backward
 #pragma once
 
 namespace {
@@ -42,14 +43,18 @@ bool all_aligned16(std::initializer_list<const void *> ps) {
 // Blocks of the norm's grids: enough for the chip to be full several times
 // over (rows beyond them are walked in steps of the grid).
 constexpr int64_t NORM_MAX_BLOCKS = 1 << 16;
-// Blocks with dW: each keeps a row of fp32 sums to be added up afterwards.
-constexpr int64_t NORM_DW_BLOCKS = 512;
-
+// Blocks with dW: each keeps a row of fp32 sums to be added up afterwards, so
+// as many as are on the chip at a time, by their registers (blocks of up to four
+// waves, which hold two rows: 8 waves per CU; wider ones 16, with masks 12). A
+// multiple of 8 (see k_rmsnorm_bwd), unless every row has a block.
 int norm_rows_per_block(ffn::NormShape s) { return s.threads == 64 ? norm::WAVE_ROWS : 1; }
 
 int64_t norm_dw_blocks(int64_t M, int64_t D) {
   const ffn::NormShape s = ffn::norm_shape((int)D);
-  return std::min<int64_t>(NORM_DW_BLOCKS, ceil_div(M, norm_rows_per_block(s)));
+  const int64_t waves = s.threads == 64 ? norm::WAVE_ROWS : s.threads / 64;
+  const int64_t per_cu = std::max<int64_t>(1, (waves <= 4 ? 8 : D % 8 == 0 ? 16 : 12) / waves);
+  const int64_t need = ceil_div(M, norm_rows_per_block(s));
+  return std::min(std::max<int64_t>(8, per_cu * cu_count() / 8 * 8), need);
 }
 
 size_t norm_ws_bytes(int64_t M, int64_t D) {
@@ -58,7 +63,9 @@ size_t norm_ws_bytes(int64_t M, int64_t D) {
 }
 
 lora4_status check_norm(int64_t M, int64_t D, float eps) {
-  if (M < 0 || M > (int64_t(1) << 31) || D < 1 || D > norm::MAX_D) return LORA4_ERR_SHAPE;
+  if (M < 0 || M > (int64_t(1) << 31) || D < 1 ||
+      D > (D % 8 == 0 ? norm::MAX_D : norm::MAX_D_UNALIGNED))
+    return LORA4_ERR_SHAPE;
   if (!std::isfinite(eps) || eps < 0.0f) return LORA4_ERR_SHAPE;
   return LORA4_OK;
 }
@@ -95,7 +102,7 @@ lora4_status norm_backward(const uint16_t *dY, const uint16_t *H, const uint16_t
   const int64_t per = norm_rows_per_block(s);
   const int64_t blocks = dW ? norm_dw_blocks(M, D) : std::min(NORM_MAX_BLOCKS, ceil_div(M, per));
   const norm::BwdParams p{dY, H, w, dH, M, (int)D, eps, dX, dW ? reinterpret_cast<float *>(ws) : nullptr};
-  TRY(launch_fn("rmsnorm_bwd", ffn::norm_bwd_kernel(s, dW != nullptr), blocks,
+  TRY(launch_fn("rmsnorm_bwd", ffn::norm_bwd_kernel(s, dW != nullptr, D % 8 != 0), blocks,
                 s.threads == 64 ? 64 * norm::WAVE_ROWS : s.threads, 0, st, p));
   if (!dW) return LORA4_OK;
   return launch_fn("rmsnorm_dw", ffn::col_sum_kernel(), ceil_div(D, 32), 1024, 0, st, (const float *)ws,
@@ -374,48 +381,90 @@ lora4_status ffn_forward(const Ffn &f, int act, const uint16_t *X, const uint16_
 }
 
 // ---------------------------------------------------------------------------
-// Gated backward
+// Backward of the gated projections, and of one projection with an activation
 // ---------------------------------------------------------------------------
 
-// The gate and the up base of a group as one base of 2 Np rows (Np: N rounded
-// up to whole row blocks; the padding rows dequantize to zero).
-PackedW halves_of(const lora4_W *W, int64_t Np) {
+// The bases of a group's projections as one base of P Np rows (Np: N rounded
+// up to whole row blocks; the padding rows dequantize to zero): the reduction
+// of dX runs over the gradients of both.
+PackedW joint_base(const lora4_W *W, int P, int64_t Np) {
   PackedW p = packed_of(Base{W, W->groups, false});
-  p.N = 2 * Np;
-  p.half = Np;
-  p.half_s2 = p.g_scales2;
-  p.g_codes *= 2;
-  p.g_scales *= 2;
-  p.g_scales2 *= 2;
+  p.N = P * Np;
+  if (P == 2) {
+    p.half = Np;
+    p.half_s2 = p.g_scales2;
+    p.g_codes *= 2;
+    p.g_scales *= 2;
+    p.g_scales2 *= 2;
+  }
   return p;
 }
 
-constexpr int64_t GATED_BWD_BLOCKS = 1024;   // blocks wanted of k_gated_bwd
-constexpr int GATED_BWD_RANGES = 16;
+constexpr int64_t ACT_DZ_BLOCKS = 1024;   // blocks wanted of k_act_dz
+constexpr int ACT_DZ_RANGES = 32;
 
-struct GatedBwdPlan {
+// How dX is made: the library's own choice for the plain layer (the 256 x 256
+// dgrad where its tiles fill the chip, else the 128 x 128 kernel), or the
+// 256 x 256 dgrad with the reduction split over blocks.
+// LORA4_FFN_DGRAD forces it for tests and measurements: "split" or "own".
+int dgrad_policy() {
+  const char *e = std::getenv("LORA4_FFN_DGRAD");
+  if (!e) return 0;
+  const std::string v(e);
+  return v == "split" ? 1 : v == "own" ? 2 : 0;
+}
+
+struct FfnBwdPlan {
   int64_t Np;
   PackedW pw;
   lora4_W Wv;        // the joint base as make_plan sees it
   Plan pl;           // its dgrad plan
+  bool dx_split;     // dX by the split dgrad, in dx_ranges ranges of dx_steps steps
+  int dx_ranges, dx_steps;
+  int64_t dx_slots;
+  int64_t slots;     // row slots of k_act_dz
   int ranges, steps;
   int rt, msplit_a, msplit_b;
   int64_t tq_a, tq_b, ncnt;
-  size_t off_z, off_skpart, off_dz, off_dgu, off_dzpart, off_pa, off_pb, off_cnt, off_partx, bytes;
+  size_t off_z, off_skpart, off_dz, off_grad, off_dzpart, off_col, off_pa, off_pb, off_cnt, off_partx, bytes;
 };
 
-GatedBwdPlan gated_bwd_plan(const Ffn &f) {
-  GatedBwdPlan p{};
+FfnBwdPlan ffn_bwd_plan(const Ffn &f, bool dbias) {
+  FfnBwdPlan p{};
   const lora4_W *W = f.W;
-  const int64_t M = std::max<int64_t>(f.M, 1), K = W->K, N = W->N, G = 2 * f.E;
+  const int64_t M = std::max<int64_t>(f.M, 1), K = W->K, N = W->N, G = f.P * f.E;
+  const int64_t extra = f.E > 1 ? std::min(f.E, M) : 0;
+  const int R = f.P * f.r;
   p.Np = w_blocks(N) * 64;
-  p.pw = halves_of(W, p.Np);
+  p.pw = joint_base(W, f.P, p.Np);
   p.Wv = *W;
-  p.Wv.N = 2 * p.Np;
+  p.Wv.N = f.P * p.Np;
   p.Wv.groups = f.E;
-  p.pl = make_plan(1, Base{&p.Wv, f.E, false}, f.M, 2 * f.r);
-  const int64_t slots = ceil_div(M, 64) + (f.E > 1 ? f.E : 0), all = p.Np / 64;
-  int64_t want = std::min<int64_t>({ceil_div(GATED_BWD_BLOCKS, slots), GATED_BWD_RANGES, all});
+  p.pl = make_plan(1, Base{&p.Wv, f.E, false}, f.M, R);
+  {
+    const int64_t ld = f.P * p.Np, steps = ceil_div(ld, dgrad::BKS), cus = cu_count();
+    p.dx_slots = ceil_div(M, dgrad::BM) + extra;
+    const int64_t tiles = p.dx_slots * ceil_div(K, dgrad::BN);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>({cus / std::max<int64_t>(tiles, 1), steps / 4, 32}));
+    p.dx_steps = (int)ceil_div(steps, want);
+    p.dx_ranges = (int)ceil_div(steps, p.dx_steps);
+    // Estimated times, us: 1.9 a step, the partial sums' way through memory, and
+    // an extra launch; against the 128 x 128 kernel's rate, on few blocks and on
+    // many. Measured
+    // (NF4, 4096 x 4096): 512 rows 52 against 73 us, 2048 rows 92 against 137;
+    // gated 4096 x 14336, 1024 rows: 224 against 767; 1024 x 2048 (MXFP4), 256
+    // rows: 33 against 25.
+    const double t_split = 1.9 * p.dx_steps + 16.0 + 2.0 * p.dx_ranges * (double)M * (double)K * 4 / 4.0e6;
+    const int64_t own_slots = ceil_div(M, BM_MAIN) + extra;
+    const double t_own = 20.0 + 2.0 * (double)own_slots * BM_MAIN * (double)K * (double)ld /
+                                    (own_slots * ceil_div(K, BN_MAIN) < cus ? 3.6e8 : 5.2e8);
+    const int pol = dgrad_policy();
+    const bool fits = big_fits(ld, M, p.pw) && big_policy() < 0;
+    p.dx_split = fits && pol != 2 && !dgrad_taken(ld, ld, f.M, p.pw, K, f.E) && (pol == 1 || t_split < t_own);
+  }
+  p.slots = ceil_div(M, 64) + extra;
+  const int64_t all = p.Np / 64;
+  const int64_t want = std::min<int64_t>({ceil_div(ACT_DZ_BLOCKS, p.slots), ACT_DZ_RANGES, all});
   p.steps = (int)ceil_div(all, std::max<int64_t>(1, want));
   p.ranges = (int)ceil_div(all, p.steps);
   p.rt = skinny_tile(f.r);
@@ -436,33 +485,34 @@ GatedBwdPlan gated_bwd_plan(const Ffn &f) {
     off += align256(b);
     return o;
   };
-  const size_t mr = (size_t)M * 2 * f.r;
+  const size_t mr = (size_t)M * R;
   p.off_z = take(mr * 2);
-  p.off_skpart = take(sk_part_bytes_for(f.M, K, 2 * f.r, f.E, 0));
+  p.off_skpart = take(sk_part_bytes_for(f.M, K, R, f.E, 0));
   p.off_dz = take(mr * 2);
-  p.off_dgu = take((size_t)M * 2 * p.Np * 2);
+  p.off_grad = take((size_t)M * f.P * p.Np * 2);
   p.off_dzpart = take((size_t)p.ranges * mr * 4);
+  p.off_col = take(dbias ? (size_t)p.slots * N * 4 : 0);
   p.off_pa = take((size_t)p.msplit_a * G * f.r * K * 4);
   p.off_pb = take((size_t)p.msplit_b * G * f.r * N * 4);
   p.off_cnt = take((size_t)p.ncnt * 4);
-  p.off_partx = take(p.pl.lds_splits > 1 ? (size_t)p.pl.lds_splits * M * K * 4 : 0);
+  const int64_t parts = p.dx_split ? p.dx_ranges : p.pl.lds_splits > 1 ? p.pl.lds_splits : 0;
+  p.off_partx = take((size_t)parts * M * K * 4);
   p.bytes = off;
   return p;
 }
 
-lora4_status gated_backward(const Ffn &f, int act, const uint16_t *X, const uint16_t *dH, const uint16_t *GU,
-                            const uint16_t *A, const uint16_t *B, float s, const int64_t *offs, const uint16_t *Z,
-                            uint16_t *dX, uint16_t *dA, uint16_t *dB, void *ws, size_t ws_bytes, hipStream_t st) {
-  TRY(check_ffn(f, act, s, offs));
-  if (!A || !B || !dA || !dB || (f.M > 0 && (!X || !dH || !GU || !dX))) return LORA4_ERR_NULL;
-  if (!all_aligned16({X, dH, GU, A, B, offs, Z, dX, dA, dB, ws})) return LORA4_ERR_ALIGN;
-  const GatedBwdPlan p = gated_bwd_plan(f);
+lora4_status ffn_backward(const Ffn &f, int act, const uint16_t *X, const uint16_t *dY, const uint16_t *pre,
+                          const uint16_t *A, const uint16_t *B, float s, const int64_t *offs, const uint16_t *Z,
+                          uint16_t *dX, uint16_t *dA, uint16_t *dB, uint16_t *dbias, void *ws, size_t ws_bytes,
+                          hipStream_t st) {
+  const FfnBwdPlan p = ffn_bwd_plan(f, dbias != nullptr);
   if (!ws || ws_bytes < p.bytes) return LORA4_ERR_WORKSPACE;
   const lora4_W *W = f.W;
-  const int64_t K = W->K, N = W->N, G = 2 * f.E;
-  const int r = f.r, R = 2 * r;
+  const int64_t K = W->K, N = W->N, G = f.P * f.E, ld = f.P * p.Np;
+  const int r = f.r, R = f.P * r;
   if (f.M == 0) {
     TRY(fill_zero(dA, G * r * K, st));
+    if (dbias) TRY(fill_zero(dbias, f.E * N, st));
     return fill_zero(dB, G * N * r, st);
   }
   const uint16_t *Zu = Z;
@@ -472,31 +522,53 @@ lora4_status gated_backward(const Ffn &f, int act, const uint16_t *X, const uint
                     ws_at<float>(ws, p.off_skpart), false, st));
     Zu = Zw;
   }
-  // dG, dU and the partial sums of dZ; its first block clears the arrival
-  // counters of the dA / dB tiles
-  uint16_t *dGU = ws_at<uint16_t>(ws, p.off_dgu), *dZ = ws_at<uint16_t>(ws, p.off_dz);
-  float *zpart = ws_at<float>(ws, p.off_dzpart);
+  // the gradients before the activation and the partial sums of dZ; the first
+  // block clears the arrival counters of the dA / dB tiles
+  uint16_t *grad = ws_at<uint16_t>(ws, p.off_grad), *dZ = ws_at<uint16_t>(ws, p.off_dz);
+  float *zpart = ws_at<float>(ws, p.off_dzpart), *col = dbias ? ws_at<float>(ws, p.off_col) : nullptr;
   unsigned *cnt = ws_at<unsigned>(ws, p.off_cnt);
   {
-    actbwd::GatedParams q{dH, GU, B, f.M, N, p.Np, r, act, offs, (int)f.E, dGU, p.steps, zpart, cnt, p.ncnt};
-    const int64_t slots = ceil_div(f.M, 64) + (f.E > 1 ? f.E : 0);
-    const void *fn = ffn::gated_bwd_kernel(r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8);
+    actbwd::DzParams q{dY,   pre,     B,     f.M, N,   p.Np,   r,     act, offs, (int)f.E,
+                       grad, p.steps, zpart, col, cnt, p.ncnt};
+    const void *fn = ffn::act_dz_kernel(f.P, r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : r <= 128 ? 8 : 16);
     void *argv[] = {&q};
-    TRY(launch_timed("gated_bwd", st, [&] {
-      (void)hipLaunchKernel(fn, dim3((unsigned)slots, (unsigned)p.ranges), dim3(actbwd::THREADS), argv, 0, st);
+    TRY(launch_timed("act_dz", st, [&] {
+      (void)hipLaunchKernel(fn, dim3((unsigned)p.slots, (unsigned)p.ranges), dim3(actbwd::THREADS), argv, 0, st);
+    }));
+  }
+  if (dbias) {
+    const int E = (int)f.E;
+    int64_t M = f.M, n = N;
+    void *argv[] = {&col, (void *)&offs, (void *)&E, &M, &n, &dbias};
+    const void *sum = ffn::col_sum_slots_kernel();
+    TRY(launch_timed("dbias_sum", st, [&] {
+      (void)hipLaunchKernel(sum, dim3((unsigned)ceil_div(N, 32), (unsigned)f.E), dim3(1024), argv, 0, st);
     }));
   }
   // dZ = s (..): by the dgrad's tail where it takes partial sums, else here
-  const bool tail = p.ranges <= big::A2_MAX_PARTS && dgrad_taken(2 * p.Np, 2 * p.Np, f.M, p.pw, K, f.E);
+  const bool big = p.dx_split || dgrad_taken(ld, ld, f.M, p.pw, K, f.E);
+  const bool tail = p.ranges <= big::A2_MAX_PARTS && big;
   const TailParts tp{zpart, p.ranges, s, dZ, s, nullptr, 0.0f};
   if (!tail)
     TRY(reduce_bf16("reduce_dz", zpart, p.ranges, f.M * R, f.M * R, dZ, s, nullptr, 0.0f, st));
   // dX = [dG dU] [deq(Wg); deq(Wu)] + dZ [Ag; Au]
-  {
+  float *partx = ws_at<float>(ws, p.off_partx);
+  if (p.dx_split) {
+    big::Params q = big_params(mat(grad, ld), p.pw, ld, mat(dZ, R), mat(A, K, (int64_t)R * K), R, f.M, K, offs, f.E,
+                               dX, K);
+    if (tail) apply_tail_parts(q, &tp);
+    q.nslots = (int)p.dx_slots;
+    q.ksplit = p.dx_ranges;
+    q.split_steps = p.dx_steps;
+    q.Cpart = partx;
+    TRY(launch_fn("gemm_nn_dgrad", ffn::dgrad_split_kernel(W->format), p.dx_slots * q.tiles_n * p.dx_ranges,
+                  dgrad::THREADS, (size_t)dgrad::lds_bytes(), st, q));
+    TRY(reduce_bf16("reduce_dx", partx, p.dx_ranges, f.M * K, f.M * K, dX, 1.0f, nullptr, 0.0f, st));
+  } else {
     NnParams q{};
-    q.A = mat(dGU, 2 * p.Np);
+    q.A = mat(grad, ld);
     q.W = p.pw;
-    q.R = 2 * p.Np;
+    q.R = ld;
     q.A2 = mat(dZ, R);
     q.B2 = mat(A, K, (int64_t)R * K);
     q.r2 = R;
@@ -504,11 +576,11 @@ lora4_status gated_backward(const Ffn &f, int act, const uint16_t *X, const uint
     q.Nc = K;
     q.offsets = offs;
     q.groups = (int)f.E;
-    q.Rsplit = 2 * p.Np;
+    q.Rsplit = ld;
     q.out = GemmOut{dX, K, nullptr, 0, 1.0f};
     q.tab = nf4_table();
     dim3 grid((unsigned)ceil_div(K, BN_MAIN), (unsigned)p.pl.row_slots, 1);
-    TRY(run_nn_main_fmt(W->format, q, grid, p.pl, ws_at<float>(ws, p.off_partx), tail ? &tp : nullptr, st));
+    TRY(run_nn_main_fmt(W->format, q, grid, p.pl, partx, tail ? &tp : nullptr, st));
   }
   // dA = dZ^T X and dB = s [dG dU]^T Z, per projection
   TnParams pa{};
@@ -525,12 +597,12 @@ lora4_status gated_backward(const Ffn &f, int act, const uint16_t *X, const uint
   pa.out = dA;
   pa.alpha = 1.0f;
   pa.transpose_out = 0;
-  pa.half_shift = 1;
-  pa.u_half = r;
+  pa.half_shift = f.P - 1;
+  pa.u_half = f.P == 2 ? r : 0;
   pa.v_half = 0;
   TnParams pb = pa;
   pb.U = mat(Zu, R);
-  pb.V = mat(dGU, 2 * p.Np);
+  pb.V = mat(grad, ld);
   pb.Q = N;
   pb.splits = p.msplit_b;
   pb.part = ws_at<float>(ws, p.off_pb);
@@ -538,35 +610,52 @@ lora4_status gated_backward(const Ffn &f, int act, const uint16_t *X, const uint
   pb.out = dB;
   pb.alpha = s;
   pb.transpose_out = 1;
-  pb.v_half = p.Np;
+  pb.v_half = f.P == 2 ? p.Np : 0;
   return run_tn2("gemm_tn_dA_dB", p.rt, pa, pb, (int)p.tq_a, (int)(p.msplit_a * G), (int)p.tq_b,
                  (int)(p.msplit_b * G), st);
 }
 
-// ---------------------------------------------------------------------------
-// Backward of the linear with an epilogue
-// ---------------------------------------------------------------------------
-
-struct FusedBwdPlan {
+// Backward of one projection without an activation: the plain layer's, and the
+// column sums of dY.
+struct ColPlan {
   int64_t xblocks;
-  int splits;          // row ranges of k_act_bwd per group
-  size_t off_dp, off_part, off_lin, lin_bytes, bytes;
+  int splits;          // row ranges of k_col_part per group
+  size_t bytes;
 };
 
-FusedBwdPlan fused_bwd_plan(const Ffn &f, bool act, bool dbias) {
-  FusedBwdPlan p{};
+ColPlan col_plan(const Ffn &f) {
+  ColPlan p{};
   const int64_t M = std::max<int64_t>(f.M, 1), N = f.W->N;
-  p.xblocks = ceil_div(N, actbwd::ACT_COLS);
+  p.xblocks = ceil_div(N, actbwd::COL_BLOCK);
   // about 1024 blocks, of at least 16 rows each
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(1024, p.xblocks * f.E), ceil_div(M, 16 * f.E)));
-  p.off_dp = 0;
-  size_t off = act ? align256((size_t)M * N * 2) : 0;
-  p.off_part = off;
-  if (dbias) off += align256((size_t)f.E * p.splits * 4 * N * 4);
-  p.off_lin = off;
-  p.lin_bytes = make_plan(1, Base{f.W, f.E, false}, f.M, f.r).bytes;
-  p.bytes = off + p.lin_bytes;
+  p.bytes = align256((size_t)f.E * p.splits * 4 * N * 4);
   return p;
+}
+
+lora4_status col_sums(const Ffn &f, const uint16_t *dY, const int64_t *offs, uint16_t *dbias, void *ws,
+                      hipStream_t st) {
+  if (f.M == 0) return fill_zero(dbias, f.E * f.W->N, st);
+  const ColPlan p = col_plan(f);
+  float *part = reinterpret_cast<float *>(ws);
+  actbwd::ColParams q{dY, f.M, (int)f.W->N, offs, (int)f.E, part};
+  const void *fn = ffn::col_part_kernel();
+  void *argv[] = {&q};
+  TRY(launch_timed("dbias_part", st, [&] {
+    (void)hipLaunchKernel(fn, dim3((unsigned)p.xblocks, (unsigned)p.splits, (unsigned)f.E), dim3(actbwd::THREADS),
+                          argv, 0, st);
+  }));
+  const int n = p.splits * 4, D = (int)f.W->N;
+  void *sargv[] = {&part, (void *)&n, (void *)&D, &dbias};
+  const void *sum = ffn::col_sum_kernel();
+  return launch_timed("dbias_sum", st, [&] {
+    (void)hipLaunchKernel(sum, dim3((unsigned)ceil_div(D, 32), (unsigned)f.E), dim3(1024), sargv, 0, st);
+  });
+}
+
+size_t fused_bwd_bytes(const Ffn &f, bool act, bool dbias) {
+  if (act) return ffn_bwd_plan(f, dbias).bytes;
+  return (dbias ? col_plan(f).bytes : 0) + make_plan(1, Base{f.W, f.E, false}, f.M, f.r).bytes;
 }
 
 }  // namespace

@@ -78,8 +78,10 @@ struct WRaw {
 
 // SHARED: the row tiles ignore the groups (Params::shared_rows). HALVES: the
 // reduction runs over two projections (PackedW::half), which only NF4-DQ's
-// second-level scales have to know.
-template <int FMT, bool SHARED, bool HALVES = false>
+// second-level scales have to know. SPLIT: block b computes reduction range
+// b % ksplit (p.split_steps steps; the rank-r tail with range 0) of tile
+// b / ksplit and writes fp32 sums to p.Cpart [range][M][Nc].
+template <int FMT, bool SHARED, bool HALVES = false, bool SPLIT = false>
 __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
   const uint32_t sel = big::sel_base();
@@ -87,12 +89,16 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
   uint16_t *const Bs0 = smem + 2 * TILE_A, *const Bs1 = smem + 2 * TILE_A + TILE_W;
 
   int b = blockIdx.x;
-  {
+  const int split = SPLIT ? b % p.ksplit : 0;
+  if constexpr (SPLIT) {
+    b /= p.ksplit;
+  } else {
     const int per = p.nblocks >> 3;
     if (b < per * 8) b = (b & 7) * per + (b >> 3);
   }
+  const int sb = SPLIT ? split * p.split_steps : 0;   // first step of this block's range
   int tn, slot;
-  big::grouped_tile(b, p.tiles_n, p.nblocks / p.tiles_n, slot, tn);
+  big::grouped_tile(b, p.tiles_n, SPLIT ? p.nslots : p.nblocks / p.tiles_n, slot, tn);
   const RowTile rt = big::tile_rows<SHARED>(p, slot, BM);
   if (rt.group < 0) return;
   const int g = rt.group;
@@ -112,6 +118,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
   const uint32_t a_cstep = (uint32_t)(32 * p.A.ld * 2);
   // dY of step s into stage As, chunks 4 half .. 4 half + 3
   auto issue_a = [&](int s, uint16_t *As, int half) {
+    if constexpr (SPLIT) s += sb;
     const int64_t k0 = (int64_t)s * BKS;
     const bool edge = k0 + a_kq >= p.R;
 #pragma unroll
@@ -166,6 +173,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
   };
 
   auto load_w = [&](int s, WRaw &w) {
+    if constexpr (SPLIT) s += sb;
     const int wo = (int)(w_step * s);
     w.c0 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(w_rsrc, w_voff0, wo, 0));
     w.c1 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(w_rsrc, w_voff1, wo, 0));
@@ -286,6 +294,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
     uint32_t t[8];
   };
   auto issue_a1 = [&](int s, uint16_t *As, int c) {
+    if constexpr (SPLIT) s += sb;
     const int64_t k0 = (int64_t)s * BKS;
     const bool edge = k0 + a_kq >= p.R;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (__attribute__((address_space(3))) void *)(As + (c * 4 + wave) * 512),
@@ -294,6 +303,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
   // global loads of run s after the dY chunks: codes 0..3, codes 4..7, scales
   constexpr int W_LOADS_D = FMT == FMT_NF4 ? 3 : 4;
   auto load_w1 = [&](int s, WRaw &w, int part) {
+    if constexpr (SPLIT) s += sb;
     const int wo = (int)(w_step * s);
     const int so = (int)(s_step * s);
     if (part == 0) {
@@ -446,7 +456,8 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
     }
   };
 
-  const int steps = (int)((p.R + BKS - 1) / BKS);
+  const int all_steps = (int)((p.R + BKS - 1) / BKS);
+  const int steps = SPLIT ? min(all_steps - sb, p.split_steps) : all_steps;
   WRaw r0, r1;
   issue_a(0, As0, 0);
   issue_a(0, As0, 1);
@@ -495,7 +506,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
   // the tile's groups run as one block-diagonal product (big::TileGroups):
   // reduction row k is row k - i rp of the tile's group i. Each step ends
   // with a barrier, so the stages are free again.
-  if (p.r2 > 0) {
+  if (p.r2 > 0 && split == 0) {
     const bool a_vec = (p.A2.ld % 8) == 0;
     const bool b_vec = (p.B2.ld % 8) == 0;
     const int64_t row_hi = min(row0 + BM, row_end);
@@ -568,6 +579,30 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
 
   // ---- epilogue: register e of acc[j][i] holds
   // dX[wm0 + 32 i + lane % 32][wn0 + 32 j + 8 (e / 4) + 4 (lane / 32) + e % 4].
+  if constexpr (SPLIT) {
+    float *dst = p.Cpart + (int64_t)split * p.M * p.Nc;
+    const bool vec = (p.Nc % 4) == 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t grow = row0 + wm0 + 32 * i + l32;
+      if (grow >= row_end) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const int64_t gcol = col0 + wn0 + 32 * j + 8 * r4 + 4 * h;
+          if (vec && gcol + 4 <= p.Nc) {
+            *reinterpret_cast<f32x4_t *>(dst + grow * p.Nc + gcol) =
+                f32x4_t{acc[j][i][4 * r4], acc[j][i][4 * r4 + 1], acc[j][i][4 * r4 + 2], acc[j][i][4 * r4 + 3]};
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (gcol + e < p.Nc) dst[grow * p.Nc + gcol + e] = acc[j][i][4 * r4 + e];
+          }
+        }
+    }
+    return;
+  }
   // Each wave stages its 128 x 128 bf16 block in LDS (free now; 32 KB per
   // wave, 256-byte rows, chunk c of row r at c ^ (r % 16)) and writes it back
   // as 4 whole 256-byte row segments per store instruction (element stores

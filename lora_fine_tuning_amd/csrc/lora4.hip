@@ -1830,7 +1830,7 @@ size_t lora4_gated_workspace_bytes(int which, const lora4_W *W, int64_t M, int32
   const Ffn f = gated_of(W, M, r);
   const int64_t some = 0;   // (stands for the offsets, which the sizes do not depend on)
   if (check_ffn(f, LORA4_ACT_NONE, 1.0f, f.E > 1 ? &some : nullptr) != LORA4_OK) return 0;
-  return which == 0 ? ffn_plan(f).bytes : gated_bwd_plan(f).bytes;
+  return which == 0 ? ffn_plan(f).bytes : ffn_bwd_plan(f, false).bytes;
 }
 
 lora4_status lora4_gated_forward(const lora4_W *W, int32_t activation, const uint16_t *X, int64_t M,
@@ -1848,8 +1848,12 @@ lora4_status lora4_gated_backward(const lora4_W *W, int32_t activation, const ui
                                   uint16_t *dA, uint16_t *dB, void *workspace, size_t workspace_bytes,
                                   void *stream) {
   if (!W) return LORA4_ERR_NULL;
-  return gated_backward(gated_of(W, M, r), activation, X, dH, GU, A, B, s, group_offsets, Z, dX, dA, dB, workspace,
-                        workspace_bytes, reinterpret_cast<hipStream_t>(stream));
+  const Ffn f = gated_of(W, M, r);
+  TRY(check_ffn(f, activation, s, group_offsets));
+  if (!A || !B || !dA || !dB || (M > 0 && (!X || !dH || !GU || !dX))) return LORA4_ERR_NULL;
+  if (!all_aligned16({X, dH, GU, A, B, group_offsets, Z, dX, dA, dB, workspace})) return LORA4_ERR_ALIGN;
+  return ffn_backward(f, activation, X, dH, GU, A, B, s, group_offsets, Z, dX, dA, dB, nullptr, workspace,
+                      workspace_bytes, reinterpret_cast<hipStream_t>(stream));
 }
 
 size_t lora4_epilogue_workspace_bytes(int which, const lora4_W *W, int64_t M, int32_t r) {
@@ -1857,7 +1861,8 @@ size_t lora4_epilogue_workspace_bytes(int which, const lora4_W *W, int64_t M, in
   const Ffn f = fused_of(W, M, r);
   const int64_t some = 0;
   if (check_ffn(f, LORA4_ACT_NONE, 1.0f, f.E > 1 ? &some : nullptr) != LORA4_OK) return 0;
-  return which == 0 ? ffn_plan(f).bytes : fused_bwd_plan(f, true, true).bytes;
+  return which == 0 ? ffn_plan(f).bytes
+                    : std::max(fused_bwd_bytes(f, true, true), fused_bwd_bytes(f, false, true));
 }
 
 lora4_status lora4_forward_epilogue(const lora4_W *W, int32_t activation, const uint16_t *X, int64_t M,
@@ -1881,34 +1886,18 @@ lora4_status lora4_backward_epilogue(const lora4_W *W, int32_t activation, const
   const bool act = activation != LORA4_ACT_NONE;
   if (!A || !B || !dA || !dB || (M > 0 && (!X || !dY || !dX || (act && !P)))) return LORA4_ERR_NULL;
   if (!all_aligned16({X, dY, P, A, B, group_offsets, Z, dX, dA, dB, dbias, workspace})) return LORA4_ERR_ALIGN;
-  const FusedBwdPlan pl = fused_bwd_plan(f, act, dbias != nullptr);
-  if (!workspace || workspace_bytes < pl.bytes) return LORA4_ERR_WORKSPACE;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const int64_t N = W->N;
-  if (M == 0) {
-    if (dbias) TRY(fill_zero(dbias, f.E * N, st));
-  } else if (act || dbias) {
-    float *part = dbias ? ws_at<float>(workspace, pl.off_part) : nullptr;
-    uint16_t *dP = act ? ws_at<uint16_t>(workspace, pl.off_dp) : nullptr;
-    actbwd::ActParams q{dY, act ? P : nullptr, M, (int)N, activation, group_offsets, (int)f.E, dP, part};
-    const void *fn = ffn::act_bwd_kernel();
-    void *argv[] = {&q};
-    TRY(launch_timed("act_bwd", st, [&] {
-      (void)hipLaunchKernel(fn, dim3((unsigned)pl.xblocks, (unsigned)pl.splits, (unsigned)f.E), dim3(actbwd::THREADS),
-                            argv, 0, st);
-    }));
-    if (dbias) {
-      const int n = pl.splits * 4, D = (int)N;
-      void *sargv[] = {&part, (void *)&n, (void *)&D, &dbias};
-      const void *sum = ffn::col_sum_kernel();
-      TRY(launch_timed("dbias_sum", st, [&] {
-        (void)hipLaunchKernel(sum, dim3((unsigned)ceil_div(N, 32), (unsigned)f.E), dim3(1024), sargv, 0, st);
-      }));
-    }
-    if (act) dY = dP;
+  if (act)
+    return ffn_backward(f, activation, X, dY, P, A, B, s, group_offsets, Z, dX, dA, dB, dbias, workspace,
+                        workspace_bytes, st);
+  if (!workspace || workspace_bytes < fused_bwd_bytes(f, false, dbias != nullptr)) return LORA4_ERR_WORKSPACE;
+  size_t off = 0;
+  if (dbias) {
+    TRY(col_sums(f, dY, group_offsets, dbias, workspace, st));
+    off = col_plan(f).bytes;
   }
   return backward_impl(Base{W, f.E, false}, X, dY, M, A, B, r, s, group_offsets, Z, dX, dA, dB,
-                       ws_at<char>(workspace, pl.off_lin), pl.lin_bytes, stream);
+                       ws_at<char>(workspace, off), workspace_bytes - off, stream);
 }
 
 }  // extern "C"

@@ -16,9 +16,13 @@
 // adapter (bf16 Y) of a layer read one value.
 //
 // Rows of any length: a row of D % 8 != 0 elements starts at an address that
-// is a multiple of 2 only; the 16-byte accesses are issued there all the same
-// (global memory takes them at any alignment on amdhsa), the row's last D % 8
-// elements one by one.
+// is a multiple of 2 only. The forward issues its 16-byte accesses there all
+// the same (global memory takes them at any alignment on amdhsa; 4097 rows of
+// 5003: 5.1 TB/s), the row's last D % 8 elements one by one. The backward, with
+// three tensors to read for one to write, loses half its rate that way: there
+// a thread's vectors are the memory's aligned ones, which lie 0 to 7 elements
+// before the row's (the same shift for all the tensors of a row), and the
+// elements of the neighbouring rows are masked out.
 #pragma once
 
 #include "common.hpp"
@@ -27,7 +31,8 @@
 namespace lora4 {
 namespace norm {
 
-constexpr int MAX_D = 16384;   // 1024 threads x 2 vectors of 8
+// 1024 threads x 2 vectors of 8; one vector less for rows that start unaligned
+constexpr int MAX_D = 16384, MAX_D_UNALIGNED = 16376;
 
 struct FwdParams {
   const uint16_t *X;
@@ -201,92 +206,142 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 64 * MAX_WAVES) void k_rmsn
 // Rows blockIdx.x * RPB + .., in steps of gridDim.x * RPB. With DW each thread
 // keeps the sums of its columns over the block's rows in registers and writes
 // them out once (dw_part, RPB rows of partials per block), summed in a fixed
-// order by k_col_sum.
-template <bool WAVE, int VPT, bool DW>
-__global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 64 * MAX_WAVES) void k_rmsnorm_bwd(BwdParams p) {
+// order by k_col_sum; there are few blocks then (their partials cost traffic),
+// and in blocks of up to four waves the next row's loads are issued before a
+// row is worked on (two register sets in turn), so that a block keeps memory
+// busy over its reductions; wider blocks rather share a CU. MAXW: waves of the
+// largest block this instantiation runs with.
+//
+// Loads and whole-vector stores go through a buffer descriptor of the row, so
+// that lanes past its end need no branch (one after a load makes it wait).
+// EDGE (D % 8 != 0): rows of one block are a multiple of 8 apart (or there is
+// one), so that the shift of their aligned vectors, and with it a thread's
+// columns, are the same for all; the neighbouring rows' elements in the first
+// and the last vector are masked out and not written.
+template <bool WAVE, int VPT, bool DW, int MAXW, bool EDGE>
+__global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 64 * MAXW) void k_rmsnorm_bwd(BwdParams p) {
   __shared__ float red[2][MAX_WAVES][2];
   constexpr int RPB = WAVE ? WAVE_ROWS : 1;
-  const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x, sub = WAVE ? threadIdx.x >> 6 : 0;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x, sub = WAVE ? wave : 0;
   const int TPR = WAVE ? 64 : blockDim.x;
   const int D = p.D;
-  u32x4_t wv[VPT];
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + sub;
+  // elements from the aligned vector's start to the row's: this thread's vector
+  // j holds columns c0[j] .. + 7, at byte 16 (tid + j TPR) of the row's vectors
+  const int shift = EDGE ? (int)((row * D) & 7) : 0;
+  const uint32_t bytes = (uint32_t)((shift + D) * 2 + 3) & ~3u;
+  int c0[VPT];
+  u32x4_t wv[VPT], mask[EDGE ? VPT : 1];
   float dw[DW ? VPT : 1][8];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int v = tid + j * TPR;
+    c0[j] = 8 * (tid + j * TPR) - shift;
     wv[j] = u32x4_t{0u, 0u, 0u, 0u};
-    if (8 * v < D) wv[j] = load_vec(p.w, v, D);
+    if (c0[j] >= 0 && c0[j] + 8 <= D) wv[j] = *reinterpret_cast<const u32x4_a2_t *>(p.w + c0[j]);
+    if constexpr (EDGE) {
+      mask[j] = u32x4_t{~0u, ~0u, ~0u, ~0u};
+      if (c0[j] < 0 || c0[j] + 8 > D) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (c0[j] + e >= 0 && c0[j] + e < D) wv[j][e >> 1] |= (uint32_t)p.w[c0[j] + e] << (16 * (e & 1));
+          else mask[j][e >> 1] &= 0xFFFF0000u >> (16 * (e & 1));
+        }
+      }
+    }
     if constexpr (DW)
 #pragma unroll
       for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
   }
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < p.M; row += (int64_t)gridDim.x * RPB) {
-    const uint16_t *hp = p.H + row * D, *yp = p.dY + row * D;
-    u32x4_t hv[VPT], yv[VPT], gv[VPT];
+  struct Row {
+    u32x4_t h[VPT], y[VPT], g[VPT];
+  };
+  auto load = [&](Row &r, int64_t row) {
+    const int64_t at = row * D - shift;
+    const big::rsrc_t hs = big::make_rsrc(p.H + at, bytes), ys = big::make_rsrc(p.dY + at, bytes);
+    const big::rsrc_t gs = big::make_rsrc(p.dH ? p.dH + at : p.H, p.dH ? bytes : 0u);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int v = tid + j * TPR;
-      hv[j] = u32x4_t{0u, 0u, 0u, 0u};
-      yv[j] = u32x4_t{0u, 0u, 0u, 0u};
-      if (8 * v < D) {
-        hv[j] = load_vec(hp, v, D);
-        yv[j] = load_vec(yp, v, D);
-      }
+      const uint32_t off = 16u * (tid + j * TPR);
+      r.h[j] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(hs, off, 0, 0));
+      r.y[j] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ys, off, 0, 0));
+      r.g[j] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(gs, off, 0, 0));
     }
-    if (p.dH) {
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int v = tid + j * TPR;
-        gv[j] = u32x4_t{0u, 0u, 0u, 0u};
-        if (8 * v < D) gv[j] = load_vec(p.dH + row * D, v, D);
-      }
-    }
+  };
+  int turn = 0;
+  auto work = [&](Row &r, int64_t row) {
     float ss = 0.0f, st = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float h0 = lo_f32(hv[j][e]), h1 = hi_f32(hv[j][e]);
+        if constexpr (EDGE) {
+          r.h[j][e] &= mask[j][e];
+          r.y[j][e] &= mask[j][e];
+        }
+        const float h0 = lo_f32(r.h[j][e]), h1 = hi_f32(r.h[j][e]);
         ss += h0 * h0 + h1 * h1;
-        st += lo_f32(yv[j][e]) * lo_f32(wv[j][e]) * h0 + hi_f32(yv[j][e]) * hi_f32(wv[j][e]) * h1;
+        st += lo_f32(r.y[j][e]) * lo_f32(wv[j][e]) * h0 + hi_f32(r.y[j][e]) * hi_f32(wv[j][e]) * h1;
       }
     row_sum2<WAVE>(ss, st, red[turn]);
     turn ^= 1;
     const float rstd = 1.0f / sqrtf(ss / (float)D + p.eps);
     const float c = st / (float)D * rstd * rstd;   // mean(t n) rstd
+    const big::rsrc_t os = big::make_rsrc(p.dX + (row * D - shift), bytes);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int v = tid + j * TPR;
       u32x4_t o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float h0 = lo_f32(hv[j][e]), h1 = hi_f32(hv[j][e]);
-        const float y0 = lo_f32(yv[j][e]), y1 = hi_f32(yv[j][e]);
-        float d0 = rstd * (y0 * lo_f32(wv[j][e]) - h0 * c);
-        float d1 = rstd * (y1 * hi_f32(wv[j][e]) - h1 * c);
-        if (p.dH) {
-          d0 += lo_f32(gv[j][e]);
-          d1 += hi_f32(gv[j][e]);
-        }
+        const float h0 = lo_f32(r.h[j][e]), h1 = hi_f32(r.h[j][e]);
+        const float y0 = lo_f32(r.y[j][e]), y1 = hi_f32(r.y[j][e]);
+        const float d0 = rstd * (y0 * lo_f32(wv[j][e]) - h0 * c) + lo_f32(r.g[j][e]);
+        const float d1 = rstd * (y1 * hi_f32(wv[j][e]) - h1 * c) + hi_f32(r.g[j][e]);
         o[e] = pack_bf16x2(d0, d1);
         if constexpr (DW) {
           dw[j][2 * e] += y0 * (h0 * rstd);
           dw[j][2 * e + 1] += y1 * (h1 * rstd);
         }
       }
-      if (8 * v < D) store_vec(p.dX + row * D, v, D, o);
+      const bool whole = !EDGE || (c0[j] >= 0 && c0[j] + 8 <= D);
+      __builtin_amdgcn_raw_buffer_store_b128(o, os, whole ? 16u * (tid + j * TPR) : big::OOB, 0, 0);
+      if constexpr (EDGE) {
+        if (!whole) {
+          uint16_t *dst = p.dX + row * D + c0[j];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c0[j] + e >= 0 && c0[j] + e < D) dst[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+  };
+  if constexpr (DW && (WAVE || MAXW <= 4)) {
+    Row a, b;
+    if (row < p.M) load(a, row);
+    while (row < p.M) {
+      const int64_t next = row + step;
+      if (next < p.M) load(b, next);
+      work(a, row);
+      if (next >= p.M) break;
+      row = next + step;
+      if (row < p.M) load(a, row);
+      work(b, next);
+    }
+  } else {
+    for (; row < p.M; row += step) {
+      Row a;
+      load(a, row);
+      work(a, row);
     }
   }
   if constexpr (DW) {
     float *dst = p.dw_part + ((int64_t)blockIdx.x * RPB + sub) * D;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = tid + j * TPR;
+    for (int j = 0; j < VPT; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (8 * v + e < D) dst[8 * v + e] = dw[j][e];
-    }
+        if (c0[j] + e >= 0 && c0[j] + e < D) dst[c0[j] + e] = dw[j][e];
   }
 }
 

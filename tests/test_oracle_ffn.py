@@ -91,7 +91,7 @@ OK, ENULL, ESHAPE, EALIGN, EFORMAT, EWS = 0, -1, -2, -3, -4, -5
 def test_norm_abi_refusals():
     def fwd(X=4096, R=4096, w=4096, M=8, D=256, eps=1e-5, H=8192, Y=8192, c=None, s=None):
         return L.lora4_rmsnorm_forward(X, R, w, M, D, eps, H, Y, c, s, None)
-    assert fwd(M=-1) == ESHAPE and fwd(D=0) == ESHAPE and fwd(D=16385) == ESHAPE
+    assert fwd(M=-1) == ESHAPE and fwd(D=0) == ESHAPE and fwd(D=16385) == ESHAPE and fwd(D=16377) == ESHAPE
     assert fwd(eps=float("nan")) == ESHAPE and fwd(eps=-1.0) == ESHAPE
     assert fwd(X=None) == ENULL and fwd(w=None) == ENULL and fwd(Y=None) == ENULL
     assert fwd(R=None) == ENULL                        # H without a residual

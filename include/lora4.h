@@ -382,7 +382,7 @@ typedef enum {
  * rstd = 1 / sqrt(mean(h^2) + eps) of each row.
  *  X, R    : bf16 [M, D]; R may be NULL. 1 <= D <= 16384 (16376 unless a
  *            multiple of 8).
- *  weight  : bf16 [D]. eps: finite, >= 0.
+ *  weight  : bf16 [D]. eps: finite, >= 0 (0 makes a row of zeros NaN).
  *  H       : bf16 [M, D] output bf16(h), may be NULL (must be without R). May
  *            be X or R itself; no other overlap is allowed.
  *  Y       : bf16 [M, D] output (the norm is of the unrounded h), may be NULL
@@ -429,8 +429,8 @@ lora4_status lora4_rmsnorm_backward(const uint16_t *dY, const uint16_t *H, const
  *  GU      : bf16 [M, 2 N] output, G in columns 0 .. N - 1 and U in N .. 2 N - 1
  *            (kept for the backward); may be NULL.
  *  Z       : bf16 [M, 2 r] output, X Ag^T then X Au^T; may be NULL.
- *  workspace : lora4_gated_workspace_bytes(0, W, M, r) bytes (0 reports
- *            invalid arguments). Where W has several groups pass W as it is.
+ *  workspace : lora4_gated_workspace_bytes(0, W, M, r) bytes (which = 0; 1 for
+ *            the backward; 0 is returned for invalid arguments).
  * Few tokens per expert (single-token decoding, small batches) run a kernel
  * of their own. LORA4_ERR_SHAPE also for bases past 32-bit offsets within a
  * group (2 GiB of codes). M may be 0: nothing is launched. */

@@ -250,9 +250,10 @@ FfnPlan ffn_plan(const Ffn &f) {
     return o;
   };
   if (p.z_small) {
-    const int64_t chunks = K / 32;
-    p.z_splits =
-        (int)std::max<int64_t>(1, std::min(ceil_div(chunks, small::Z_WAVES * small::Z_CHUNKS), max_zsplits));
+    // ranges of one pass of loads each, while they do not fill the chip anyway
+    const int64_t chunks = K / 32, blocks = (ceil_div(M, 16) + extra) * ceil_div(R, 16);
+    p.z_splits = (int)std::max<int64_t>(
+        1, std::min({ceil_div(chunks, small::Z_WAVES * small::Z_CHUNKS), max_zsplits, 8 * cus / blocks}));
     p.z_per = ceil_div(chunks, p.z_splits);
     p.z_splits = (int)ceil_div(chunks, p.z_per);
     p.off_zpart = take((size_t)p.z_splits * M * R * 4);

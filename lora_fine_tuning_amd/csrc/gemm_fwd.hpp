@@ -745,9 +745,8 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
           }
       // (the residual pieces of U rows per lane are loaded before the first is
       // needed: one load's latency per U rows)
-      constexpr int U = EPI == EPI_FUSED ? 4 : 1;
       constexpr int ITS = PB * 32 * LPR / 64;
-      static_assert(ITS % U == 0, "whole groups");
+      constexpr int U = EPI == EPI_FUSED ? (ITS < 4 ? ITS : 4) : 1;
 #pragma unroll 1
       for (int it0 = 0; it0 < ITS; it0 += U) {
         u32x4_t rv[U];

@@ -125,9 +125,9 @@ struct Ffn {
 };
 
 // Tokens per group up to which the few-token kernel runs: one slot of it, and
-// two for one projection (14336 -> 4096, NF4, 16 tokens: 25 us against 35 with
-// the split tiles; gated, 4096 -> 14336: 39 against 36, 8192 -> 28672 MXFP4: 99
-// against 78).
+// two for one projection without groups (14336 -> 4096, NF4, 16 tokens: 25 us
+// against 39 with the split tiles; gated, 4096 -> 14336: 38 against 39,
+// 8192 -> 28672 MXFP4: 99 against 73; 16 experts of 2048 x 7168: 77 against 45).
 constexpr int64_t SMALL_ROWS = 8;
 
 // Forced schedule for tests and measurements (LORA4_FFN_ROWS): 4 or 8 the
@@ -169,15 +169,18 @@ struct TileShape {
   int rows, cols;      // per tile (gated: columns of each projection)
   bool split;
   int occ;
-  double alone, shared;
+  double alone, shared;   // 0: DEEP_STEP
 };
+// The deep tiles (fwd::deep_tile) are bound by the decode of their 256 columns,
+// on a CU of their own or not: NF4's by table lookups, the others' by conversions.
+constexpr double DEEP_STEP_NF4 = 0.75, DEEP_STEP = 0.52;
 constexpr TileShape GATED_TILES[] = {
-    {64, 128, false, 2, 0.75, 0.65},  {128, 128, false, 1, 0.95, 0.95}, {256, 128, false, 1, 1.7, 1.7},
-    {32, 128, true, 3, 0.75, 0.65},   {64, 128, true, 2, 0.75, 0.65},   {128, 128, true, 1, 0.95, 0.95},
+    {64, 128, false, 2, 0, 0}, {128, 128, false, 1, 0.95, 0.95}, {256, 128, false, 1, 1.7, 1.7},
+    {32, 128, true, 3, 0, 0},  {64, 128, true, 2, 0, 0},         {128, 128, true, 1, 0.95, 0.95},
 };
 constexpr TileShape FUSED_TILES[] = {
-    {64, 128, false, 3, 0.48, 0.38},  {128, 128, false, 2, 0.62, 0.6},  {256, 256, false, 1, 1.7, 1.7},
-    {32, 256, true, 3, 0.75, 0.65},   {64, 256, true, 2, 0.75, 0.65},   {128, 256, true, 1, 0.95, 0.95},
+    {64, 128, false, 3, 0.48, 0.38}, {128, 128, false, 2, 0.62, 0.6}, {256, 256, false, 1, 1.7, 1.7},
+    {32, 256, true, 3, 0, 0},        {64, 256, true, 2, 0, 0},        {128, 256, true, 1, 0.95, 0.95},
 };
 
 void choose_tiles(const Ffn &f, int64_t M, int pol, int64_t cus, FfnPlan &p) {
@@ -186,8 +189,15 @@ void choose_tiles(const Ffn &f, int64_t M, int pol, int64_t cus, FfnPlan &p) {
   for (const TileShape &s : f.epi == fwd::EPI_GATED ? GATED_TILES : FUSED_TILES) {
     if (pol && pol != (s.split ? 2000 : 1000) + s.rows) continue;
     const int64_t slots = ceil_div(M, s.rows) + extra, cb = ceil_div(N, s.cols);
-    // tiles with rows: a group's last one is half full on average
-    const double tiles = (double)cb * (f.E > 1 ? (double)M / s.rows + 0.5 * (double)extra : (double)ceil_div(M, s.rows));
+    // tiles with rows: one for each group, and a group's last one is half full on average
+    const double tiles = (double)cb * (f.E > 1 ? std::max((double)extra, (double)M / s.rows + 0.5 * (double)extra)
+                                               : (double)ceil_div(M, s.rows));
+    const double deep = f.W->format == LORA4_NF4 || f.W->format == LORA4_NF4_DQ ? DEEP_STEP_NF4 : DEEP_STEP;
+    double alone = s.alone > 0 ? s.alone : deep, shared = s.shared > 0 ? s.shared : deep;
+    // groups of few rows run the 256-row tiles' shorter code; the largest of
+    // uneven groups sets the pace, with about twice the mean (16 experts of
+    // 7168 x 2048, 16 rows each: 65 us; 64-row split tiles 77)
+    if (f.E > 1 && s.rows == 256 && 2 * M <= 128 * f.E) alone = shared = 2 * M <= 64 * f.E ? deep : 0.95;
     // a split: as many ranges (of at least four steps) as keep the chip full once
     int64_t per = steps, ks = 1;
     if (s.split) {
@@ -199,7 +209,7 @@ void choose_tiles(const Ffn &f, int64_t M, int pol, int64_t cus, FfnPlan &p) {
     const double blocks = tiles * (double)ks;
     const double rounds = std::ceil(blocks / (double)(s.occ * cus));
     const double each = std::max(1.0, blocks / (rounds * (double)cus));   // blocks on a CU at a time
-    const double step = s.occ == 1 ? s.alone : std::max(s.alone, each * s.shared);
+    const double step = s.occ == 1 ? alone : std::max(alone, each * shared);
     double t = rounds * (step * (double)per + 4.0);
     if (s.split) t += 6.0 + blocks * s.rows * (4 * 64 * 4) * 2 / 4.0e6;
     if (p.rows == 0 || t < best) {
@@ -227,7 +237,7 @@ FfnPlan ffn_plan(const Ffn &f) {
   const int64_t mean = ceil_div(M, f.E);
   p.ksplit = 1;
   p.split_steps = 1 << 30;
-  p.small = pol ? pol < 1000 : mean <= (f.P == 1 ? 2 : 1) * SMALL_ROWS;
+  p.small = pol ? pol < 1000 : mean <= (f.P == 1 && f.E == 1 ? 2 : 1) * SMALL_ROWS;
   int64_t max_zsplits = big::A2_MAX_PARTS;
   if (p.small) {
     p.xt = pol ? pol : mean <= 4 ? 4 : 8;

@@ -58,6 +58,11 @@ constexpr int TILE = BM * BKS;   // one X stage, bf16 elements
 
 __host__ __device__ constexpr int lds_bytes() { return STAGES * TILE * 2; }
 
+// Short tiles with an epilogue run few MFMAs per step, so the loads of a step
+// take longer than two of its steps: they keep W four steps and X five steps
+// ahead, in a ring of seven stages, where the others have two and three.
+__host__ __device__ constexpr bool deep_tile(int tbm, int nj) { return tbm == 32 || (tbm == 64 && nj == 2); }
+
 __device__ __forceinline__ int swz(int row, int chunk) { return tile64_swz(row, chunk); }
 
 // Decoded operands of one lane for one step: row j (two 32-row blocks), four
@@ -102,6 +107,9 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
   // so that several short ones share a CU
   constexpr int STG = EPI == EPI_NONE ? TILE : TBM * BKS;
   static_assert(EPI != EPI_GATED || NJ == 2, "a gated tile has a gate and an up block per wave");
+  constexpr bool DEEP = EPI != EPI_NONE && deep_tile(TBM, NJ);
+  constexpr int XA = DEEP ? 5 : 3, WA = DEEP ? 4 : 2;   // steps that X and W are loaded ahead
+  constexpr int NST = XA + 2;                           // X stages
   constexpr int WJ = EPI == EPI_GATED ? 0 : 32;     // output columns between a wave's blocks
   constexpr int WN = EPI == EPI_GATED ? 32 : 32 * NJ;   // output columns per wave
   constexpr int CPS = 8 / RB;        // hand-dealt slices per MFMA row block (8 slices per sub-step)
@@ -132,7 +140,9 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
   // X of step s into stage As, chunks 2 part .. 2 part + 1 (part 0..3)
   // steps are numbered within this block's range, which starts at step sb
   const int sb = is_split ? split * p.split_steps : 0;
-  const int Ri = (int)p.R;   // < 2^31 (the buffer offsets are 32-bit)
+  // (deep tiles end with the block's range: what they load ahead past it is zero)
+  const int Ri = DEEP && is_split ? (int)min(p.R, ((int64_t)sb + p.split_steps) * BKS)
+                                  : (int)p.R;   // < 2^31 (the buffer offsets are 32-bit)
   auto issue_a = [&](int s, uint16_t *As, int part) {
     const int k0 = (s + sb) * BKS;
     const bool edge = k0 + a_kq >= Ri;
@@ -263,11 +273,11 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16_t{};
 
   // At the mid-step wait of step s, the X of step s+1 (issued during step
-  // s-2) must have landed; still in flight may be everything issued during
-  // step s-1 and during sub-steps 0 and 1 of step s (X chunks go out two per
+  // s+1-XA) must have landed; still in flight may be everything issued during
+  // the XA-2 steps before s and during sub-steps 0 and 1 of step s (X chunks go out two per
   // sub-step from sub-step 0, W loads in sub-steps 0 .. NJ - 1). lgkmcnt 0 as
   // well.
-  constexpr int VM_OUT = (RB + W_LOADS) + ((RB < 4 ? RB : 4) + W_LOADS);
+  constexpr int VM_OUT = (XA - 2) * (RB + W_LOADS) + ((RB < 4 ? RB : 4) + W_LOADS);
   static_assert(VM_OUT < 64, "vmcnt field");
   constexpr int VMCNT = (VM_OUT & 15) | (7 << 4) | (0 << 8) | ((VM_OUT >> 4) << 14);
 
@@ -436,27 +446,27 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
     }
   };
   auto body_s = [&](int s, const uint16_t *cur, const uint16_t *nxt, uint16_t *ahead, const WRaw &rdec,
-                    WRaw &rload, const WFrag &fcur, WFrag &fnxt, u32x4_t x[RB], RunDec &d0) {
+                    const WRaw &rnext, WRaw &rload, const WFrag &fcur, WFrag &fnxt, u32x4_t x[RB], RunDec &d0) {
     RunDec d1{};
     RunBuild rb;
     WordDec wd[2];
-    // X chunks c < RB of step s + 3 go out two per sub-step, from sub-step 0
+    // X chunks c < RB of step s + XA go out two per sub-step, from sub-step 0
     auto x_chunk = [&](int c) {
-      if (c < RB) issue_a1(s + 3, ahead, c);
+      if (c < RB) issue_a1(s + XA, ahead, c);
     };
     sub_step_s(fcur, 0, x, cur, h * 4 + 1, [&](int i) {
       dec_slice(i, rdec, fnxt, d0, 0, 0, wd);
-      if (i == 0) load_w_scale(s + 2, rload, 0);
+      if (i == 0) load_w_scale(s + WA, rload, 0);
       if (i == 2) x_chunk(0);
-      if (i == 4) load_w_codes(s + 2, rload, 0);
+      if (i == 4) load_w_codes(s + WA, rload, 0);
       if (i == 6) x_chunk(1);
     });
     sub_step_s(fcur, 1, x, cur, h * 4 + 2, [&](int i) {
       dec_slice(i, rdec, fnxt, d0, 0, 2, wd);
       if (NJ > 1) run_slice(i, rdec, 1, rb, d1);
-      if (NJ > 1 && i == 0) load_w_scale(s + 2, rload, 1);
+      if (NJ > 1 && i == 0) load_w_scale(s + WA, rload, 1);
       if (i == 2) x_chunk(2);
-      if (NJ > 1 && i == 4) load_w_codes(s + 2, rload, 1);
+      if (NJ > 1 && i == 4) load_w_codes(s + WA, rload, 1);
       if (i == 6) x_chunk(3);
     });
     __builtin_amdgcn_s_waitcnt(VMCNT);
@@ -470,7 +480,7 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
     });
     sub_step_s(fcur, 3, x, nxt, h * 4 + 0, [&](int i) {
       if (NJ > 1) dec_slice(i, rdec, fnxt, d1, 1, 2, wd);
-      run_slice(i, rload, 0, rb, d0);
+      run_slice(i, rnext, 0, rb, d0);
       if (i == 2) x_chunk(6);
       if (i == 6) x_chunk(7);
     });
@@ -481,17 +491,17 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
   WRaw r0, r1;
   WFrag f0, f1;
   u32x4_t x[RB];
-  // ring of five stages; step s uses stage s % 5
-  auto stage = [&](int i) -> uint16_t * { return smem + (i >= STAGES ? i - STAGES : i) * STG; };
+  // ring of NST stages; step s uses stage s % NST
+  auto stage = [&](int i) -> uint16_t * { return smem + (i >= NST ? i - NST : i) * STG; };
 #pragma unroll
   for (int part = 0; part < 4; ++part) {
-    issue_a(0, stage(0), part);
-    issue_a(1, stage(1), part);
-    issue_a(2, stage(2), part);
+#pragma unroll
+    for (int i = 0; i < XA; ++i) issue_a(i, stage(i), part);
     load_w(0, r0, part);
   }
+  WRaw r2, r3;   // DEEP
   // ---- rank-r product (s Z) B^T first, into the zeroed accumulators: Z rows
-  // through LDS stage 4 (free until step 1 refills it), B rows to registers.
+  // through the last LDS stage (free until step 1 refills it), B rows to registers.
   // Its operand loads are issued right behind the first X and W loads, so
   // their latency overlaps. (Sub-steps whose reduction slots all lie past r2
   // are skipped: in sub-step kk lane half h holds k0 + 32 h + 8 kk ..)
@@ -499,7 +509,7 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
   // the tile's groups run as one block-diagonal product (big::TileGroups):
   // reduction column k is column k - i rp of the tile's group i.
   if (p.r2 > 0 && split == 0) {
-    uint16_t *As = stage(4);
+    uint16_t *As = stage(NST - 1);
     const bool a_vec = (p.A2.ld % 8) == 0;
     const bool b_vec = (p.B2.ld % 8) == 0;
     const int64_t row_hi = min(row0 + TBM, row_end);
@@ -604,19 +614,36 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
     decode_words(r0, f0, d, j, 2);
   }
 #pragma unroll
-  for (int part = 0; part < 4; ++part) load_w(1, r1, part);
+  for (int part = 0; part < 4; ++part) {
+    load_w(1, r1, part);
+    if constexpr (DEEP) {
+      load_w(2, r2, part);
+      load_w(3, r3, part);
+    }
+  }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
   RunDec d0 = make_run(r1, 0);
 #pragma unroll
   for (int i = 0; i < RB; ++i) x[i] = lds_read_b128(stage(0) + swz(i * 32 + l32, h * 4));
-  int s = 0, si = 0;   // si = s % 5
-  for (; s + 2 <= steps; s += 2) {
-    body_s(s, stage(si), stage(si + 1), stage(si + 3), r1, r0, f0, f1, x, d0);
-    body_s(s + 1, stage(si + 1), stage(si + 2), stage(si + 4), r0, r1, f1, f0, x, d0);
-    si = si + 2 >= STAGES ? si + 2 - STAGES : si + 2;
+  int s = 0, si = 0;   // si = s % NST
+  if constexpr (DEEP) {
+    // (NST = 7: step s + 7 is back at stage si; steps past the last multiply zeros)
+    for (; s < steps; s += 4) {
+      body_s(s, stage(si), stage(si + 1), stage(si + 5), r1, r2, r0, f0, f1, x, d0);
+      body_s(s + 1, stage(si + 1), stage(si + 2), stage(si + 6), r2, r3, r1, f1, f0, x, d0);
+      body_s(s + 2, stage(si + 2), stage(si + 3), stage(si), r3, r0, r2, f0, f1, x, d0);
+      body_s(s + 3, stage(si + 3), stage(si + 4), stage(si + 1), r0, r1, r3, f1, f0, x, d0);
+      si = si + 4 >= NST ? si + 4 - NST : si + 4;
+    }
+  } else {
+    for (; s + 2 <= steps; s += 2) {
+      body_s(s, stage(si), stage(si + 1), stage(si + 3), r1, r0, r0, f0, f1, x, d0);
+      body_s(s + 1, stage(si + 1), stage(si + 2), stage(si + 4), r0, r1, r1, f1, f0, x, d0);
+      si = si + 2 >= NST ? si + 2 - NST : si + 2;
+    }
+    if (s < steps) body_s(s, stage(si), stage(si + 1), stage(si + 3), r1, r0, r0, f0, f1, x, d0);
   }
-  if (s < steps) body_s(s, stage(si), stage(si + 1), stage(si + 3), r1, r0, f0, f1, x, d0);
   // the look-ahead loads past the end still write (zeros) into the ring, which
   // the epilogue reuses
   __builtin_amdgcn_s_waitcnt(0);
@@ -838,7 +865,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_gemm_fwd_epi(Params p) {
 // LDS of an epilogue tile: its X stages, or the fp32 sums it stages (whole
 // tiles; up to 128 rows of 64 floats per wave).
 __host__ __device__ constexpr int epi_lds_bytes(int tbm, int nj, bool split) {
-  const int x = STAGES * tbm * BKS * 2, e = split ? 0 : 4 * (tbm < 128 ? tbm : 128) * 32 * nj * 4;
+  const int x = (deep_tile(tbm, nj) ? STAGES + 2 : STAGES) * tbm * BKS * 2, e = split ? 0 : 4 * (tbm < 128 ? tbm : 128) * 32 * nj * 4;
   return x > e ? x : e;
 }
 

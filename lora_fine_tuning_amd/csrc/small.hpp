@@ -135,7 +135,7 @@ __host__ __device__ constexpr int lds_bytes(int P, int XT, int NW) { return NW *
 template <int FMT, int EPI, int XT, int NW>
 __global__ __launch_bounds__(64 * NW, 4) void k_small(Params p) {
   constexpr int P = EPI == fwd::EPI_GATED ? 2 : 1;
-    constexpr int PF = P == 2 ? 3 : 4;   // chunks in flight (one more or fewer: within 3%)
+  constexpr int PF = P == 2 ? 3 : 4;   // chunks in flight (one more or fewer: within 3%)
   constexpr int XL = XT / 4;   // X loads per chunk
   extern __shared__ __attribute__((aligned(16))) f32x4_t lds[];   // [NW][P][64] sums, then [NW][XT][16] X pieces
   // Blocks go to the XCDs in turn: the four column blocks of one 64-row block

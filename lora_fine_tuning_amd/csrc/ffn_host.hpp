@@ -171,7 +171,7 @@ struct TileShape {
   int occ;
   double alone, shared;   // 0: DEEP_STEP
 };
-// The deep tiles (fwd::deep_tile) are bound by the decode of their 256 columns,
+// The deep tiles (fwd::deep_tile) of 256 columns are bound by their decode,
 // on a CU of their own or not: NF4's by table lookups, the others' by conversions.
 constexpr double DEEP_STEP_NF4 = 0.75, DEEP_STEP = 0.52;
 constexpr TileShape GATED_TILES[] = {
@@ -179,7 +179,7 @@ constexpr TileShape GATED_TILES[] = {
     {32, 128, true, 3, 0, 0},  {64, 128, true, 2, 0, 0},         {128, 128, true, 1, 0.95, 0.95},
 };
 constexpr TileShape FUSED_TILES[] = {
-    {64, 128, false, 3, 0.48, 0.38}, {128, 128, false, 2, 0.62, 0.6}, {256, 256, false, 1, 1.7, 1.7},
+    {64, 128, false, 2, 0.55, 0.5}, {128, 128, false, 2, 0.62, 0.6}, {256, 256, false, 1, 1.7, 1.7},
     {32, 256, true, 3, 0, 0},        {64, 256, true, 2, 0, 0},        {128, 256, true, 1, 0.95, 0.95},
 };
 

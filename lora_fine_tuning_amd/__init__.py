@@ -1,5 +1,6 @@
 """Python binding of liblora4 (include/lora4.h): the unmerged-LoRA linear over
-a frozen 4-bit base (NF4, NF4 with double-quantized scales, MXFP4) on MI355X.
+a frozen 4-bit base (NF4, NF4 with double-quantized scales, MXFP4) on MI355X,
+and the operators around it in the feed-forward half of a block.
 
 This module only marshals arguments: it takes device pointers and the current
 stream from torch tensors and calls the C ABI through ctypes. Every step of the
@@ -10,7 +11,11 @@ Low-level functions carry the ABI's names and signatures (pointers as ints):
 ``lora4_forward``, ``lora4_backward``, ``lora4_workspace_bytes``,
 ``lora4_packed_bytes``, ``quant_pack_nf4``, ``quant_pack_mxfp4``. The torch-level helpers ``pack_nf4``,
 ``pack_mxfp4``, ``forward`` and ``backward`` allocate outputs with torch and call
-them.
+them; so do ``rmsnorm``, ``gated_forward`` (gate and up projections, activation
+and product) and ``forward_epilogue`` (the linear with bias, activation and
+residual), with their backward passes ``rmsnorm_backward``, ``gated_backward``
+and ``backward_epilogue``: a pre-norm block's feed-forward half is rmsnorm ->
+gated_forward -> forward_epilogue with the residual stream added.
 """
 
 import ctypes

@@ -30,6 +30,11 @@
 //
 // PF register sets of a chunk's codes, scales and X are in flight. Token rows
 // past the group's last repeat its last row (their results are not stored).
+//
+// Measured (MI355X), one token: gated 4096 -> 2 x 14336 NF4 21 us (3.2 TB/s;
+// the VALU is busy 13 us of it, and of the 896 workgroups some CUs have 4 and
+// others 3); 14336 -> 4096 NVFP4, 4 tokens, 13 us (2.5 TB/s). With k_small_z:
+// MXFP4 4096 -> 2 x 14336 18 us, 8192 -> 2 x 28672 54 to 58 us (4.3 to 4.6 TB/s).
 #pragma once
 
 #include "gemm_fwd.hpp"
@@ -65,7 +70,8 @@ struct Params {
 // Z = X A^T for few tokens: one workgroup per 16 tokens x 16 rank columns x
 // one of `splits` ranges of the reduction, its four waves taking 32-wide chunks
 // in turn, joined in LDS. The consumer adds the ranges' fp32 sums up, so a long
-// reduction costs one pass of loads instead of many in a row.
+// reduction costs one pass of loads instead of many in a row: 3 to 4 us, which
+// is a launch and two memory latencies (24 tokens, 8192 -> 128 columns: 6 us).
 // ---------------------------------------------------------------------------
 
 struct ZParams {

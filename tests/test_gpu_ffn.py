@@ -292,6 +292,36 @@ def test_experts_forward(fmt, offsets, policy, monkeypatch):
     check_epilogue(c, "gelu", True, True, run_epilogue(c, "gelu", True, True))
 
 
+# long reductions (many turns of every load-ahead ring; split ranges that end
+# inside one) and many rows (Z by the row pass, whose range partials the tiles
+# add up, or whole)
+LONG = [(24, 4160, 128, 16), (1, 8192, 48, 8), (1100, 256, 130, 8), (2100, 2048, 72, 20)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("shape", LONG)
+@pytest.mark.parametrize("policy", ["", "1064", "2032", "2064", "2128"])
+def test_long_and_tall_forward(fmt, shape, policy, monkeypatch):
+    print_case("long", fmt, shape, policy)
+    monkeypatch.setenv("LORA4_FFN_ROWS", policy)
+    c = Case(*shape, fmt, 2, seed=4)
+    check_gated(c, "silu", run_gated(c, "silu"))
+    c = Case(*shape, fmt, 1, seed=5)
+    check_epilogue(c, "gelu_tanh", True, True, run_epilogue(c, "gelu_tanh", True, True))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("policy", ["", "1064", "1256", "2064"])
+def test_tall_experts_forward(fmt, policy, monkeypatch):
+    print_case("tall experts", fmt, policy)
+    monkeypatch.setenv("LORA4_FFN_ROWS", policy)
+    offsets = [0, 20, 20, 700, 1000, 1001, 1300]
+    c = Case(offsets[-1], 256, 72, 12, fmt, 2, offsets, seed=6)
+    check_gated(c, "gelu", run_gated(c, "gelu"))
+    c = Case(offsets[-1], 256, 72, 12, fmt, 1, offsets, seed=7)
+    check_epilogue(c, "silu", True, True, run_epilogue(c, "silu", True, True))
+
+
 BWD = [((1, 256, 96, 16), None), ((70, 320, 200, 8), None), ((130, 640, 257, 4), None), ((300, 192, 515, 128), None),
        ((600, 512, 640, 40), None), ((100, 256, 130, 8), [0, 0, 37, 100]), ((460, 192, 200, 12), [0, 150, 150, 460])]
 

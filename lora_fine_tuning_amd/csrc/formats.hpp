@@ -165,12 +165,12 @@ struct PackedW {
   int64_t g_codes;        // bytes per group
   int64_t g_scales;       // scale entries per group
   int64_t g_scales2;      // second-level entries per group
-  int32_t shared;         // 1: one W for every row group (adapters over one base)
+  int32_t shared = 0;     // 1: one W for every row group (adapters over one base)
   // Two projections of one group seen as one base of 2 `half` rows (half % 64
   // == 0, each padded to whole row blocks): rows from `half` on are the second
   // projection's, whose NF4-DQ second-level scales start half_s2 entries
   // further and count from its own first row. 0: one base.
-  int64_t half, half_s2;
+  int64_t half = 0, half_s2 = 0;
 };
 
 // group of W that row group g reads

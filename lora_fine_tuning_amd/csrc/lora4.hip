@@ -270,7 +270,7 @@ struct Base {
 
 PackedW packed_of(const Base &b) {
   const lora4_W *W = b.W;
-  PackedW p;
+  PackedW p{};   // (half, half_s2: one base)
   p.codes = W->codes;
   p.scales = W->scales;
   p.scales2 = W->scales2;

@@ -27,6 +27,7 @@ namespace lora4 {
 namespace actbwd {
 
 constexpr int THREADS = 256;
+constexpr float BF16_MAX = 0x1.FEp127f;
 
 // ---------------------------------------------------------------------------
 // Gradient of the activation, and dZ
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(THREADS) void k_act_dz(DzParams p) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int rl = 32 * h + (t >> 3);
-      u32x4_t d[P], lo[P];
+      u32x4_t d[P], hi[P], lo[P];   // the gradient; its two parts for dZ
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float v0, d0, v1, d1;
@@ -134,15 +135,18 @@ __global__ __launch_bounds__(THREADS) void k_act_dz(DzParams p) {
 #pragma unroll
         for (int j = 0; j < P; ++j) {
           d[j][e] = pack_bf16x2(a[j], b[j]);
-          // (an infinite value has no remainder)
-          const float ra = a[j] - norm::lo_f32(d[j][e]), rb = b[j] - norm::hi_f32(d[j][e]);
-          lo[j][e] = pack_bf16x2(ra == ra ? ra : 0.0f, rb == rb ? rb : 0.0f);
+          // dZ's first part is at most bf16's largest value, so that the second,
+          // the rest, is finite where the gradient is (an infinite or NaN
+          // gradient shows as an infinite or NaN rest)
+          hi[j][e] = pack_bf16x2(__builtin_amdgcn_fmed3f(a[j], -BF16_MAX, BF16_MAX),
+                                 __builtin_amdgcn_fmed3f(b[j], -BF16_MAX, BF16_MAX));
+          lo[j][e] = pack_bf16x2(a[j] - norm::lo_f32(hi[j][e]), b[j] - norm::hi_f32(hi[j][e]));
         }
       }
       const int64_t row = rt.row0 + rl;
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        lds_write_b128(As[j][0] + tile64_swz(rl, t & 7), d[j]);
+        lds_write_b128(As[j][0] + tile64_swz(rl, t & 7), hi[j]);
         lds_write_b128(As[j][1] + tile64_swz(rl, t & 7), lo[j]);
         if (row < rt.row_end)
           *reinterpret_cast<u32x4_t *>(p.out + row * P * p.Np + j * p.Np + (int64_t)s * 64 + 8 * (t & 7)) = d[j];

@@ -602,9 +602,36 @@ __device__ __forceinline__ void fwd_tile(const Params &p, uint16_t *smem, const 
       u32x4_t xt[RB];
 #pragma unroll
       for (int i = 0; i < RB; ++i) xt[i] = lds_read_b128(As + swz(i * 32 + l32, h * 4));
+      if constexpr (EPI == EPI_GATED) {
+        // A sub-step's columns (8 from k in lane half 0, 8 from k + 32 in the
+        // other) enter the blocks whose half they reach, masked to that half
+        // (zeros of B alone would make NaN of the other's infinite Z).
+        const int rj = p.r2 >> 1;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        if (kk < nkk) sub_step(bt, kk, xt, As, h * 4 + kk + 1, kk < 3, [] {});
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < nkk) {
+            const int k = k0 + 8 * kk, past = (k + 32 < rc ? k + 32 : k) + 8;
+            const int n = rj - (k + 32 * h);   // this lane's first n columns are the gate's
+            u32x4_t m;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) m[w] = n >= 2 * w + 2 ? 0xFFFFFFFFu : n == 2 * w + 1 ? 0xFFFFu : 0u;
+            if (k < rj) {
+#pragma unroll
+              for (int i = 0; i < RB; ++i) acc[i][0] = mfma_32x32x16(bt.w[0][kk], xt[i] & m, acc[i][0]);
+            }
+            if (past > rj) {
+#pragma unroll
+              for (int i = 0; i < RB; ++i) acc[i][1] = mfma_32x32x16(bt.w[1][kk], xt[i] & ~m, acc[i][1]);
+            }
+            if (kk < 3)
+#pragma unroll
+              for (int i = 0; i < RB; ++i) xt[i] = lds_read_b128(As + swz(i * 32 + l32, h * 4 + kk + 1));
+          }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < nkk) sub_step(bt, kk, xt, As, h * 4 + kk + 1, kk < 3, [] {});
+      }
       if (k0 + BKS < rc) __syncthreads();   // before the next chunk restages
     }
   }

@@ -11,6 +11,7 @@
 // within the device's limits. Prints the number of launches of every kernel
 // and "ok".
 #include <cstring>
+#include <limits>
 #include <string>
 
 #include "lora4.hip"
@@ -176,7 +177,7 @@ void expect(long got, long want) {
   if (got != want) fail(context.c_str(), ("status " + std::to_string(got) + ", want " + std::to_string(want)).c_str());
 }
 
-// A call with the workspace that its size query names, and with one byte less.
+// A call with the workspace that its size query names.
 template <typename Call>
 void run(const char *what, const lora4_W &W, int64_t M, int r, size_t bytes, Call &&call) {
   context = std::string(what) + " format " + std::to_string(W.format) + " N " + std::to_string(W.N) + " K " +
@@ -266,6 +267,121 @@ void norms() {
   for (int64_t Dn : {0, 16377, 16385}) expect((long)lora4_rmsnorm_workspace_bytes(8, Dn), 0);
 }
 
+// Refused arguments of the feed-forward operators (tests/abi_driver.c has the
+// others'): one thing wrong at a time, and the status that names it.
+void refusals() {
+  uint16_t *const MIS = D + 4;   // 8-byte aligned
+  uint8_t *const u8 = reinterpret_cast<uint8_t *>(D);
+  const size_t n = (size_t)1 << 40;
+  const float inf = std::numeric_limits<float>::infinity();
+  context = "refusals of the norm";
+  auto norm = [&](uint16_t *X, uint16_t *R, uint16_t *w, int64_t M, int64_t Dn, float eps, uint16_t *H, uint16_t *Y,
+                  uint8_t *c, uint8_t *sc) {
+    return lora4_rmsnorm_forward(X, R, w, M, Dn, eps, H, Y, c, sc, nullptr);
+  };
+  expect(norm(D, D, D, -1, 256, 1e-5f, D, D, u8, u8), LORA4_ERR_SHAPE);
+  expect(norm(D, D, D, ((int64_t)1 << 31) + 1, 256, 1e-5f, D, D, u8, u8), LORA4_ERR_SHAPE);
+  expect(norm(D, D, D, 4, 0, 1e-5f, D, D, nullptr, nullptr), LORA4_ERR_SHAPE);
+  expect(norm(D, D, D, 4, 16385, 1e-5f, D, D, nullptr, nullptr), LORA4_ERR_SHAPE);
+  expect(norm(D, D, D, 4, 40, 1e-5f, D, D, u8, u8), LORA4_ERR_SHAPE);
+  expect(norm(D, D, D, 4, 256, -1e-5f, D, D, u8, u8), LORA4_ERR_SHAPE);
+  expect(norm(D, D, D, 4, 256, inf, D, D, u8, u8), LORA4_ERR_SHAPE);
+  expect(norm(nullptr, D, D, 4, 256, 1e-5f, D, D, u8, u8), LORA4_ERR_NULL);
+  expect(norm(D, nullptr, D, 4, 256, 1e-5f, D, D, u8, u8), LORA4_ERR_NULL);
+  expect(norm(D, D, nullptr, 4, 256, 1e-5f, D, D, u8, u8), LORA4_ERR_NULL);
+  expect(norm(D, D, D, 4, 256, 1e-5f, D, nullptr, nullptr, nullptr), LORA4_ERR_NULL);
+  expect(norm(D, D, D, 4, 256, 1e-5f, D, D, u8, nullptr), LORA4_ERR_NULL);
+  expect(norm(D, MIS, D, 4, 256, 1e-5f, D, D, u8, u8), LORA4_ERR_ALIGN);
+  auto norm_bwd = [&](uint16_t *dY, uint16_t *H, uint16_t *w, uint16_t *dX, uint16_t *dW, void *ws, size_t b) {
+    return lora4_rmsnorm_backward(dY, H, w, D, 4, 256, 1e-5f, dX, dW, ws, b, nullptr);
+  };
+  expect(norm_bwd(nullptr, D, D, D, D, WS, n), LORA4_ERR_NULL);
+  expect(norm_bwd(D, nullptr, D, D, D, WS, n), LORA4_ERR_NULL);
+  expect(norm_bwd(D, D, nullptr, D, D, WS, n), LORA4_ERR_NULL);
+  expect(norm_bwd(D, D, D, nullptr, D, WS, n), LORA4_ERR_NULL);
+  expect(norm_bwd(D, D, D, MIS, D, WS, n), LORA4_ERR_ALIGN);
+  expect(norm_bwd(D, D, D, D, D, nullptr, n), LORA4_ERR_WORKSPACE);
+  expect((long)lora4_rmsnorm_workspace_bytes(-1, 8), 0);
+
+  context = "refusals of the gated projections";
+  lora4_W G = base(LORA4_NF4, 1000, 512, 2);
+  auto gated = [&](const lora4_W *W, int act, uint16_t *X, int64_t M, uint16_t *A, int r, float s, const int64_t *offs,
+                   uint16_t *H, void *ws, size_t b) {
+    return lora4_gated_forward(W, act, X, M, A, D, r, s, offs, H, D, D, ws, b, nullptr);
+  };
+  auto gated_bwd = [&](const lora4_W *W, int act, uint16_t *X, int64_t M, uint16_t *A, int r, float s,
+                       const int64_t *offs, uint16_t *dH, void *ws, size_t b) {
+    return lora4_gated_backward(W, act, X, dH, D, M, A, D, r, s, offs, D, D, D, D, ws, b, nullptr);
+  };
+  auto both = [&](auto &&call) {
+    expect(call(nullptr, 1, D, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_NULL);
+    expect(call(&G, 4, D, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_FORMAT);
+    expect(call(&G, -1, D, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_FORMAT);
+    expect(call(&G, 1, D, -1, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_SHAPE);
+    expect(call(&G, 1, D, 16, D, 0, 1.0f, nullptr, D, WS, n), LORA4_ERR_SHAPE);
+    expect(call(&G, 1, D, 16, D, 129, 1.0f, nullptr, D, WS, n), LORA4_ERR_SHAPE);
+    expect(call(&G, 1, D, 16, D, 16, inf, nullptr, D, WS, n), LORA4_ERR_SHAPE);
+    expect(call(&G, 1, D, 16, D, 16, 1.0f, OFFS, D, WS, n), LORA4_ERR_SHAPE);
+    expect(call(&G, 1, nullptr, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_NULL);
+    expect(call(&G, 1, D, 16, nullptr, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_NULL);
+    expect(call(&G, 1, D, 16, D, 16, 1.0f, nullptr, nullptr, WS, n), LORA4_ERR_NULL);
+    expect(call(&G, 1, D, 16, MIS, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_ALIGN);
+    expect(call(&G, 1, D, 16, D, 16, 1.0f, nullptr, D, nullptr, n), LORA4_ERR_WORKSPACE);
+    expect(call(&G, 1, D, 16, D, 16, 1.0f, nullptr, D, MIS, n), LORA4_ERR_ALIGN);
+    lora4_W bad = G;
+    bad.groups = 3;
+    expect(call(&bad, 1, D, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_SHAPE);
+    bad.groups = 4;
+    expect(call(&bad, 1, D, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_NULL);
+    bad.groups = 0;
+    expect(call(&bad, 1, D, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_SHAPE);
+    bad = G;
+    bad.format = 9;
+    expect(call(&bad, 1, D, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_FORMAT);
+    bad = base(LORA4_NF4, (int64_t)1 << 26, 64, 2);   // 2 GiB of codes a group
+    expect(call(&bad, 1, D, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_SHAPE);
+    bad = base(LORA4_NF4_DQ, 1000, 512, 2);
+    bad.scales2 = nullptr;
+    expect(call(&bad, 1, D, 16, D, 16, 1.0f, nullptr, D, WS, n), LORA4_ERR_NULL);
+  };
+  both(gated);
+  both(gated_bwd);
+  expect((long)lora4_gated_workspace_bytes(2, &G, 16, 16), 0);
+  expect((long)lora4_gated_workspace_bytes(0, nullptr, 16, 16), 0);
+  expect((long)lora4_gated_workspace_bytes(1, &G, 16, 129), 0);
+
+  context = "refusals of the linear with an epilogue";
+  lora4_W W = base(LORA4_NVFP4, 1000, 512, 1);
+  auto fwd = [&](int act, int64_t M, int r, const int64_t *offs, uint16_t *bias, uint16_t *R, uint16_t *Y, void *ws,
+                 size_t b) {
+    return lora4_forward_epilogue(&W, act, D, M, D, D, r, 1.0f, offs, bias, R, Y, D, D, ws, b, nullptr);
+  };
+  expect(fwd(7, 16, 16, nullptr, D, D, D, WS, n), LORA4_ERR_FORMAT);
+  expect(fwd(2, 16, 257, nullptr, D, D, D, WS, n), LORA4_ERR_SHAPE);
+  expect(fwd(2, -1, 16, nullptr, D, D, D, WS, n), LORA4_ERR_SHAPE);
+  expect(fwd(2, 16, 16, OFFS, D, D, D, WS, n), LORA4_ERR_SHAPE);
+  expect(fwd(2, 16, 16, nullptr, MIS, D, D, WS, n), LORA4_ERR_ALIGN);
+  expect(fwd(2, 16, 16, nullptr, D, MIS, D, WS, n), LORA4_ERR_ALIGN);
+  expect(fwd(2, 16, 16, nullptr, D, D, nullptr, WS, n), LORA4_ERR_NULL);
+  expect(fwd(2, 16, 16, nullptr, D, D, D, WS, 16), LORA4_ERR_WORKSPACE);
+  auto bwd = [&](int act, uint16_t *P, uint16_t *dA, uint16_t *db, void *ws, size_t b) {
+    return lora4_backward_epilogue(&W, act, D, D, P, 16, D, D, 16, 1.0f, nullptr, nullptr, D, dA, D, db, ws, b,
+                                   nullptr);
+  };
+  for (int act : {LORA4_ACT_NONE, LORA4_ACT_SILU}) {
+    expect(bwd(act, D, nullptr, D, WS, n), LORA4_ERR_NULL);
+    expect(bwd(act, D, D, MIS, WS, n), LORA4_ERR_ALIGN);
+    expect(bwd(act, D, D, D, nullptr, n), LORA4_ERR_WORKSPACE);
+    expect(bwd(act, D, D, D, WS, 16), LORA4_ERR_WORKSPACE);
+    expect(bwd(act, D, D, D, MIS, n), LORA4_ERR_ALIGN);
+  }
+  expect(bwd(LORA4_ACT_SILU, nullptr, D, D, WS, n), LORA4_ERR_NULL);
+  expect(bwd(9, D, D, D, WS, n), LORA4_ERR_FORMAT);
+  expect((long)lora4_epilogue_workspace_bytes(0, nullptr, 16, 16), 0);
+  expect((long)lora4_epilogue_workspace_bytes(-1, &W, 16, 16), 0);
+  expect((long)lora4_epilogue_workspace_bytes(0, &W, 16, 257), 0);
+}
+
 // Size queries over the ends of their ranges (no call: nothing that large
 // exists), where an overflow of the planning's arithmetic would show.
 void sizes() {
@@ -318,6 +434,7 @@ int main() {
     if (f[0]) unsetenv(f[0]);
   }
   norms();
+  refusals();
   sizes();
   for (const auto &c : counts) std::printf("%s %d\n", c.first.c_str(), c.second);
   if (failures) return 1;

@@ -5,7 +5,8 @@ The sources are compiled for the host alone, against a stand-in HIP runtime
 with AddressSanitizer and UndefinedBehaviorSanitizer, and with uninitialised
 variables filled with a pattern (-ftrivial-auto-var-init) that must reach no
 kernel. The driver calls the layer and the feed-forward operators over shapes,
-formats and forced paths, and their size queries over the ends of the ranges.
+formats and forced paths, the feed-forward operators with arguments that they
+refuse, and their size queries over the ends of the ranges.
 """
 
 import os
@@ -45,3 +46,12 @@ def test_every_launch_gets_whole_parameters(driver):
     for k in ("k_gemm_fwd_epi", "k_gemm_fwd_split", "k_epi_reduce", "k_small", "k_small_z", "k_act_dz", "k_col_part",
               "k_col_sum_slots", "k_gemm_dgrad", "k_gemm_nn", "k_gemm_tn2", "k_rmsnorm_fwd", "k_rmsnorm_bwd"):
         assert re.search(r"\d%s" % k, res.stdout), k
+
+
+def test_every_entry_point_runs_under_sanitizers():
+    """Each exported name is called by one of the two sanitized drivers."""
+    calls = ""
+    for name in ("abi_driver.c", "launch_driver.cpp"):
+        with open(os.path.join(TESTS, name)) as f:
+            calls += re.sub(r"/\*.*?\*/|//[^\n]*", "", f.read(), flags=re.S)
+    assert [e for e in L.EXPORTS if not re.search(r"\b%s\(" % e, calls)] == []

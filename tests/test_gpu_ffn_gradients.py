@@ -76,3 +76,57 @@ def test_infinite_gradient(value):
     assert torch.equal(dA.isnan(), (sign * value).isnan())
     if value == value:
         assert torch.equal(dA, torch.sign(sign) * value)
+
+
+@pytest.mark.parametrize("pairs", [1, 20, 48])
+def test_dz_keeps_what_bf16_drops(pairs):
+    """Gradients that round to the same bf16 value and meet B's rows +1 and -1: the
+    rounded parts cancel and dZ is what the rounding dropped. Gated, without an
+    activation: dG = dH U is 129^2 2^-14 = 1 + 2^-6 + 2^-14 against 130 2^-7 =
+    1 + 2^-6, both exact in fp32 and both 1 + 2^-6 in bf16."""
+    print_case("dropped", pairs)
+    N, K, r = 96, 128, 8
+    c = Case(1, K, N, r, synth.NF4, 2, seed=10)
+    dH, U, B = np.zeros((1, N)), np.zeros((1, N)), np.zeros((2, N, r))
+    for i in range(pairs):
+        dH[0, 2 * i:2 * i + 2] = 129 / 128, 130 / 128
+        U[0, 2 * i:2 * i + 2] = 129 / 128, 1.0
+        B[0, 2 * i], B[0, 2 * i + 1] = 1.0, -1.0
+    X, A, _, _ = c.dev("X", "A", "B", "dY")
+    GU, Z = np.concatenate([np.zeros((1, N)), U], 1), np.zeros((1, 2 * r))
+    o = L.gated_backward(c.base, X, to_dev(bf16(dH)), to_dev(bf16(GU)), A, to_dev(bf16(B)), 1.0, activation="none",
+                         Z=to_dev(bf16(Z)))
+    # every product and sum is exact; dA = dZ^T X is rounded once
+    want = pairs * 2.0 ** -14 * f64(c.X)[0]
+    got = f64(to_host(o["dA"]))
+    assert np.array_equal(got[0], np.broadcast_to(f64(bf16(want)), (r, K)))
+    assert not got[1].any()
+
+
+def test_dz_keeps_what_bf16_drops_behind_an_activation():
+    """The same for one projection: two slopes of SiLU that differ and round alike."""
+    N, K, r = 96, 128, 8
+    c = Case(1, K, N, r, synth.NF4, 1, seed=11)
+    p = f64(np.arange(0x4000, 0x4080, dtype=np.uint16))          # bf16 values of 2 to 4
+    d = ffn.act(p, "silu")[1]
+    q = f64(bf16(d))
+    # (in [1, 1.1]; far from the middle between two bf16 values, which fp32 could round otherwise)
+    safe = np.abs(d - q) < 2.0 ** -8 - 2.0 ** -16
+    i, j = max(((i, j) for i in range(len(p)) for j in range(len(p)) if safe[i] and safe[j] and q[i] == q[j]),
+               key=lambda t: d[t[0]] - d[t[1]])
+    diff = d[i] - d[j]
+    assert diff > 2.0 ** -10
+    pre, B = np.empty((1, N)), np.empty((N, r))
+    pre[0, ::2], pre[0, 1::2] = p[i], p[j]
+    B[::2], B[1::2] = 1.0, -1.0
+    X, A = c.dev("X", "A")
+    o = L.backward_epilogue(c.base, X, torch.ones((1, N), dtype=torch.bfloat16, device=X.device), A, to_dev(bf16(B)),
+                            1.0, P=to_dev(bf16(pre)), activation="silu", Z=torch.zeros((1, r), dtype=torch.bfloat16,
+                                                                                      device=X.device))
+    got, x = f64(to_host(o["dA"])), f64(c.X)[0]
+    # per pair: the remainders (at most 2^-8) rounded to bf16, 2^-17 each, and the
+    # fp32 slopes, within 2^-21 each; then dZ's and dA's own roundings, 2^-8 each
+    ref = N // 2 * diff * x
+    bound = N // 2 * 2 * (2.0 ** -17 + 2.0 ** -21) * np.abs(x) * (1 + 2.0 ** -6) + 2.01 * 2.0 ** -8 * np.abs(ref)
+    assert np.all(np.abs(got - ref) <= bound)
+    assert np.all(bound < 0.25 * np.abs(ref) + (x == 0))         # (dropping the remainders would miss it)

@@ -390,8 +390,11 @@ typedef enum {
  *  codes, scales_e8m0 : the MXFP8 form of Y, uint8 [M, D] and [M, D / 32], bit
  *            for bit what quant_pack_mxfp8 gives for the bf16 Y; both or
  *            neither, D % 32 == 0.
+ *            The codes are an output like Y: lora4_forward_mx takes bf16 and
+ *            quantizes it itself.
  * The sum of squares is held in fp32: a row with |h| past about 1e19 is out of
- * its range. Infinities and NaNs make their own row's outputs non-finite.
+ * its range. A NaN makes its row of Y NaN; an infinite h makes its own element
+ * NaN and the row's others zero (rstd is 0). Other rows are untouched.
  * M may be 0. Errors: LORA4_ERR_SHAPE, LORA4_ERR_NULL, LORA4_ERR_ALIGN,
  * LORA4_ERR_HIP. */
 lora4_status lora4_rmsnorm_forward(const uint16_t *X, const uint16_t *R, const uint16_t *weight, int64_t M,
@@ -432,7 +435,9 @@ lora4_status lora4_rmsnorm_backward(const uint16_t *dY, const uint16_t *H, const
  *  workspace : lora4_gated_workspace_bytes(0, W, M, r) bytes (which = 0; 1 for
  *            the backward; 0 is returned for invalid arguments).
  * Few tokens per expert (single-token decoding, small batches) run a kernel
- * of their own. LORA4_ERR_SHAPE also for bases past 32-bit offsets within a
+ * of their own. As in lora4_forward, s Z is rounded to bf16 for its product with
+ * B. An infinity or NaN in one projection's A, B or Z stays out of the other's G
+ * or U, and one in a token's row of X out of the other tokens. LORA4_ERR_SHAPE also for bases past 32-bit offsets within a
  * group (2 GiB of codes). M may be 0: nothing is launched. */
 size_t lora4_gated_workspace_bytes(int which, const lora4_W *W, int64_t M, int32_t r);
 lora4_status lora4_gated_forward(const lora4_W *W, int32_t activation, const uint16_t *X, int64_t M,
@@ -441,8 +446,9 @@ lora4_status lora4_gated_forward(const lora4_W *W, int32_t activation, const uin
                                  void *workspace, size_t workspace_bytes, void *stream);
 
 /* Backward of the gated projections, from dH and the saved GU:
- *   dG = dH U act'(G), dU = dH act(G)   (rounded to bf16 for the products)
- *   dZg = s dG Bg, dX = dG deq(Wg) + dU deq(Wu) + dZg Ag + dZu Au,
+ *   dG = dH U act'(G), dU = dH act(G)   (rounded to bf16 for dX and dB)
+ *   dZg = s dG Bg                       (of the unrounded dG; rounded to bf16)
+ *   dX = dG deq(Wg) + dU deq(Wu) + dZg Ag + dZu Au,
  *   dAg = dZg^T X, dBg = s dG^T Zg, and the same for the up projection.
  *  GU      : bf16 [M, 2 N] from lora4_gated_forward.
  *  Z       : bf16 [M, 2 r] from it, or NULL to recompute.
@@ -472,8 +478,9 @@ lora4_status lora4_forward_epilogue(const lora4_W *W, int32_t activation, const 
                                     uint16_t *Y, uint16_t *P, uint16_t *Z, void *workspace, size_t workspace_bytes,
                                     void *stream);
 
-/* Its backward: dP = dY act'(P) (rounded to bf16 for the products), dbias =
- * the column sums of dP, and dX, dA, dB of lora4_backward for dP. The
+/* Its backward: dP = dY act'(P) (rounded to bf16 for dX and dB; dbias and dZ are
+ * made from the unrounded dP, dZ is rounded to bf16), dbias = the column sums of
+ * dP, and dX, dA, dB of lora4_backward for dP. The
  * residual's gradient is dY itself.
  *  P     : bf16 [M, N] from lora4_forward_epilogue; may be NULL without an
  *          activation.

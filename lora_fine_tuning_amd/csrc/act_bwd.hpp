@@ -10,8 +10,9 @@
 //  k_col_part  : the column sums of dY (dbias where there is no activation).
 //
 // All are HBM-bound (gated: 6 bytes read and 4 written per element of dH).
-// Measured (MI355X): gated 4096 x 14336, rank 16, 113 us for 587 MB (5.2 TB/s);
-// one projection 2048 x 4096 with GELU, dbias and rank 32 23 us.
+// Measured (MI355X): gated 4096 x 14336, rank 16, 112 to 115 us for 587 MB (5.2
+// TB/s); one projection 2048 x 4096 with GELU, dbias and rank 32 23 us (50 MB: its
+// 32 row slots are cut into 32 ranges of two steps, mostly prologue and epilogue).
 // dG, dU and dP are rounded to bf16 because the large matrix products that
 // follow take bf16 operands. The rank-r products take the rounding's remainder
 // as a second bf16 operand too (two MFMAs for one, of which there are few), so

@@ -81,7 +81,8 @@ struct WRaw {
 // second-level scales have to know. SPLIT: block b computes reduction range
 // b % ksplit (p.split_steps steps; the rank-r tail with range 0) of tile
 // b / ksplit and writes fp32 sums to p.Cpart [range][M][Nc] (NF4 4096 x 4096,
-// 2048 rows: 77 us and 14 us for the sum, against 137 with the 128 x 128 kernel).
+// 2048 rows: 75 us and 13 us for the sum, against 137 with the 128 x 128 kernel;
+// the range's start costs registers: these four spill 32, the others none).
 template <int FMT, bool SHARED, bool HALVES = false, bool SPLIT = false>
 __global__ __launch_bounds__(THREADS, 1) void k_gemm_dgrad(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];

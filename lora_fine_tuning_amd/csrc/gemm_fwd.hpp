@@ -60,9 +60,10 @@ __host__ __device__ constexpr int lds_bytes() { return STAGES * TILE * 2; }
 
 // Short tiles with an epilogue run few MFMAs per step, so the loads of a step
 // take longer than two of its steps: they keep W four steps and X five steps
-// ahead, in a ring of seven stages, where the others have two and three (gated,
-// MXFP4 8192 x 28672, 24 rows: 60 against 66 us; 16 experts of 7168 x 2048, 128
-// rows each: 140 against 168). With 128 rows it changes nothing.
+// ahead, in a ring of seven stages, where the others have two and three. Measured
+// in turn: gated, MXFP4 8192 x 28672, 24 rows, split tiles 60 against 66 us; 16
+// experts of 7168 x 2048, 128 rows each, 140 against 168 (140 to 151 over several
+// cards). With 128 rows it changes nothing.
 __host__ __device__ constexpr bool deep_tile(int tbm) { return tbm <= 64; }
 
 __device__ __forceinline__ int swz(int row, int chunk) { return tile64_swz(row, chunk); }
@@ -872,9 +873,9 @@ __device__ __forceinline__ void fwd_whole_tile(const Params &p, uint16_t *smem, 
 // A tile with one of the epilogues, TBM rows x 256 (NJ 2; gated: 128) or 128
 // (NJ 1) columns, in grouped tile order over p.nslots row slots of TBM rows.
 // SHORT (TBM 256): short last row tiles of a group run the shorter code.
-// Bound by the tile's core as the plain layer's forward (4096 tokens, NF4:
-// gated 4096 -> 2 x 14336 835 us with G and U written, 806 without, the two
-// plain forwards 810; 14336 -> 4096 with the residual 395 us, plain 385), and
+// Bound by the tile's core as the plain layer's forward (4096 tokens, NF4, in
+// one run: gated 4096 -> 2 x 14336 826 us, the two plain forwards 819, with G and
+// U written 844 to 872; 14336 -> 4096 with the residual 389 us, plain 377), and
 // with short tiles by the decode and the latency of a step.
 template <int FMT, int EPI, int TBM, int NJ, bool SHORT>
 __global__ __launch_bounds__(THREADS, 1) void k_gemm_fwd_epi(Params p) {

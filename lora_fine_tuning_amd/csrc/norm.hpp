@@ -12,12 +12,14 @@
 // registers of its threads (a wave, or a whole block; VPT vectors of 8
 // elements each) between the sums and the outputs. The sums of the forward run
 // over the unrounded fp32 h = x + res; Y is rounded once. The MXFP8 codes are
-// those of the rounded Y, as quant_pack_mxfp8 gives them, so that the base
-// product (MXFP8) and the adapter (bf16 Y) of a layer read one value.
+// those of the rounded Y, as quant_pack_mxfp8 gives them, so that both outputs
+// stand for one value (the MX-native forward does not read them: it takes bf16
+// and quantizes it into an order of its own).
 //
-// Measured (MI355X): forward 4096 x 4096 21 us (6.3 TB/s), 8192 x 8192 with H,
-// Y and MXFP8 108 us (5.6 TB/s), one row of 4096 2.8 us; backward with dH and
-// dW 4096 x 4096 30 us (4.4 TB/s; 21 us without dW), 4097 x 5003 50 us.
+// Measured (MI355X): forward 4096 x 4096 with H 22 us (6.0 TB/s), 8192 x 8192
+// with H, Y and MXFP8 108 us (5.6 TB/s), one row of 4096 2.8 us; backward with
+// dH 4096 x 4096 23 us, with dW too 28 us and 4 for the sum of its partials
+// (4.2 TB/s), 8192 x 8192 106 and 5 (4.8 TB/s), 4097 x 5003 50 to 54 us.
 //
 // Rows of any length: a row of D % 8 != 0 elements starts at an address that
 // is a multiple of 2 only. The forward issues its 16-byte accesses there all
@@ -221,7 +223,8 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 64 * MAX_WAVES) void k_rmsn
 // EDGE (D % 8 != 0): rows of one block are a multiple of 8 apart (or there is
 // one), so that the shift of their aligned vectors, and with it a thread's
 // columns, are the same for all; the neighbouring rows' elements in the first
-// and the last vector are masked out and not written.
+// and the last vector are masked out and not written. (The widest of these with
+// dW, blocks of 16 waves, spills 37 registers: 128 are all that 16 waves leave.)
 template <bool WAVE, int VPT, bool DW, int MAXW, bool EDGE>
 __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 64 * MAXW) void k_rmsnorm_bwd(BwdParams p) {
   __shared__ float red[2][MAX_WAVES][2];

@@ -31,10 +31,11 @@
 // PF register sets of a chunk's codes, scales and X are in flight. Token rows
 // past the group's last repeat its last row (their results are not stored).
 //
-// Measured (MI355X), one token: gated 4096 -> 2 x 14336 NF4 21 us (3.2 TB/s;
+// Measured (MI355X), one token: gated 4096 -> 2 x 14336 NF4 22 us (3.0 TB/s;
 // the VALU is busy 13 us of it, and of the 896 workgroups some CUs have 4 and
-// others 3); 14336 -> 4096 NVFP4, 4 tokens, 13 us (2.5 TB/s). With k_small_z:
-// MXFP4 4096 -> 2 x 14336 18 us, 8192 -> 2 x 28672 54 to 58 us (4.3 to 4.6 TB/s).
+// others 3), MXFP4 14 us (4.5 TB/s), 8192 -> 2 x 28672 48 us (5.2 TB/s); one
+// projection, 14336 -> 4096 NVFP4, 4 tokens, 13 us (2.5 TB/s: as many bytes of X
+// as of codes). k_small_z in front of each takes 4 us.
 #pragma once
 
 #include "gemm_fwd.hpp"

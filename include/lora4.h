@@ -435,10 +435,11 @@ lora4_status lora4_rmsnorm_backward(const uint16_t *dY, const uint16_t *H, const
  *  workspace : lora4_gated_workspace_bytes(0, W, M, r) bytes (which = 0; 1 for
  *            the backward; 0 is returned for invalid arguments).
  * Few tokens per expert (single-token decoding, small batches) run a kernel
- * of their own. As in lora4_forward, s Z is rounded to bf16 for its product with
- * B. An infinity or NaN in one projection's A, B or Z stays out of the other's G
- * or U, and one in a token's row of X out of the other tokens. LORA4_ERR_SHAPE also for bases past 32-bit offsets within a
- * group (2 GiB of codes). M may be 0: nothing is launched. */
+ * of their own. As in lora4_forward, s Z is rounded to bf16 for its product
+ * with B. An infinity or NaN in one projection's A, B or Z stays out of the
+ * other's G or U, and one in a token's row of X out of the other tokens.
+ * LORA4_ERR_SHAPE also for bases past 32-bit offsets within a group (2 GiB of
+ * codes). M may be 0: nothing is launched. */
 size_t lora4_gated_workspace_bytes(int which, const lora4_W *W, int64_t M, int32_t r);
 lora4_status lora4_gated_forward(const lora4_W *W, int32_t activation, const uint16_t *X, int64_t M,
                                  const uint16_t *A, const uint16_t *B, int32_t r, float s,
@@ -478,10 +479,10 @@ lora4_status lora4_forward_epilogue(const lora4_W *W, int32_t activation, const 
                                     uint16_t *Y, uint16_t *P, uint16_t *Z, void *workspace, size_t workspace_bytes,
                                     void *stream);
 
-/* Its backward: dP = dY act'(P) (rounded to bf16 for dX and dB; dbias and dZ are
- * made from the unrounded dP, dZ is rounded to bf16), dbias = the column sums of
- * dP, and dX, dA, dB of lora4_backward for dP. The
- * residual's gradient is dY itself.
+/* Its backward: dP = dY act'(P) (rounded to bf16 for dX and dB; dbias and dZ
+ * are made from the unrounded dP, dZ is rounded to bf16), dbias = the column
+ * sums of dP, and dX, dA, dB of lora4_backward for dP. The residual's gradient
+ * is dY itself.
  *  P     : bf16 [M, N] from lora4_forward_epilogue; may be NULL without an
  *          activation.
  *  dbias : bf16 [groups][N] output, or NULL.

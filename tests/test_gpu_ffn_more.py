@@ -258,3 +258,31 @@ def test_two_calls_at_once():
     for i in (0, 1):
         for outs in got[i]:
             assert all(torch.equal(x, y) for x, y in zip(outs, want[i]))
+
+
+@pytest.mark.parametrize("double_quant", [False, True])
+def test_joint_base_past_32_bit_offsets(double_quant):
+    """Projections whose bases together pass 2 GiB of codes: dX of the gated backward is the
+    sum of the plain layer's over each base."""
+    M, K, N, r = 8, 8192, 262272, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s, std=1.0: (torch.randn(s, generator=g, device="cuda") * std).to(torch.bfloat16)
+    base = L.pack_nf4(rand(2, N, K, std=0.05), double_quant=double_quant)
+    assert base.codes.numel() > 1 << 31
+    X, A, B, dH, GU = rand(M, K), rand(2, r, K, std=K ** -0.5), rand(2, N, r, std=0.01), rand(M, N), rand(M, 2 * N)
+    Z = rand(M, 2 * r)
+    o = L.gated_backward(base, X, dH, GU, A, B, 1.0, activation="none", Z=Z)
+    grads = [(dH.float() * GU[:, (1 - j) * N:(2 - j) * N].float()).to(torch.bfloat16) for j in (0, 1)]
+    dX, inter = np.zeros((M, K)), np.zeros((M, K))
+    for j, d in enumerate(grads):
+        one = L.PackedBase(base.fmt, N, K, 1, base.codes[j], base.scales[j],
+                           base.scales2[j] if double_quant else None)
+        b = L.backward(one, X, d, A[j], B[j], 1.0, Z=Z[:, j * r:(j + 1) * r].contiguous())
+        h = f64(to_host(b["dX"]))
+        dX += h
+        # the plain results' own rounding, and dZ: there of the rounded gradient (off by
+        # at most 2^-8 of each term), and rounded itself on both sides
+        dz = d.double().abs() @ B[j].double().abs() + 2 * (d.double() @ B[j].double()).abs()
+        inter += np.abs(h) + (dz @ A[j].double().abs()).cpu().numpy()
+        compare_full("dB", f64(to_host(o["dB"][j])), f64(to_host(b["dB"])), np.abs(f64(to_host(b["dB"]))))
+    compare_full("dX", f64(to_host(o["dX"])), dX, inter)

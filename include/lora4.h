@@ -494,6 +494,77 @@ lora4_status lora4_backward_epilogue(const lora4_W *W, int32_t activation, const
                                      uint16_t *dA, uint16_t *dB, uint16_t *dbias, void *workspace,
                                      size_t workspace_bytes, void *stream);
 
+/* ---- Attention ----------------------------------------------------------------
+ * Causal attention between the query, key and value projections and the output
+ * projection of a block: packed sequences of different lengths, grouped heads,
+ * whole prompts, chunks and single tokens over a cache. Sequence i has Lq
+ * queries and Lk keys; its query a sees the keys b <= a + Lk - Lq (the last
+ * query sees every key), and per query head
+ *   S = scale Q K^T,  P = softmax of S over the visible keys,  O = P V,
+ *   lse = log of the sum of exp S over them.
+ * A query that sees no key (Lk < Lq, or no keys at all) has O = 0 and
+ * lse = -infinity, and no gradient.
+ *  Tq, Tk   : rows (tokens) of Q and O, and of K and V; 0 is allowed. 1 <= seqs.
+ *  Hq, Hkv  : query heads and key heads, Hq a multiple of Hkv, at most 64 query
+ *             heads to a key head (G = Hq / Hkv; head h reads key head h / G).
+ *  D        : elements of a head, a multiple of 8 up to 128.
+ *  scale    : finite, > 0.
+ *  ldq, ldk, ldv : elements between the tokens of Q, K and V (multiples of 8,
+ *             at least Hq D, Hkv D and Hkv D): the heads of a token are
+ *             contiguous, and q, k and v may be columns of one projection's output.
+ *  q_offsets, k_offsets : DEVICE int64 [seqs + 1], non-decreasing row offsets:
+ *             sequence i has the rows [i] .. [i + 1] - 1. k_offsets NULL: the
+ *             q_offsets (Tk == Tq). Both NULL: seqs == 1, all rows.
+ *  k_lengths : DEVICE int64 [seqs] or NULL: only the first k_lengths[i] of
+ *             sequence i's key rows are keys (a cache's filled part; at most
+ *             the rows that k_offsets gives it).
+ * Offsets and lengths are held inside the tensors whatever they say. Rows
+ * behind the last sequence (and before the first), and key rows past
+ * k_lengths, are neither read nor written, in outputs and gradients alike. An
+ * infinity or NaN of one sequence stays out of the others; inside its sequence
+ * it may reach queries that do not see it (a masked score is exact, but
+ * 0 times infinity in its product is not 0). */
+typedef struct lora4_attn {
+  int64_t Tq, Tk, seqs;
+  int32_t Hq, Hkv, D;
+  float scale;
+  int64_t ldq, ldk, ldv;
+  const int64_t *q_offsets, *k_offsets, *k_lengths;
+} lora4_attn;
+
+/* Workspace (bytes) of lora4_attention_forward (which = 0) or _backward (1).
+ * Returns 0 for invalid arguments. */
+size_t lora4_attention_workspace_bytes(int which, int64_t Tq, int64_t Tk, int64_t seqs, int32_t Hq, int32_t Hkv,
+                                       int32_t D);
+
+/* Forward.
+ *  Q : bf16 [Tq][Hq][D], K, V : bf16 [Tk][Hkv][D], with the token strides above.
+ *  O : bf16 [Tq][Hq][D] output, dense.
+ *  lse : fp32 [Tq][Hq] output (kept for the backward), may be NULL.
+ *  workspace : lora4_attention_workspace_bytes(0, ..) bytes.
+ * P is rounded to bf16 for its product with V; scores, maxima and sums are
+ * fp32. Tokens' K and V are read once for the G query heads of their key head;
+ * few queries over many keys split the keys over workgroups. The same inputs
+ * give the same bits on every call. Errors: LORA4_ERR_NULL, LORA4_ERR_SHAPE,
+ * LORA4_ERR_ALIGN, LORA4_ERR_WORKSPACE, LORA4_ERR_HIP;
+ * LORA4_ERR_UNIMPLEMENTED for D > 128. */
+lora4_status lora4_attention_forward(const lora4_attn *attn, const uint16_t *Q, const uint16_t *K, const uint16_t *V,
+                                     uint16_t *O, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward: with delta = sum over the columns of dO O, P = exp(S - lse) and
+ * dS = P (dO V^T - delta),
+ *   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
+ * (dK and dV summed over the G query heads). P and dS are rounded to bf16 for
+ * their products; sums are fp32, in a fixed order.
+ *  O, lse : from lora4_attention_forward. dO : bf16 [Tq][Hq][D], dense.
+ *  dQ, dK, dV : bf16 outputs with token strides lddq, lddk, lddv (as ldq .. ldv).
+ *             A sequence without queries has dK = dV = 0.
+ *  workspace : lora4_attention_workspace_bytes(1, ..) bytes. */
+lora4_status lora4_attention_backward(const lora4_attn *attn, const uint16_t *Q, const uint16_t *K, const uint16_t *V,
+                                      const uint16_t *O, const float *lse, const uint16_t *dO, uint16_t *dQ,
+                                      uint16_t *dK, uint16_t *dV, int64_t lddq, int64_t lddk, int64_t lddv,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
 /* A static, human-readable name for a status code. */
 const char *lora4_status_string(lora4_status status);
 

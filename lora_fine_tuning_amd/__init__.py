@@ -38,6 +38,7 @@ EXPORTS = ["lora4_forward", "lora4_forward_noalloc", "lora4_backward", "lora4_wo
            "lora4_rmsnorm_workspace_bytes", "lora4_rmsnorm_forward", "lora4_rmsnorm_backward",
            "lora4_gated_workspace_bytes", "lora4_gated_forward", "lora4_gated_backward",
            "lora4_epilogue_workspace_bytes", "lora4_forward_epilogue", "lora4_backward_epilogue",
+           "lora4_attention_workspace_bytes", "lora4_attention_forward", "lora4_attention_backward",
            "lora4_status_string", "lora4_timing_enable", "lora4_timing_collect", "lora4_version"]
 
 
@@ -51,6 +52,13 @@ class lora4_W(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int32), ("block", ctypes.c_int32), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("groups", ctypes.c_int64), ("codes", ctypes.c_void_p),
                 ("scales", ctypes.c_void_p), ("scales2", ctypes.c_void_p)]
+
+
+class lora4_attn(ctypes.Structure):
+    _fields_ = [("Tq", ctypes.c_int64), ("Tk", ctypes.c_int64), ("seqs", ctypes.c_int64), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("scale", ctypes.c_float), ("ldq", ctypes.c_int64),
+                ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64), ("q_offsets", ctypes.c_void_p),
+                ("k_offsets", ctypes.c_void_p), ("k_lengths", ctypes.c_void_p)]
 
 
 class lora4_kernel_time(ctypes.Structure):
@@ -122,6 +130,13 @@ def lib():
         L.lora4_backward_epilogue.argtypes = [Wp, i32, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp,
                                               sz, vp]
         L.lora4_backward_epilogue.restype = ctypes.c_int
+        Ap = ctypes.POINTER(lora4_attn)
+        L.lora4_attention_workspace_bytes.argtypes = [ctypes.c_int, i64, i64, i64, i32, i32, i32]
+        L.lora4_attention_workspace_bytes.restype = sz
+        L.lora4_attention_forward.argtypes = [Ap, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.lora4_attention_forward.restype = ctypes.c_int
+        L.lora4_attention_backward.argtypes = [Ap, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+        L.lora4_attention_backward.restype = ctypes.c_int
         L.lora4_status_string.argtypes = [ctypes.c_int]
         L.lora4_status_string.restype = ctypes.c_char_p
         L.lora4_timing_enable.argtypes = [ctypes.c_int]
@@ -266,6 +281,20 @@ def lora4_backward_epilogue(W, activation, X, dY, P, M, A, B, r, s, group_offset
                             workspace_bytes, stream):
     return lib().lora4_backward_epilogue(ctypes.byref(W), activation, X, dY, P, M, A, B, r, s, group_offsets, Z, dX,
                                          dA, dB, dbias, workspace, workspace_bytes, stream)
+
+
+def lora4_attention_workspace_bytes(which, Tq, Tk, seqs, Hq, Hkv, D):
+    return lib().lora4_attention_workspace_bytes(which, Tq, Tk, seqs, Hq, Hkv, D)
+
+
+def lora4_attention_forward(attn, Q, K, V, O, lse, workspace, workspace_bytes, stream):
+    return lib().lora4_attention_forward(ctypes.byref(attn), Q, K, V, O, lse, workspace, workspace_bytes, stream)
+
+
+def lora4_attention_backward(attn, Q, K, V, O, lse, dO, dQ, dK, dV, lddq, lddk, lddv, workspace, workspace_bytes,
+                             stream):
+    return lib().lora4_attention_backward(ctypes.byref(attn), Q, K, V, O, lse, dO, dQ, dK, dV, lddq, lddk, lddv,
+                                          workspace, workspace_bytes, stream)
 
 
 def timing_enable(on=True):
@@ -1054,3 +1083,131 @@ def backward_epilogue(base, X, dY, A, B, s, P=None, activation="none", Z=None, w
                                      _ptr(workspace), workspace.numel(), stream)
     _check_ws_status(st, "lora4_backward_epilogue")
     return {"dX": dX, "dA": dA, "dB": dB, "dbias": dbias}
+
+
+# ---------------------------------------------------------------------------
+# Attention
+# ---------------------------------------------------------------------------
+
+def _heads(t, name, dev=None, shape=None):
+    """Checks a bf16 tensor [T, H, D] whose tokens hold their heads contiguously
+    (columns of one projection's output among them); returns its token stride."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D tensor [tokens, heads, D]")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    T, H, D = t.shape
+    if t.numel() == 0:
+        return H * D
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if T <= 1:
+        return H * D
+    if st < H * D or st % 8 != 0:
+        raise ValueError(f"{name}: the token stride must be a multiple of 8 and at least {H * D}, got {st}")
+    return st
+
+
+def _attention_args(Q, K, V, scale, q_offsets, k_offsets, k_lengths):
+    """The ABI description of an attention problem, its tensors checked."""
+    import torch
+    ldq = _heads(Q, "Q")
+    dev = Q.device
+    ldk = _heads(K, "K", dev)
+    ldv = _heads(V, "V", dev, K.shape)
+    Tq, Hq, D = Q.shape
+    Tk, Hkv, Dk = K.shape
+    if Dk != D:
+        raise ValueError(f"Q has heads of {D} elements, K and V of {Dk}")
+    if Hkv < 1 or Hq < 1 or Hq % Hkv != 0:
+        raise ValueError(f"{Hq} query heads do not share {Hkv} key heads evenly")
+    seqs = 1
+    if q_offsets is not None:
+        seqs = q_offsets.numel() - 1
+        _need(q_offsets, "q_offsets", (max(seqs, 1) + 1,), torch.int64, dev)
+        if k_offsets is not None:
+            _need(k_offsets, "k_offsets", (seqs + 1,), torch.int64, dev)
+        elif Tq != Tk:
+            raise ValueError("without k_offsets the keys are the queries' tokens: K must have as many as Q")
+    elif k_offsets is not None:
+        raise ValueError("k_offsets are only taken with q_offsets")
+    if k_lengths is not None:
+        _need(k_lengths, "k_lengths", (seqs,), torch.int64, dev)
+    return lora4_attn(Tq, Tk, seqs, Hq, Hkv, D, float(scale), ldq, ldk, ldv, _ptr(q_offsets), _ptr(k_offsets),
+                      _ptr(k_lengths))
+
+
+def attention_workspace(which, Tq, Tk, seqs, Hq, Hkv, D, device):
+    """Workspace of attention (which = 0) or attention_backward (1)."""
+    return _workspace(lora4_attention_workspace_bytes(which, Tq, Tk, seqs, Hq, Hkv, D),
+                      "lora4_attention_workspace_bytes", device)
+
+
+def attention(Q, K, V, scale, q_offsets=None, k_offsets=None, k_lengths=None, want_lse=True, workspace=None, out=None):
+    """Causal attention of bf16 Q [Tq, Hq, D] over K, V [Tk, Hkv, D]: {"O"
+    [Tq, Hq, D], "lse" fp32 [Tq, Hq]} (lse, which the backward takes, is None
+    without want_lse). Tokens may be strided (columns of one projection's
+    output). Packed sequences: q_offsets, k_offsets int64 [S + 1] on the device
+    (k_offsets None: the same tokens), and k_lengths int64 [S], the filled rows of
+    each sequence's cache. A sequence's last query sees its last key. Rows of no
+    sequence are left as they are (a new O is not initialised there)."""
+    import torch
+    out = out or {}
+    a = _attention_args(Q, K, V, scale, q_offsets, k_offsets, k_lengths)
+    dev = Q.device
+    O, lse = out.get("O"), out.get("lse")
+    if O is not None:
+        _need(O, "O", Q.shape, torch.bfloat16, dev)
+    else:
+        O = torch.empty(Q.shape, dtype=torch.bfloat16, device=dev)
+    if lse is not None:
+        _need(lse, "lse", Q.shape[:2], torch.float32, dev)
+    elif want_lse:
+        lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=dev)
+    stream, guard = _on_device(dev)
+    with guard:
+        if workspace is None:
+            workspace = attention_workspace(0, a.Tq, a.Tk, a.seqs, a.Hq, a.Hkv, a.D, dev)
+        else:
+            _given(workspace, dev)
+        st = lora4_attention_forward(a, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), _ptr(workspace),
+                                     workspace.numel(), stream)
+    _check_ws_status(st, "lora4_attention_forward")
+    return {"O": O, "lse": lse}
+
+
+def attention_backward(Q, K, V, O, lse, dO, scale, q_offsets=None, k_offsets=None, k_lengths=None, workspace=None,
+                       out=None):
+    """{"dQ", "dK", "dV"} of attention for dO [Tq, Hq, D] and the forward's O and
+    lse. `out` may hold them, strided as Q, K and V may be (columns of one
+    projection's gradient); rows of no sequence are left as they are."""
+    import torch
+    out = out or {}
+    a = _attention_args(Q, K, V, scale, q_offsets, k_offsets, k_lengths)
+    dev = Q.device
+    _need(O, "O", Q.shape, torch.bfloat16, dev)
+    _need(dO, "dO", Q.shape, torch.bfloat16, dev)
+    _need(lse, "lse", Q.shape[:2], torch.float32, dev)
+    grads, lds = [], []
+    for name, ref in (("dQ", Q), ("dK", K), ("dV", V)):
+        t = out.get(name)
+        if t is None:
+            t = torch.empty(ref.shape, dtype=torch.bfloat16, device=dev)
+        lds.append(_heads(t, name, dev, ref.shape))
+        grads.append(t)
+    stream, guard = _on_device(dev)
+    with guard:
+        if workspace is None:
+            workspace = attention_workspace(1, a.Tq, a.Tk, a.seqs, a.Hq, a.Hkv, a.D, dev)
+        else:
+            _given(workspace, dev)
+        st = lora4_attention_backward(a, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), _ptr(dO), *map(_ptr, grads),
+                                      *lds, _ptr(workspace), workspace.numel(), stream)
+    _check_ws_status(st, "lora4_attention_backward")
+    return dict(zip(("dQ", "dK", "dV"), grads))

@@ -14,9 +14,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "liblora4.so")
 SOURCES = [os.path.join(HERE, "csrc", "lora4.hip")]   # includes every csrc/*.hpp
-# the feed-forward operators' kernels, compiled beside it (lora4.hip includes
-# them itself where it is compiled alone)
-FFN_SOURCES = [os.path.join(HERE, "csrc", "ffn.hip")]
+# the kernels of the feed-forward operators and of attention, compiled beside
+# it (lora4.hip includes them itself where it is compiled alone)
+FFN_SOURCES = [os.path.join(HERE, "csrc", "ffn.hip"), os.path.join(HERE, "csrc", "attn.hip")]
 # measured roofline denominators (MFMA rate, HBM read bandwidth), beside the library
 PROBE_LIB = os.path.join(HERE, "libpeakprobe.so")
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "peak_probe.hip")]
@@ -69,7 +69,7 @@ def build(verbose=False):
     """Compile the library and the peak probe; returns the library's path.
     Always recompiles."""
     _compile(PROBE_SOURCES, PROBE_LIB, verbose)
-    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(2) as pool:
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(4) as pool:
         objs = list(pool.map(lambda s: _object(s, os.path.join(tmp, os.path.basename(s) + ".o"), verbose),
                              SOURCES + FFN_SOURCES))
         _compile(objs, LIB, verbose)

@@ -1,0 +1,720 @@
+// Causal attention over packed sequences with grouped heads: forward (whole
+// prompts, chunks and single tokens over a cache) and backward.
+//
+// Per sequence with Lq queries and Lk keys, query i sees the keys
+// j <= i + Lk - Lq:
+//
+//   S = scale Q K^T,  P = softmax of a row's visible S,  O = P V,
+//   lse = log(sum exp S)
+//   backward: delta = sum_d dO O,  P = exp(S - lse),  dP = dO V^T,
+//   dS = P (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
+//
+// Packed rows: the G = Hq / Hkv query heads of a key head are rows of one
+// matrix, row i G + g for query i and head g of the group. A tile of rows
+// reads its keys and values once for all heads of the group, single tokens
+// over a cache fill their tiles G times better, and dK, dV are sums over rows
+// that need no second pass over the heads.
+//
+// Products run on v_mfma_f32_32x32x16_bf16 in the transposed form: a wave
+// computes S^T = K Q^T, so that a lane's 16 results of a 32 x 32 block belong
+// to one row (its column lane % 32), and the softmax is lane-local but for one
+// exchange between the two lane halves. Result register r of half h holds
+// key 8 (r / 4) + 4 h + r % 4. As second operand of the next product
+// (O^T = V^T P^T) a lane half supplies 8 keys per 16-deep step; the reduction's
+// order is free, so the 16 keys of a step are taken in the order in which the
+// registers hold them, and V is fetched to match: two transposing reads of
+// rows 16 b + 4 h .. +3 and 16 b + 8 + 4 h .. +3. P never passes through LDS.
+//
+// LDS tiles of [rows][D] bf16 (rows of 128 or 256 bytes) are filled by direct
+// loads, 16 bytes a lane; a row's 16-byte chunks are stored at
+// chunk ^ row_swz(row), which keeps both kinds of read off each other's banks.
+// Rows past a sequence's end and columns past D are out of the descriptor's
+// range and read as zeros, so that nothing of another sequence (or of a cache's
+// unfilled part) enters a product, NaN included.
+#pragma once
+
+#include "common.hpp"
+#include "gemm_big.hpp"
+
+namespace lora4 {
+namespace attn {
+
+using big::rsrc_t;
+
+constexpr int THREADS = 256;
+constexpr int ROWS = 128;     // packed query rows of a forward or dQ tile (32 a wave)
+constexpr int KEYS = 64;      // keys of a step of these
+constexpr int BKEYS = 128;    // keys of a dK, dV tile (32 a wave)
+constexpr int BROWS = 64;     // packed query rows of a step of it
+constexpr uint32_t OOB = big::OOB;
+constexpr float LOG2E = 1.44269504088896340736f;
+
+struct Params {
+  const uint16_t *Q, *K, *V;
+  int64_t ldq, ldk, ldv;      // elements between tokens
+  int64_t Tq, Tk;
+  int seqs;
+  int Hq, Hkv, G, D;
+  uint32_t gmagic;            // ceil(2^32 / G), 0 for G == 1
+  float scale;
+  const int64_t *qo, *ko, *kl;
+  int slots;                  // row tiles (forward, dQ) or key tiles (dK, dV) of the grid
+  int splits;                 // key ranges (forward) or row ranges (dK, dV) per tile
+  uint16_t *O;                // [Tq][Hq][D]
+  float *lse;                 // [Tq][Hq] or null
+  float *part;                // splits > 1: fp32 partials
+  float *part_ml;             // forward: [splits][Tq Hq][2] running maximum and sum
+  // backward
+  const uint16_t *dO;
+  const float *delta;         // [Tq][Hq]
+  uint16_t *dQ, *dK, *dV;
+  int64_t lddq, lddk, lddv;
+};
+
+// Query of packed row r, exact for r < 2^32 / G (which the host checks).
+__device__ __forceinline__ uint32_t row_query(const Params &p, uint32_t r) {
+  return p.gmagic ? __umulhi(r, p.gmagic) : r;
+}
+
+// One tile of the grid.
+struct Tile {
+  int64_t q0, k0;   // the sequence's first query and key
+  int Lq, Lk;
+  int tile;         // tile of the sequence, -1: none
+};
+
+__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+// Sequence s, its ranges held inside the tensors whatever the offsets say.
+__device__ __forceinline__ void seq_range(const Params &p, int s, int64_t &q0, int64_t &Lq, int64_t &k0, int64_t &Lk) {
+  if (p.qo) {
+    q0 = clamp64(p.qo[s], 0, p.Tq);
+    Lq = clamp64(p.qo[s + 1], q0, p.Tq) - q0;
+  } else {
+    q0 = 0;
+    Lq = p.Tq;
+  }
+  if (p.ko) {
+    k0 = clamp64(p.ko[s], 0, p.Tk);
+    Lk = clamp64(p.ko[s + 1], k0, p.Tk) - k0;
+  } else {
+    k0 = 0;
+    Lk = p.Tk;
+  }
+  if (p.kl) Lk = clamp64(p.kl[s], 0, Lk);
+}
+
+// The slot-th tile of the batch: sequences in order, each cut into tiles of
+// `per` packed rows (BY_KEYS: keys). The lanes of a wave look through 64
+// sequences at a time.
+template <bool BY_KEYS>
+__device__ __forceinline__ Tile map_tile(const Params &p, int slot, int per) {
+  Tile t{0, 0, 0, 0, -1};
+  const int lane = threadIdx.x & 63;
+  int64_t base = 0;
+  for (int s0 = 0; s0 < p.seqs; s0 += 64) {
+    int64_t q0 = 0, Lq = 0, k0 = 0, Lk = 0;
+    if (s0 + lane < p.seqs) seq_range(p, s0 + lane, q0, Lq, k0, Lk);
+    const int nt = (int)(((BY_KEYS ? Lk : Lq * p.G) + per - 1) / per);
+    int incl = nt;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int64_t first = base + incl - nt;
+    const unsigned long long hit = __ballot(slot >= first && slot < first + nt);
+    if (hit) {
+      const int src = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
+      t.tile = __builtin_amdgcn_readfirstlane(__shfl((int)(slot - first), src));
+      t.q0 = uniform64(__shfl((long long)q0, src));
+      t.k0 = uniform64(__shfl((long long)k0, src));
+      t.Lq = __builtin_amdgcn_readfirstlane(__shfl((int)Lq, src));
+      t.Lk = __builtin_amdgcn_readfirstlane(__shfl((int)Lk, src));
+      return t;
+    }
+    base += __shfl(incl, 63);
+  }
+  return t;
+}
+
+// Block -> (slot, key head, split). Consecutive blocks go to consecutive XCDs:
+// with eight key heads (or a group of eight of more) a head's blocks share one
+// XCD's L2, whatever their slots.
+struct Job {
+  int slot, head, split;
+};
+__device__ __forceinline__ Job map_job(const Params &p) {
+  int id = blockIdx.x;
+  const int hw = p.Hkv % 8 == 0 ? 8 : p.Hkv;   // heads side by side
+  const int per = p.slots * p.splits * hw;
+  const int g = id / per;
+  id -= g * per;
+  Job j;
+  j.head = g * hw + id % hw;
+  id /= hw;
+  j.split = id % p.splits;
+  j.slot = id / p.splits;
+  return j;
+}
+
+// ---------------------------------------------------------------------------
+// LDS tiles
+// ---------------------------------------------------------------------------
+
+// Bytes of a tile row for DC 32-element column blocks, and the swizzle. A
+// 16-byte-per-lane read takes 16 lanes at a time (256 bytes, 64 banks): 16
+// consecutive rows at one chunk, which land in 16 different places. A
+// transposing read takes 32 lanes at a time: four consecutive rows (from a
+// multiple of four) of 64 bytes, which land in the four quarters.
+template <int DC>
+struct Lds {
+  static constexpr int CH = DC <= 2 ? 8 : 16;     // 16-byte chunks of a row
+  static constexpr int RW = CH * 8;               // elements of a row
+  static __device__ __forceinline__ int swz(int row) {
+    return CH == 16 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  }
+  static __device__ __forceinline__ int at(int row, int chunk) { return row * RW + ((chunk ^ swz(row)) << 3); }
+};
+
+__device__ __forceinline__ void load_lds16(const rsrc_t &r, uint16_t *dst, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, voff, 0, 0, 0);
+}
+
+// Key or value tile: NR rows from key k of the descriptor (whose range ends with
+// the sequence) into LDS. Lane l of a wave writes the l-th 16 bytes of 1 KB.
+template <int DC, int NR>
+__device__ __forceinline__ void load_kv(const rsrc_t &r, uint16_t *lds, int64_t ld, int D, int wave, int lane) {
+  using T = Lds<DC>;
+  constexpr int RPI = 64 / T::CH;          // rows of one load instruction
+  constexpr int NI = NR / RPI / 4;         // instructions per wave
+  const int rl = lane / T::CH, cp = lane % T::CH;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int row = (i * 4 + wave) * RPI + rl;
+    const int c = cp ^ T::swz(row);
+    load_lds16(r, lds + (i * 4 + wave) * 512, c * 8 < D ? (uint32_t)(row * (int)ld * 2 + c * 16) : OOB);
+  }
+}
+
+// A operand of 16 reduction columns from kk * 16 of the 32 rows from row0 (the rows
+// are the product's rows).
+template <int DC>
+__device__ __forceinline__ u32x4_t frag_rows(const uint16_t *lds, int row0, int kk, int lane) {
+  return lds_read_b128(lds + Lds<DC>::at(row0 + (lane & 31), 2 * kk + (lane >> 5)));
+}
+
+// A operand of a product that reduces over the tile's rows: columns 32 db ..
+// +31 as its rows, the 16 rows from row0 in the order of the result registers.
+template <int DC>
+__device__ __forceinline__ u32x4_t frag_cols(const uint16_t *lds, int row0, int db, int lane) {
+  const int h = lane >> 5, i = lane & 15;
+  const int col = db * 32 + ((lane >> 4) & 1) * 16 + (i & 3) * 4;
+  const int r = row0 + 4 * h + (i >> 2);
+  const u32x2_t lo = lds_read_tr16(lds + Lds<DC>::at(r, col >> 3) + (col & 7));
+  const u32x2_t hi = lds_read_tr16(lds + Lds<DC>::at(r + 8, col >> 3) + (col & 7));
+  return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+}
+
+// 8 result registers (one 16-row step) as bf16 operand.
+__device__ __forceinline__ u32x4_t pack8(const f32x16_t &v, int r0) {
+  return u32x4_t{pack_bf16x2(v[r0], v[r0 + 1]), pack_bf16x2(v[r0 + 2], v[r0 + 3]), pack_bf16x2(v[r0 + 4], v[r0 + 5]),
+                 pack_bf16x2(v[r0 + 6], v[r0 + 7])};
+}
+
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// B operand straight from memory: this lane's row, 8 columns from 16 kk + 8 h.
+template <int DC>
+__device__ __forceinline__ void load_row_frags(u32x4_t (&f)[2 * DC], const uint16_t *row, bool ok, int D, int h) {
+#pragma unroll
+  for (int kk = 0; kk < 2 * DC; ++kk) {
+    const int c = 16 * kk + 8 * h;
+    f[kk] = ok && c < D ? ldg_b128_cached(row + c) : u32x4_t{0u, 0u, 0u, 0u};
+  }
+}
+
+// This lane's row of a transposed result [32 DC columns][rows] times a, as bf16.
+template <int DC>
+__device__ __forceinline__ void store_row(uint16_t *dst, const f32x16_t (&acc)[DC], float a, int D, int h) {
+#pragma unroll
+  for (int db = 0; db < DC; ++db)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = db * 32 + 8 * i + 4 * h;
+      if (c < D)
+        *reinterpret_cast<u32x2_t *>(dst + c) =
+            u32x2_t{pack_bf16x2(acc[db][4 * i] * a, acc[db][4 * i + 1] * a),
+                    pack_bf16x2(acc[db][4 * i + 2] * a, acc[db][4 * i + 3] * a)};
+    }
+}
+
+template <int DC>
+__device__ __forceinline__ void store_row_f32(float *dst, const f32x16_t (&acc)[DC], int D, int h) {
+#pragma unroll
+  for (int db = 0; db < DC; ++db)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = db * 32 + 8 * i + 4 * h;
+      if (c < D)
+        *reinterpret_cast<f32x4_t *>(dst + c) =
+            f32x4_t{acc[db][4 * i], acc[db][4 * i + 1], acc[db][4 * i + 2], acc[db][4 * i + 3]};
+    }
+}
+
+// Descriptor of head `head` of the keys (or values) from key k of the sequence to
+// its end.
+__device__ __forceinline__ rsrc_t kv_rsrc(const uint16_t *X, int64_t ld, const Params &p, const Tile &t, int head,
+                                          int k) {
+  const int64_t left = (int64_t)t.Lk - k;
+  return big::make_rsrc(X + (t.k0 + (left > 0 ? k : 0)) * ld + head * p.D,
+                        left > 0 ? big::clamp_bytes(((left - 1) * ld + p.D) * 2) : 0u);
+}
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+
+template <int DC>
+__global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
+  using T = Lds<DC>;
+  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  constexpr int TE = KEYS * T::RW;   // elements of one tile
+  // K and V of two steps: K0 V0 K1 V1
+
+  Job j = map_job(p);
+  const Tile t = map_tile<false>(p, p.slots - 1 - j.slot, ROWS);   // long rows of keys first
+  if (t.tile < 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int h = lane >> 5;
+  const int R = t.Lq * p.G;
+  const int off = t.Lk - t.Lq;
+
+  // this lane's row
+  const int r = t.tile * ROWS + wave * 32 + (lane & 31);
+  const bool row_ok = r < R;
+  const int qi = (int)row_query(p, (uint32_t)(row_ok ? r : R - 1));
+  const int64_t oi = (t.q0 + qi) * p.Hq + j.head * p.G + ((row_ok ? r : R - 1) - qi * p.G);   // (token, head)
+  u32x4_t qf[2 * DC];
+  load_row_frags<DC>(qf, p.Q + (t.q0 + qi) * p.ldq + (oi - (t.q0 + qi) * p.Hq) * p.D, row_ok, p.D, h);
+
+  // keys that the block's last row sees, and that all of the wave's rows see
+  const int q_hi = (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + ROWS - 1));
+  const int q_lo = (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + wave * 32));
+  const int kend = min(t.Lk, q_hi + off + 1);
+  int nt = kend > 0 ? (kend + KEYS - 1) / KEYS : 0;
+  int t0 = 0;
+  if (p.splits > 1) {
+    const int per = (nt + p.splits - 1) / p.splits;
+    t0 = min(nt, j.split * per);
+    nt = min(nt, t0 + per);
+  }
+  const int full = min(t.Lk, q_lo + off + 1);   // keys seen by every row of the wave
+
+  f32x16_t acc[DC];
+#pragma unroll
+  for (int i = 0; i < DC; ++i) acc[i] = f32x16_t{};
+  float m = -INFINITY, l = 0.0f;
+  const float c = p.scale * LOG2E;
+  const int lim = qi + off;   // last key this lane's row sees
+
+  auto issue = [&](int s) {
+    const int k = s * KEYS;
+    uint16_t *dst = smem + (s & 1) * 2 * TE;
+    load_kv<DC, KEYS>(kv_rsrc(p.K, p.ldk, p, t, j.head, k), dst, p.ldk, p.D, wave, lane);
+    load_kv<DC, KEYS>(kv_rsrc(p.V, p.ldv, p, t, j.head, k), dst + TE, p.ldv, p.D, wave, lane);
+  };
+
+  if (t0 < nt) issue(t0);
+  for (int s = t0; s < nt; ++s) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // this wave's loads of step s have landed
+    __syncthreads();                      // everyone's have, and step s - 1 is done with
+    if (s + 1 < nt) issue(s + 1);
+    const uint16_t *Ks = smem + (s & 1) * 2 * TE, *Vs = Ks + TE;
+    const int k0 = s * KEYS;
+
+    f32x16_t sc[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      sc[kb] = f32x16_t{};
+#pragma unroll
+      for (int kk = 0; kk < 2 * DC; ++kk)
+        sc[kb] = mfma_32x32x16(frag_rows<DC>(Ks, kb * 32, kk, lane), qf[kk], sc[kb]);
+    }
+    if (k0 + KEYS > full) {
+      const int lk = lim - k0 - 4 * h;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (kb * 32 + 8 * (i >> 2) + (i & 3) > lk) sc[kb][i] = -INFINITY;
+    }
+    float mt = sc[0][0];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[kb][i]);
+    mt = fmaxf(mt, other_half(mt));
+    if (__ballot(mt > m)) {
+      const float mn = fmaxf(m, mt);
+      const float a = mn == m ? 1.0f : exp2_hw((m - mn) * c);
+#pragma unroll
+      for (int i = 0; i < DC; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] *= a;
+      l *= a;
+      m = mn;
+    }
+    const float mc = m == -INFINITY ? 0.0f : m * c;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float e = exp2_hw(__builtin_fmaf(sc[kb][i], c, -mc));
+        sc[kb][i] = e;
+        l += e;
+      }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const u32x4_t pf = pack8(sc[b >> 1], (b & 1) * 8);
+#pragma unroll
+      for (int db = 0; db < DC; ++db) acc[db] = mfma_32x32x16(frag_cols<DC>(Vs, b * 16, db, lane), pf, acc[db]);
+    }
+  }
+
+  l += other_half(l);
+  if (!row_ok) return;
+  if (p.splits > 1) {
+    const int64_t pi = (int64_t)j.split * p.Tq * p.Hq + oi;
+    store_row_f32<DC>(p.part + pi * p.D, acc, p.D, h);
+    if (h == 0) {
+      p.part_ml[2 * pi] = m * c;
+      p.part_ml[2 * pi + 1] = l;
+    }
+    return;
+  }
+  store_row<DC>(p.O + oi * p.D, acc, l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l), p.D, h);
+  if (p.lse && h == 0) p.lse[oi] = l == 0.0f ? -INFINITY : m * p.scale + __logf(l);
+}
+
+// Joins the key ranges of a row: a wave to a row, two columns a lane.
+static __global__ __launch_bounds__(THREADS) void k_attn_join(Params p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t rows = p.Tq * p.Hq;
+  if (row >= rows) return;
+  const int64_t q = row / p.Hq;
+  if (p.qo && (q < p.qo[0] || q >= p.qo[p.seqs])) return;   // rows of no sequence
+  float mx = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) mx = fmaxf(mx, p.part_ml[2 * (s * rows + row)]);
+  float l = 0.0f;
+  float o[2] = {0.0f, 0.0f};
+  for (int s = 0; s < p.splits; ++s) {
+    const int64_t pi = s * rows + row;
+    const float ls = p.part_ml[2 * pi + 1];
+    if (ls == 0.0f) continue;   // (a NaN is not 0)
+    const float a = exp2_hw(p.part_ml[2 * pi] - mx);
+    l += a * ls;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int d = lane * 2 + e;
+      if (d < p.D) o[e] += a * p.part[pi * p.D + d];
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (lane * 2 < p.D) *reinterpret_cast<uint32_t *>(p.O + row * p.D + lane * 2) = pack_bf16x2(o[0] * inv, o[1] * inv);
+  if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : mx * (1.0f / LOG2E) + __logf(l);
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+
+// delta = sum over the columns of dO O: 16 lanes to a (token, head).
+static __global__ __launch_bounds__(THREADS) void k_attn_delta(const uint16_t *O, const uint16_t *dO, int64_t rows, int D,
+                                                         float *delta) {
+  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int c = (threadIdx.x & 15) * 8;
+  float s = 0.0f;
+  if (row < rows && c < D) {
+    const u32x4_t a = ldg_b128_cached(O + row * D + c), b = ldg_b128_cached(dO + row * D + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s = __builtin_fmaf(bf16_bits_to_f32(a[i] & 0xFFFFu), bf16_bits_to_f32(b[i] & 0xFFFFu), s);
+      s = __builtin_fmaf(bf16_bits_to_f32(a[i] >> 16), bf16_bits_to_f32(b[i] >> 16), s);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if (row < rows && (threadIdx.x & 15) == 0) delta[row] = s;
+}
+
+// dQ: a tile of rows over its keys, as the forward.
+template <int DC>
+__global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
+  using T = Lds<DC>;
+  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  constexpr int TE = KEYS * T::RW;
+
+  Job j = map_job(p);
+  const Tile t = map_tile<false>(p, p.slots - 1 - j.slot, ROWS);
+  if (t.tile < 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int h = lane >> 5;
+  const int R = t.Lq * p.G;
+  const int off = t.Lk - t.Lq;
+
+  const int r = t.tile * ROWS + wave * 32 + (lane & 31);
+  const bool row_ok = r < R;
+  const int qi = (int)row_query(p, (uint32_t)(row_ok ? r : R - 1));
+  const int64_t oi = (t.q0 + qi) * p.Hq + j.head * p.G + ((row_ok ? r : R - 1) - qi * p.G);
+  const int64_t hd = (oi - (t.q0 + qi) * p.Hq) * p.D;   // the head's first column
+  u32x4_t qf[2 * DC], of[2 * DC];
+  load_row_frags<DC>(qf, p.Q + (t.q0 + qi) * p.ldq + hd, row_ok, p.D, h);
+  load_row_frags<DC>(of, p.dO + oi * p.D, row_ok, p.D, h);
+  const float ls = p.lse[oi];
+  // a row that saw no key has no gradient: P = exp2(-inf) = 0
+  const float lse2 = ls == -INFINITY ? INFINITY : ls * LOG2E;
+  const float dl = p.delta[oi];
+
+  const int q_hi = (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + ROWS - 1));
+  const int q_lo = (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + wave * 32));
+  const int kend = min(t.Lk, q_hi + off + 1);
+  const int nt = kend > 0 ? (kend + KEYS - 1) / KEYS : 0;
+  const int full = min(t.Lk, q_lo + off + 1);
+
+  f32x16_t acc[DC];
+#pragma unroll
+  for (int i = 0; i < DC; ++i) acc[i] = f32x16_t{};
+  const float c = p.scale * LOG2E;
+  const int lim = qi + off;
+
+  auto issue = [&](int s) {
+    const int k = s * KEYS;
+    uint16_t *dst = smem + (s & 1) * 2 * TE;
+    load_kv<DC, KEYS>(kv_rsrc(p.K, p.ldk, p, t, j.head, k), dst, p.ldk, p.D, wave, lane);
+    load_kv<DC, KEYS>(kv_rsrc(p.V, p.ldv, p, t, j.head, k), dst + TE, p.ldv, p.D, wave, lane);
+  };
+
+  if (nt > 0) issue(0);
+  for (int s = 0; s < nt; ++s) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    if (s + 1 < nt) issue(s + 1);
+    const uint16_t *Ks = smem + (s & 1) * 2 * TE, *Vs = Ks + TE;
+    const int k0 = s * KEYS;
+    const bool edge = k0 + KEYS > full;
+    const int lk = lim - k0 - 4 * h;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      f32x16_t sc = f32x16_t{}, dp = f32x16_t{};
+#pragma unroll
+      for (int kk = 0; kk < 2 * DC; ++kk) {
+        sc = mfma_32x32x16(frag_rows<DC>(Ks, kb * 32, kk, lane), qf[kk], sc);
+        dp = mfma_32x32x16(frag_rows<DC>(Vs, kb * 32, kk, lane), of[kk], dp);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float ds = exp2_hw(__builtin_fmaf(sc[i], c, -lse2)) * (dp[i] - dl);
+        if (edge && kb * 32 + 8 * (i >> 2) + (i & 3) > lk) ds = 0.0f;
+        sc[i] = ds;
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const u32x4_t df = pack8(sc, b * 8);
+#pragma unroll
+        for (int db = 0; db < DC; ++db)
+          acc[db] = mfma_32x32x16(frag_cols<DC>(Ks, kb * 32 + b * 16, db, lane), df, acc[db]);
+      }
+    }
+  }
+  if (row_ok) store_row<DC>(p.dQ + (t.q0 + qi) * p.lddq + hd, acc, p.scale, p.D, h);
+}
+
+// dK, dV: a tile of keys (32 a wave, K and V in registers) over the packed rows
+// that see them.
+template <int DC>
+__global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
+  using T = Lds<DC>;
+  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  constexpr int TE = BROWS * T::RW;
+  constexpr int RPI = 64 / T::CH, NI = BROWS / RPI / 4;
+  // Q and dO of two steps, then lse (times log2 e), delta and last key of the rows
+  float *stat = reinterpret_cast<float *>(smem + 4 * TE);   // [2][3][BROWS]
+
+  Job j = map_job(p);
+  const Tile t = map_tile<true>(p, j.slot, BKEYS);
+  if (t.tile < 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int h = lane >> 5;
+  const int R = t.Lq * p.G;
+  const int off = t.Lk - t.Lq;
+
+  const int kt = t.tile * BKEYS;                   // the tile's first key
+  const int key = kt + wave * 32 + (lane & 31);    // this lane's
+  const bool key_ok = key < t.Lk;
+  const int64_t kr = t.k0 + (key_ok ? key : t.Lk - 1);
+  u32x4_t kf[2 * DC], vf[2 * DC];
+  load_row_frags<DC>(kf, p.K + kr * p.ldk + j.head * p.D, key_ok, p.D, h);
+  load_row_frags<DC>(vf, p.V + kr * p.ldv + j.head * p.D, key_ok, p.D, h);
+
+  // rows from the first query that sees the tile's first key
+  const int64_t r_lo = (int64_t)max(0, kt - off) * p.G;
+  const int s_lo = (int)(r_lo / BROWS), s_hi = (R + BROWS - 1) / BROWS;
+  int s0 = min(s_lo, s_hi), s1 = s_hi;
+  if (p.splits > 1) {
+    const int per = (s1 - s0 + p.splits - 1) / p.splits;
+    s0 = min(s1, s0 + j.split * per);
+    s1 = min(s1, s0 + per);
+  }
+  // from this row on every row sees every key of the wave
+  const int64_t full = (int64_t)max(0, kt + wave * 32 + 31 - off) * p.G;
+
+  f32x16_t dk[DC], dv[DC];
+#pragma unroll
+  for (int i = 0; i < DC; ++i) dk[i] = dv[i] = f32x16_t{};
+  const float c = p.scale * LOG2E;
+
+  auto issue = [&](int s) {
+    const int r0 = s * BROWS;
+    const int q0 = (int)row_query(p, (uint32_t)r0);
+    uint16_t *dst = smem + (s & 1) * 2 * TE;
+    const int64_t left = (int64_t)t.Lq - q0;
+    const int64_t ldo = (int64_t)p.Hq * p.D;
+    const rsrc_t rq = big::make_rsrc(p.Q + (t.q0 + q0) * p.ldq, big::clamp_bytes(((left - 1) * p.ldq + ldo) * 2));
+    const rsrc_t ro = big::make_rsrc(p.dO + (t.q0 + q0) * ldo, big::clamp_bytes(left * ldo * 2));
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int row = (i * 4 + wave) * RPI + lane / T::CH;
+      const int ch = (lane % T::CH) ^ T::swz(row);
+      const uint32_t q = row_query(p, (uint32_t)(r0 + row));
+      const uint32_t hd = (uint32_t)(j.head * p.G + (r0 + row) - (int)q * p.G) * (uint32_t)p.D + (uint32_t)ch * 8;
+      const bool ok = ch * 8 < p.D && r0 + row < R;
+      load_lds16(rq, dst + (i * 4 + wave) * 512, ok ? ((q - q0) * (uint32_t)p.ldq + hd) * 2 : OOB);
+      load_lds16(ro, dst + TE + (i * 4 + wave) * 512, ok ? ((q - q0) * (uint32_t)ldo + hd) * 2 : OOB);
+    }
+  };
+  // the rows' statistics of step s, a row to a thread
+  float st_l = 0.0f, st_d = 0.0f;
+  int st_k = 0;
+  auto stats = [&](int s) {
+    const int r = s * BROWS + (int)threadIdx.x;
+    st_l = INFINITY;   // P = 0
+    st_d = 0.0f;
+    st_k = -1;
+    if (threadIdx.x < BROWS && r < R) {
+      const int q = (int)row_query(p, (uint32_t)r);
+      const int64_t oi = (t.q0 + q) * p.Hq + j.head * p.G + (r - q * p.G);
+      const float ls = p.lse[oi];
+      if (ls != -INFINITY) st_l = ls * LOG2E;
+      st_d = p.delta[oi];
+      st_k = q + off;
+    }
+  };
+  auto put_stats = [&](int s) {
+    if (threadIdx.x < BROWS) {
+      float *d = stat + (s & 1) * 3 * BROWS + threadIdx.x;
+      d[0] = st_l;
+      d[BROWS] = st_d;
+      reinterpret_cast<int *>(d)[2 * BROWS] = st_k;
+    }
+  };
+
+  if (s0 < s1) {
+    issue(s0);
+    stats(s0);
+    put_stats(s0);
+  }
+  for (int s = s0; s < s1; ++s) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    if (s + 1 < s1) {
+      issue(s + 1);
+      stats(s + 1);
+    }
+    const uint16_t *Qs = smem + (s & 1) * 2 * TE, *Os = Qs + TE;
+    const float *sl = stat + (s & 1) * 3 * BROWS;
+    const bool edge = (int64_t)s * BROWS < full;
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      f32x16_t sc = f32x16_t{}, dp = f32x16_t{};
+#pragma unroll
+      for (int kk = 0; kk < 2 * DC; ++kk) {
+        sc = mfma_32x32x16(frag_rows<DC>(Qs, rb * 32, kk, lane), kf[kk], sc);
+        dp = mfma_32x32x16(frag_rows<DC>(Os, rb * 32, kk, lane), vf[kk], dp);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = rb * 32 + 8 * i + 4 * h;
+        const f32x4_t l4 = *reinterpret_cast<const f32x4_t *>(sl + row);
+        const f32x4_t d4 = *reinterpret_cast<const f32x4_t *>(sl + BROWS + row);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float pe = exp2_hw(__builtin_fmaf(sc[4 * i + e], c, -l4[e]));
+          float ds = pe * (dp[4 * i + e] - d4[e]);
+          if (edge && key > reinterpret_cast<const int *>(sl)[2 * BROWS + row + e]) pe = ds = 0.0f;
+          sc[4 * i + e] = pe;
+          dp[4 * i + e] = ds;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const u32x4_t pf = pack8(sc, b * 8), df = pack8(dp, b * 8);
+#pragma unroll
+        for (int db = 0; db < DC; ++db) {
+          dv[db] = mfma_32x32x16(frag_cols<DC>(Os, rb * 32 + b * 16, db, lane), pf, dv[db]);
+          dk[db] = mfma_32x32x16(frag_cols<DC>(Qs, rb * 32 + b * 16, db, lane), df, dk[db]);
+        }
+      }
+    }
+    if (s + 1 < s1) put_stats(s + 1);
+  }
+  if (!key_ok) return;
+  if (p.splits > 1) {
+    const int64_t n = p.Tk * p.Hkv * p.D;
+    float *dst = p.part + 2 * j.split * n + (kr * p.Hkv + j.head) * p.D;
+    store_row_f32<DC>(dst, dk, p.D, h);
+    store_row_f32<DC>(dst + n, dv, p.D, h);
+    return;
+  }
+  store_row<DC>(p.dK + kr * p.lddk + j.head * p.D, dk, p.scale, p.D, h);
+  store_row<DC>(p.dV + kr * p.lddv + j.head * p.D, dv, 1.0f, p.D, h);
+}
+
+// Sums the row ranges' dK (times scale) and dV in order: 4 columns a thread. The
+// grid runs over the key slots, so that keys of no sequence are left alone.
+static __global__ __launch_bounds__(THREADS) void k_attn_dkv_sum(Params p) {
+  const Tile t = map_tile<true>(p, blockIdx.x, 16);
+  if (t.tile < 0) return;
+  const int64_t n = p.Tk * p.Hkv * p.D;
+  const int w = p.Hkv * p.D;
+  const int keys = min(16, t.Lk - t.tile * 16);
+  for (int i = threadIdx.x * 4; i < keys * w; i += THREADS * 4) {
+    const int64_t kr = t.k0 + t.tile * 16 + i / w;
+    const int col = i % w;
+    const float *src = p.part + kr * w + col;
+    f32x4_t a = {0.f, 0.f, 0.f, 0.f}, b = a;
+    for (int s = 0; s < p.splits; ++s) {
+      a += *reinterpret_cast<const f32x4_t *>(src + 2 * s * n);
+      b += *reinterpret_cast<const f32x4_t *>(src + (2 * s + 1) * n);
+    }
+    *reinterpret_cast<u32x2_t *>(p.dK + kr * p.lddk + col) =
+        u32x2_t{pack_bf16x2(a[0] * p.scale, a[1] * p.scale), pack_bf16x2(a[2] * p.scale, a[3] * p.scale)};
+    *reinterpret_cast<u32x2_t *>(p.dV + kr * p.lddv + col) =
+        u32x2_t{pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+  }
+}
+
+// The kernels as the host code launches them: by address, so that they compile
+// as a unit of their own (attn.hip). dc: 32-element column blocks of a head.
+int col_blocks(int D);
+const void *fwd_kernel(int dc);
+const void *join_kernel();
+const void *delta_kernel();
+const void *dq_kernel(int dc);
+const void *dkv_kernel(int dc);
+const void *dkv_sum_kernel();
+
+}  // namespace attn
+}  // namespace lora4

@@ -33,6 +33,7 @@
 #include "gemm_big.hpp"
 #include "gemm_fwd.hpp"
 #include "gemm_dgrad.hpp"
+#include "attn.hpp"
 #include "ffn.hpp"
 #include "mx.hpp"
 #include "loftq.hpp"
@@ -1243,6 +1244,7 @@ dim3 pack_grid(int64_t N, int64_t K) {
 }  // namespace
 
 #include "ffn_host.hpp"
+#include "attn_host.hpp"
 
 // ===========================================================================
 // Exported C ABI
@@ -1900,11 +1902,33 @@ lora4_status lora4_backward_epilogue(const lora4_W *W, int32_t activation, const
                        ws_at<char>(workspace, off), workspace_bytes - off, stream);
 }
 
+// ---- attention (attn_host.hpp) ----------------------------------------------
+
+size_t lora4_attention_workspace_bytes(int which, int64_t Tq, int64_t Tk, int64_t seqs, int32_t Hq, int32_t Hkv,
+                                       int32_t D) {
+  if (which != 0 && which != 1) return 0;
+  return attn_workspace(which, Tq, Tk, seqs, Hq, Hkv, D);
+}
+
+lora4_status lora4_attention_forward(const lora4_attn *attn, const uint16_t *Q, const uint16_t *K, const uint16_t *V,
+                                     uint16_t *O, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+  return attn_forward(attn, Q, K, V, O, lse, workspace, workspace_bytes, reinterpret_cast<hipStream_t>(stream));
+}
+
+lora4_status lora4_attention_backward(const lora4_attn *attn, const uint16_t *Q, const uint16_t *K, const uint16_t *V,
+                                      const uint16_t *O, const float *lse, const uint16_t *dO, uint16_t *dQ,
+                                      uint16_t *dK, uint16_t *dV, int64_t lddq, int64_t lddk, int64_t lddv,
+                                      void *workspace, size_t workspace_bytes, void *stream) {
+  return attn_backward(attn, Q, K, V, O, lse, dO, dQ, dK, dV, lddq, lddk, lddv, workspace, workspace_bytes,
+                       reinterpret_cast<hipStream_t>(stream));
+}
+
 }  // extern "C"
 #pragma GCC visibility pop
 
-// The feed-forward kernels compile as a unit of their own (ffn.hip) where the
-// build asks for it, else here.
+// The feed-forward and the attention kernels compile as units of their own
+// (ffn.hip, attn.hip) where the build asks for it, else here.
 #ifndef LORA4_FFN_SEPARATE
+#include "attn.hip"
 #include "ffn.hip"
 #endif

@@ -1,0 +1,87 @@
+"""Oracle of causal attention over packed sequences with grouped heads, forward
+and backward, in float64 (test infrastructure; no code shared with the HIP path).
+
+Sequence i has queries q_ranges[i] = (first, end) and keys k_ranges[i] likewise;
+its query a sees the keys b <= a + Lk - Lq. A query that sees none has O = 0,
+lse = -inf and no gradient.
+"""
+
+import numpy as np
+
+
+def _weights(q, k, scale):
+    """P [Lq, Lk] and lse [Lq] of one head."""
+    Lq, Lk = q.shape[0], k.shape[0]
+    seen = np.arange(Lk)[None, :] <= np.arange(Lq)[:, None] + (Lk - Lq)
+    s = np.where(seen, scale * (q @ k.T), -np.inf)
+    top = s.max(axis=1, initial=-np.inf, keepdims=True)
+    e = np.where(seen, np.exp(s - np.where(np.isfinite(top), top, 0.0)), 0.0)
+    n = e.sum(axis=1, keepdims=True)
+    with np.errstate(divide="ignore"):
+        lse = (np.where(np.isfinite(top), top, 0.0) + np.log(n))[:, 0]
+    return e / np.where(n > 0, n, 1.0), lse
+
+
+# A value below the smallest normal number of fp32 and bf16 may be flushed to
+# zero: it is off by at most this, absolutely.
+TINY = 2.0 ** -126
+
+
+def weight_error(q, k, lse, scale):
+    """[Lq]: how far a weight P computed in fp32 may be off, relative to itself.
+    A score is D exact products summed in fp32, off by at most D 2^-24 of the sum of
+    their sizes; its multiple of log2 e and lse (which is fp32 itself) by 2^-24 each;
+    exp2 of a number of size x by 2^-24 x and one unit."""
+    if k.shape[0] == 0:
+        return np.zeros(q.shape[0])
+    size = scale * (np.abs(q) @ np.abs(k).T).max(axis=1)
+    return 2.0 ** -24 * ((q.shape[1] + 4) * size + 4 * np.abs(np.where(np.isfinite(lse), lse, 0.0))) + 2.0 ** -20
+
+
+def forward(Q, K, V, scale, q_ranges, k_ranges):
+    """{"O", "lse", "I_O", "E_O"}; I_O = sum over the keys of P |V|, the scale of
+    what rounding P costs; E_O: what fp32 arithmetic may cost. Rows of no sequence
+    are NaN."""
+    Hq, Hkv = Q.shape[1], K.shape[1]
+    O, I, E = (np.full(Q.shape, np.nan) for _ in range(3))
+    lse = np.full(Q.shape[:2], np.nan)
+    for (a, b), (c, d) in zip(q_ranges, k_ranges):
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            P, lse[a:b, h] = _weights(Q[a:b, h], K[c:d, g], scale)
+            O[a:b, h] = P @ V[c:d, g]
+            I[a:b, h] = P @ np.abs(V[c:d, g])
+            # the weights, and their sum that divides
+            E[a:b, h] = 2 * weight_error(Q[a:b, h], K[c:d, g], lse[a:b, h], scale)[:, None] * I[a:b, h]
+            E[a:b, h] += TINY * (1 + np.abs(V[c:d, g]).sum(axis=0))
+    return {"O": O, "lse": lse, "I_O": I, "E_O": E}
+
+
+def backward(Q, K, V, O, dO, scale, q_ranges, k_ranges):
+    """{"dQ", "dK", "dV"}, with delta from the given O, and I_dQ, I_dK, I_dV: the
+    sums of absolute values that the roundings of dS and P enter; E_dQ, E_dK, E_dV:
+    what fp32 arithmetic may cost (the weights' error, and that of dP and delta,
+    sums of D exact products each, whose difference may cancel)."""
+    Hq, Hkv = Q.shape[1], K.shape[1]
+    o = {p + n: np.full(x.shape, np.nan) for n, x in (("dQ", Q), ("dK", K), ("dV", V)) for p in ("", "I_", "E_")}
+    for (a, b), (c, d) in zip(q_ranges, k_ranges):
+        for n in ("dK", "dV", "I_dK", "I_dV", "E_dK", "E_dV"):
+            o[n][c:d] = 0.0
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            q, k, do = Q[a:b, h], K[c:d, g], dO[a:b, h]
+            P, lse = _weights(q, k, scale)
+            dS = P * (do @ V[c:d, g].T - (do * O[a:b, h]).sum(axis=1, keepdims=True)) * scale
+            r = weight_error(q, k, lse, scale)[:, None]
+            terms = np.abs(do) @ np.abs(V[c:d, g]).T + np.abs(do * O[a:b, h]).sum(axis=1, keepdims=True)
+            e = r * np.abs(dS) + P * terms * scale * Q.shape[2] * 2.0 ** -24 + TINY * (1 + scale * (1 + terms))
+            o["E_dQ"][a:b, h] = e @ np.abs(k) + TINY
+            o["E_dK"][c:d, g] += e.T @ np.abs(q) + TINY
+            o["E_dV"][c:d, g] += (r * P + TINY).T @ np.abs(do) + TINY
+            o["dQ"][a:b, h] = dS @ k
+            o["dK"][c:d, g] += dS.T @ q
+            o["dV"][c:d, g] += P.T @ do
+            o["I_dQ"][a:b, h] = np.abs(dS) @ np.abs(k)
+            o["I_dK"][c:d, g] += np.abs(dS).T @ np.abs(q)
+            o["I_dV"][c:d, g] += P.T @ np.abs(do)
+    return o

@@ -92,8 +92,12 @@ void inspect(const std::string &name, void **args) {
   else if (is(name, "k_rmsnorm_fwd")) checked<lora4::norm::FwdParams>(name, args[0]);
   else if (is(name, "k_rmsnorm_bwd")) checked<lora4::norm::BwdParams>(name, args[0]);
   else if (is(name, "k_rows_lds") || is(name, "k_rows_skinny")) checked<lora4::skinny::Params>(name, args[0]);
-  else {   // (scalars only)
-    for (const char *k : {"k_fill_u16", "k_reduce_bf16", "k_col_sum", "k_col_sum_slots", "k_quant_mxfp8"})
+  else if (is(name, "k_attn_fwd") || is(name, "k_attn_join") || is(name, "k_attn_dq") || is(name, "k_attn_dkv") ||
+           is(name, "k_attn_dkv_sum")) {
+    const lora4::attn::Params &p = checked<lora4::attn::Params>(name, args[0]);
+    if (p.G * p.Hkv != p.Hq || p.splits < 1 || (p.splits > 1 && !p.part)) fail(context.c_str(), name.c_str());
+  } else {   // (scalars only)
+    for (const char *k : {"k_attn_delta", "k_fill_u16", "k_reduce_bf16", "k_col_sum", "k_col_sum_slots", "k_quant_mxfp8"})
       if (is(name, k)) return;
     fail("a kernel this driver does not know", name.c_str());
   }
@@ -382,6 +386,80 @@ void refusals() {
   expect((long)lora4_epilogue_workspace_bytes(0, &W, 16, 257), 0);
 }
 
+// Attention over lengths, heads and sequences: every launch, its refusals, and
+// its size queries over the ends of their ranges.
+void attention() {
+  float *F = reinterpret_cast<float *>(D);
+  for (int64_t Tq : {0, 1, 7, 300, 4096, 70000})
+    for (int64_t Tk : {0, 1, 300, 4096, 800000})
+      for (int64_t seqs : {1, 24, 5000})
+        for (int Hq : {1, 12, 64})
+          for (int Hkv : {1, 4})
+            for (int Dh : {8, 72, 128}) {
+              if (Hq % Hkv) continue;
+              const lora4_attn a{Tq, Tk, seqs, Hq, Hkv, Dh, 0.1f, (int64_t)Hq * Dh + 64, (int64_t)Hkv * Dh,
+                                 (int64_t)Hkv * Dh, OFFS, OFFS, Tk % 2 ? OFFS : nullptr};
+              context = "attention Tq " + std::to_string(Tq) + " Tk " + std::to_string(Tk) + " seqs " +
+                        std::to_string(seqs) + " heads " + std::to_string(Hq) + " " + std::to_string(Hkv) + " D " +
+                        std::to_string(Dh);
+              size_t n = lora4_attention_workspace_bytes(0, Tq, Tk, seqs, Hq, Hkv, Dh);
+              expect(lora4_attention_forward(&a, D, D, D, D, F, WS, n, nullptr), LORA4_OK);
+              expect(lora4_attention_forward(&a, D, D, D, D, F, WS, n - 1, nullptr),
+                     Tq ? LORA4_ERR_WORKSPACE : LORA4_OK);
+              n = lora4_attention_workspace_bytes(1, Tq, Tk, seqs, Hq, Hkv, Dh);
+              expect(lora4_attention_backward(&a, D, D, D, D, F, D, D, D, D, a.ldq, a.ldk, a.ldv, WS, n, nullptr),
+                     LORA4_OK);
+              expect(lora4_attention_backward(&a, D, D, D, D, F, D, D, D, D, a.ldq, a.ldk, a.ldv, WS, n - 1, nullptr),
+                     LORA4_ERR_WORKSPACE);
+            }
+  context = "refusals of attention";
+  const lora4_attn good{64, 64, 1, 8, 2, 128, 0.1f, 1024, 256, 256, nullptr, nullptr, nullptr};
+  const size_t n = (size_t)1 << 40;
+  auto both = [&](const lora4_attn *a, long want) {
+    expect(lora4_attention_forward(a, D, D, D, D, F, WS, n, nullptr), want);
+    expect(lora4_attention_backward(a, D, D, D, D, F, D, D, D, D, 1 << 20, 1 << 20, 1 << 20, WS, n, nullptr), want);
+  };
+  both(&good, LORA4_OK);
+  both(nullptr, LORA4_ERR_NULL);
+  lora4_attn a = good;
+  a.Hq = 9;
+  both(&a, LORA4_ERR_SHAPE);
+  a = good;
+  a.D = 136;
+  both(&a, LORA4_ERR_UNIMPLEMENTED);
+  a = good;
+  a.scale = std::numeric_limits<float>::infinity();
+  both(&a, LORA4_ERR_SHAPE);
+  a = good;
+  a.seqs = 2;
+  both(&a, LORA4_ERR_NULL);
+  a = good;
+  a.ldk = 252;
+  both(&a, LORA4_ERR_SHAPE);
+  a = good;
+  a.Tq = std::numeric_limits<int64_t>::max();
+  both(&a, LORA4_ERR_SHAPE);
+  a = good;
+  a.Tk = std::numeric_limits<int64_t>::min();
+  both(&a, LORA4_ERR_SHAPE);
+  expect(lora4_attention_forward(&good, D + 4, D, D, D, F, WS, n, nullptr), LORA4_ERR_ALIGN);
+  expect(lora4_attention_forward(&good, D, nullptr, D, D, F, WS, n, nullptr), LORA4_ERR_NULL);
+  expect(lora4_attention_backward(&good, D, D, D, D, F, D, D, nullptr, D, 1024, 256, 256, WS, n, nullptr),
+         LORA4_ERR_NULL);
+  expect(lora4_attention_backward(&good, D, D, D, D, F, D, D, D, D, 1016, 256, 256, WS, n, nullptr), LORA4_ERR_SHAPE);
+  for (int64_t Tq : {(int64_t)0, (int64_t)1, (int64_t)1 << 20, (int64_t)1 << 30, (int64_t)1 << 62})
+    for (int64_t Tk : {(int64_t)0, (int64_t)1, (int64_t)1 << 30, std::numeric_limits<int64_t>::max()})
+      for (int64_t seqs : {(int64_t)1, (int64_t)1 << 20, std::numeric_limits<int64_t>::max()})
+        for (int Hq : {1, 64, 65535, std::numeric_limits<int>::max()})
+          for (int which = 0; which < 2; ++which) {
+            context = "attention sizes";
+            const bool ok = Tq <= 1 << 30 && Tk <= 1 << 30 && seqs <= 1 << 20 && Hq <= 64 &&
+                            Tq * Hq < (int64_t)1 << 31 && (Tq * Hq + 128) * Hq < (int64_t)1 << 32;
+            if ((lora4_attention_workspace_bytes(which, Tq, Tk, seqs, Hq, 1, 128) != 0) != ok)
+              fail(context.c_str(), (std::to_string(Tq) + " " + std::to_string(Tk) + " " + std::to_string(Hq)).c_str());
+          }
+}
+
 // Size queries over the ends of their ranges (no call: nothing that large
 // exists), where an overflow of the planning's arithmetic would show.
 void sizes() {
@@ -434,6 +512,7 @@ int main() {
     if (f[0]) unsetenv(f[0]);
   }
   norms();
+  attention();
   refusals();
   sizes();
   for (const auto &c : counts) std::printf("%s %d\n", c.first.c_str(), c.second);

@@ -565,6 +565,37 @@ lora4_status lora4_attention_backward(const lora4_attn *attn, const uint16_t *Q,
                                       uint16_t *dK, uint16_t *dV, int64_t lddq, int64_t lddk, int64_t lddv,
                                       void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- The loss over the vocabulary ----------------------------------------------
+ * Softmax cross entropy behind a frozen bf16 head (the output projection over
+ * the vocabulary, which 4-bit fine-tuning leaves in bf16), with the gradient of
+ * its input; the head gets none, as every base here:
+ *   l = X W^T,  loss_i = log(sum over v of exp l_iv) - l_it,
+ *   dX_i = w_i (softmax(l_i) - onehot(t_i)) W,   total = sum of w_i loss_i
+ * over the rows whose target t_i is not ignore_index. The logits are not
+ * kept: the vocabulary is taken in pieces, and a row's gradient is summed up
+ * beside its loss, in one pass.
+ *  X       : bf16 [M, K]; K a multiple of 8. W : bf16 [V, K], any V >= 1.
+ *  targets : DEVICE int64 [M]. A target that is neither a word (0 .. V - 1) nor
+ *            ignore_index makes its row's loss and dX (and total) NaN.
+ *  weights : fp32 [M], w_i (the gradient of whatever is made of the losses), or
+ *            NULL: 1 / the number of rows that are not ignored, the mean.
+ *  loss    : fp32 [M] output, 0 at ignored rows.
+ *  lse     : fp32 [M] output log(sum exp l), 0 at ignored rows; may be NULL.
+ *  total   : fp32 [1] output, 0 if every row is ignored; may be NULL.
+ *  dX      : bf16 [M, K] output, zero at ignored rows; NULL: the loss alone.
+ *  workspace : lora4_head_loss_workspace_bytes(dX != NULL, M, K, V) bytes (0 is
+ *            returned for invalid sizes).
+ * Logits are summed in fp32; the exponentials are rounded to bf16 for their
+ * product with W (the target's own, p_t - 1, is not), which is summed in fp32.
+ * A NaN in a row of X stays in that row; an infinity or NaN in W reaches every
+ * row. The same inputs give the same bits on every call. M may be 0. Errors:
+ * LORA4_ERR_SHAPE, LORA4_ERR_NULL, LORA4_ERR_ALIGN, LORA4_ERR_WORKSPACE,
+ * LORA4_ERR_HIP. */
+size_t lora4_head_loss_workspace_bytes(int grad, int64_t M, int64_t K, int64_t V);
+lora4_status lora4_head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targets, const float *weights,
+                             int64_t M, int64_t K, int64_t V, int64_t ignore_index, float *loss, float *lse,
+                             float *total, uint16_t *dX, void *workspace, size_t workspace_bytes, void *stream);
+
 /* A static, human-readable name for a status code. */
 const char *lora4_status_string(lora4_status status);
 

@@ -39,6 +39,7 @@ EXPORTS = ["lora4_forward", "lora4_forward_noalloc", "lora4_backward", "lora4_wo
            "lora4_gated_workspace_bytes", "lora4_gated_forward", "lora4_gated_backward",
            "lora4_epilogue_workspace_bytes", "lora4_forward_epilogue", "lora4_backward_epilogue",
            "lora4_attention_workspace_bytes", "lora4_attention_forward", "lora4_attention_backward",
+           "lora4_head_loss_workspace_bytes", "lora4_head_loss",
            "lora4_status_string", "lora4_timing_enable", "lora4_timing_collect", "lora4_version"]
 
 
@@ -137,6 +138,10 @@ def lib():
         L.lora4_attention_forward.restype = ctypes.c_int
         L.lora4_attention_backward.argtypes = [Ap, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
         L.lora4_attention_backward.restype = ctypes.c_int
+        L.lora4_head_loss_workspace_bytes.argtypes = [ctypes.c_int, i64, i64, i64]
+        L.lora4_head_loss_workspace_bytes.restype = sz
+        L.lora4_head_loss.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, sz, vp]
+        L.lora4_head_loss.restype = ctypes.c_int
         L.lora4_status_string.argtypes = [ctypes.c_int]
         L.lora4_status_string.restype = ctypes.c_char_p
         L.lora4_timing_enable.argtypes = [ctypes.c_int]
@@ -295,6 +300,16 @@ def lora4_attention_backward(attn, Q, K, V, O, lse, dO, dQ, dK, dV, lddq, lddk, 
                              stream):
     return lib().lora4_attention_backward(ctypes.byref(attn), Q, K, V, O, lse, dO, dQ, dK, dV, lddq, lddk, lddv,
                                           workspace, workspace_bytes, stream)
+
+
+def lora4_head_loss_workspace_bytes(grad, M, K, V):
+    return lib().lora4_head_loss_workspace_bytes(grad, M, K, V)
+
+
+def lora4_head_loss(X, W, targets, weights, M, K, V, ignore_index, loss, lse, total, dX, workspace, workspace_bytes,
+                    stream):
+    return lib().lora4_head_loss(X, W, targets, weights, M, K, V, ignore_index, loss, lse, total, dX, workspace,
+                                 workspace_bytes, stream)
 
 
 def timing_enable(on=True):
@@ -1211,3 +1226,57 @@ def attention_backward(Q, K, V, O, lse, dO, scale, q_offsets=None, k_offsets=Non
                                       *lds, _ptr(workspace), workspace.numel(), stream)
     _check_ws_status(st, "lora4_attention_backward")
     return dict(zip(("dQ", "dK", "dV"), grads))
+
+
+# ---------------------------------------------------------------------------
+# The loss over the vocabulary
+# ---------------------------------------------------------------------------
+
+def head_loss_workspace(grad, M, K, V, device):
+    """Workspace of head_loss for up to M tokens, with (grad) or without dX."""
+    return _workspace(lora4_head_loss_workspace_bytes(1 if grad else 0, M, K, V), "lora4_head_loss_workspace_bytes",
+                      device)
+
+
+def head_loss(X, W, targets, weights=None, ignore_index=-100, want_grad=True, want_lse=False, workspace=None, out=None):
+    """Softmax cross entropy of bf16 X [M, K] behind the frozen head W [V, K] for
+    int64 targets [M]: {"loss" fp32 [M], "total" fp32 [1], "lse" fp32 [M], "dX"
+    bf16 [M, K]} (lse and dX None where not wanted). total is the sum of weights
+    times losses, dX its gradient; weights fp32 [M], or None for the mean over the
+    rows whose target is not ignore_index."""
+    import torch
+    out = out or {}
+    for t, name in ((X, "X"), (W, "W")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{name} must be a 2-D tensor")
+    M, K = X.shape
+    V = W.shape[0]
+    dev = X.device
+    _bf16_on(X, "X", (M, K), dev)
+    _bf16_on(W, "W", (V, K), dev)
+    _need(targets, "targets", (M,), torch.int64, dev)
+    if weights is not None:
+        _need(weights, "weights", (M,), torch.float32, dev)
+    for name, shape, dtype in (("loss", (M,), torch.float32), ("lse", (M,), torch.float32),
+                               ("total", (1,), torch.float32), ("dX", (M, K), torch.bfloat16)):
+        if out.get(name) is not None:
+            _need(out[name], name, shape, dtype, dev)
+    loss, total = out.get("loss"), out.get("total")
+    if loss is None:
+        loss = torch.empty((M,), dtype=torch.float32, device=dev)
+    if total is None:
+        total = torch.empty((1,), dtype=torch.float32, device=dev)
+    lse = out.get("lse")
+    if lse is None and want_lse:
+        lse = torch.empty((M,), dtype=torch.float32, device=dev)
+    dX = _like(out.get("dX"), X) if want_grad or out.get("dX") is not None else None
+    stream, guard = _on_device(dev)
+    with guard:
+        if workspace is None:
+            workspace = head_loss_workspace(dX is not None, M, K, V, dev)
+        else:
+            _given(workspace, dev)
+        st = lora4_head_loss(_ptr(X), _ptr(W), _ptr(targets), _ptr(weights), M, K, V, int(ignore_index), _ptr(loss),
+                             _ptr(lse), _ptr(total), _ptr(dX), _ptr(workspace), workspace.numel(), stream)
+    _check_ws_status(st, "lora4_head_loss")
+    return {"loss": loss, "total": total, "lse": lse, "dX": dX}

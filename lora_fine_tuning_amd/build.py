@@ -14,9 +14,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "liblora4.so")
 SOURCES = [os.path.join(HERE, "csrc", "lora4.hip")]   # includes every csrc/*.hpp
-# the kernels of the feed-forward operators and of attention, compiled beside
-# it (lora4.hip includes them itself where it is compiled alone)
-FFN_SOURCES = [os.path.join(HERE, "csrc", "ffn.hip"), os.path.join(HERE, "csrc", "attn.hip")]
+# the kernels of the feed-forward operators, attention and the loss, compiled
+# beside it (lora4.hip includes them itself where it is compiled alone)
+FFN_SOURCES = [os.path.join(HERE, "csrc", name) for name in ("ffn.hip", "attn.hip", "loss.hip")]
 # measured roofline denominators (MFMA rate, HBM read bandwidth), beside the library
 PROBE_LIB = os.path.join(HERE, "libpeakprobe.so")
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "peak_probe.hip")]

@@ -35,6 +35,7 @@
 #include "gemm_dgrad.hpp"
 #include "attn.hpp"
 #include "ffn.hpp"
+#include "loss.hpp"
 #include "mx.hpp"
 #include "loftq.hpp"
 #include "skinny.hpp"
@@ -1245,6 +1246,7 @@ dim3 pack_grid(int64_t N, int64_t K) {
 
 #include "ffn_host.hpp"
 #include "attn_host.hpp"
+#include "loss_host.hpp"
 
 // ===========================================================================
 // Exported C ABI
@@ -1923,12 +1925,28 @@ lora4_status lora4_attention_backward(const lora4_attn *attn, const uint16_t *Q,
                        reinterpret_cast<hipStream_t>(stream));
 }
 
+// ---- the loss over the vocabulary (loss_host.hpp) ----------------------------
+
+size_t lora4_head_loss_workspace_bytes(int grad, int64_t M, int64_t K, int64_t V) {
+  if ((grad != 0 && grad != 1) || check_loss_sizes(M, K, V) != LORA4_OK) return 0;
+  return loss_plan(grad != 0, M, K, V).bytes;
+}
+
+lora4_status lora4_head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targets, const float *weights,
+                             int64_t M, int64_t K, int64_t V, int64_t ignore_index, float *loss, float *lse,
+                             float *total, uint16_t *dX, void *workspace, size_t workspace_bytes, void *stream) {
+  return head_loss(X, W, targets, weights, M, K, V, ignore_index, loss, lse, total, dX, workspace, workspace_bytes,
+                   reinterpret_cast<hipStream_t>(stream));
+}
+
 }  // extern "C"
 #pragma GCC visibility pop
 
-// The feed-forward and the attention kernels compile as units of their own
-// (ffn.hip, attn.hip) where the build asks for it, else here.
+// The kernels of attention, the feed-forward operators and the loss compile as
+// units of their own (attn.hip, ffn.hip, loss.hip) where the build asks for it,
+// else here.
 #ifndef LORA4_FFN_SEPARATE
 #include "attn.hip"
 #include "ffn.hip"
+#include "loss.hip"
 #endif

@@ -1,0 +1,24 @@
+// Instantiations of the vocabulary loss's kernels (loss.hpp).
+#include "loss.hpp"
+
+namespace lora4 {
+namespace loss {
+
+namespace {
+template <typename K>
+const void *addr(K *k) {
+  return reinterpret_cast<const void *>(k);
+}
+}  // namespace
+
+const void *rows_kernel() { return addr(k_loss_rows); }
+const void *target_kernel() { return addr(k_loss_target); }
+const void *logits_kernel(bool grad) { return grad ? addr(k_loss_logits<true>) : addr(k_loss_logits<false>); }
+const void *join_kernel(bool grad) { return grad ? addr(k_loss_join<true>) : addr(k_loss_join<false>); }
+const void *dx_kernel() { return addr(k_loss_dx); }
+const void *ignored_kernel() { return addr(k_loss_ignored); }
+const void *finish_kernel() { return addr(k_loss_finish); }
+const void *total_kernel() { return addr(k_loss_total); }
+
+}  // namespace loss
+}  // namespace lora4

@@ -1,0 +1,567 @@
+// Softmax cross entropy over a large vocabulary behind a frozen head, with the
+// gradient of its input, in pieces of the vocabulary:
+//
+//   l = X W^T,  loss_i = log(sum_v exp l_iv) - l_it,
+//   dX_i = w_i (softmax(l_i) - onehot(t_i)) W
+//
+// The logits are never kept. With the gradient wanted, one pass makes both:
+// for each piece of the vocabulary
+//
+//   E = exp(l - ref) of the piece's logits, target column left out   (bf16)
+//   S += the row sums of E (unrounded),  acc += E W_piece            (fp32)
+//
+// and at the end dX = w (acc / (S + s_t) - S / (S + s_t) W_t), s_t = exp(l_t -
+// ref): two products of the size of the logits where a second pass for them
+// would take three. The row's reference is the logit of its own target, which
+// is a term of the sum, so that no term that counts can underflow; loss =
+// log1p(S) keeps its digits where the target is nearly certain, and p_t - 1 =
+// -S / (S + s_t) does not cancel. A strip of logits more than REF_SLACK binary
+// orders above the reference is stored against its own maximum instead, and
+// k_loss_join brings the row onto the new reference.
+//
+// Rows without a target (prompts, padding) are left out before the products:
+// the rows that count are copied together once (k_loss_rows).
+//
+// Both products run 256 x 256 tiles of eight waves on v_mfma_f32_32x32x16_bf16,
+// operands by direct loads into two LDS stages of 64-deep slabs. The vocabulary
+// (the hidden columns) is the first operand, so that a lane's results belong to
+// one token: its row's maximum and sum are lane-local but for one exchange, and
+// its stores are contiguous.
+#pragma once
+
+#include "common.hpp"
+#include "gemm_big.hpp"
+
+namespace lora4 {
+namespace loss {
+
+using big::OOB;
+using big::rsrc_t;
+
+constexpr int THREADS = 512;
+constexpr int TILE = 256;            // tokens, and vocabulary or hidden columns, of a tile
+constexpr int BKS = 64;              // reduction step
+constexpr int STRIP = 128;           // vocabulary of a wave: one maximum and sum per row
+constexpr int SLAB = TILE * BKS;     // elements of one operand's stage
+constexpr size_t LDS_BYTES = 4 * SLAB * 2;
+constexpr float LOG2E = 1.44269504088896340736f;
+constexpr float REF_SLACK = 64.0f;   // binary orders a logit may lie above its row's reference
+
+struct Params {
+  const uint16_t *X;        // bf16 [M][K]
+  const uint16_t *W;        // bf16 [V][K]
+  const int64_t *target;    // [M]
+  const float *weight;      // [M] or null: 1 / rows that count
+  int64_t M, K, V;
+  int64_t ignore;
+  // the rows that count, together
+  int *count;               // [0] rows
+  int *row;                 // [M] their rows
+  int *tgt;                 // [M] their targets (-1: out of range)
+  uint16_t *Xc;             // [M][K]
+  float *lt;                // [M] target's logit
+  float *ref;               // [M] reference
+  float *S;                 // [M] sum over the other words
+  // a chunk of them and a piece of the vocabulary
+  int64_t row0;             // first (of the rows that count)
+  int rows;                 // rows of the chunk (a multiple of TILE)
+  int64_t v0;               // first word
+  int64_t cols;             // words (the last piece ends with V)
+  uint16_t *E;              // [rows][lde]
+  int64_t lde;              // a multiple of TILE
+  float *strip_ref, *strip_sum;   // [strips][rows]
+  float *acc;               // [splits][rows][K]
+  int splits, split_steps;
+  int first;                // first piece: acc is written, not added to
+  int tiles_m, tiles_n;
+  // outputs
+  float *loss, *lse, *total;
+  uint16_t *dX;
+};
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ void load_lds16(const rsrc_t &r, uint16_t *dst, uint32_t voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
+}
+
+// Tile t of the grid: consecutive blocks go to consecutive XCDs, each of which
+// takes a contiguous range of the tiles in grouped order (runs of RUN row tiles
+// walked column by column), so that its blocks share both operands in its L2.
+constexpr int RUN = 8;
+__device__ __forceinline__ bool map_tile(int id, int tiles_m, int tiles_n, int &tm, int &tn) {
+  const int n = tiles_m * tiles_n, per = (n + 7) / 8;
+  const int t = (id & 7) * per + (id >> 3);
+  if ((id >> 3) >= per || t >= n) return false;
+  const int g = t / (RUN * tiles_n), r = t - g * RUN * tiles_n;
+  const int rows = min(RUN, tiles_m - g * RUN);
+  tn = r / rows;
+  tm = g * RUN + (r - tn * rows);
+  return true;
+}
+
+// A 256 x 64 slab (rows of ld elements, the reduction contiguous) into the
+// tile64 layout. The 32 1-KB blocks go to the 8 waves in turn.
+struct SlabLoad {
+  uint32_t voff[4];
+  int chunk;        // logical 16-byte chunk this lane fetches (the same in all blocks)
+  __device__ __forceinline__ SlabLoad(int64_t ld, int wave, int lane) {
+    const int rl = lane >> 3;
+    // block b = 8 i + wave: rows 8 b .. 8 b + 7
+    chunk = (lane & 7) ^ ((((wave & 1) << 2) | (rl >> 1)) & 7);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) voff[i] = (uint32_t)((((8 * i + wave) * 8 + rl) * ld + chunk * 8) * 2);
+  }
+  __device__ __forceinline__ void issue(const rsrc_t &r, uint16_t *lds, int k0, int R, int wave) const {
+    const bool edge = k0 + chunk * 8 >= R;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_lds16(r, lds + (8 * i + wave) * 512, edge ? OOB : voff[i], k0 * 2);
+  }
+};
+
+// Operand of 16 reduction columns of the 32 rows from row0.
+__device__ __forceinline__ u32x4_t frag(const uint16_t *lds, int row0, int kk, int lane) {
+  return lds_read_b128(lds + tile64_swz(row0 + (lane & 31), 2 * kk + (lane >> 5)));
+}
+
+// ---------------------------------------------------------------------------
+// The rows that count
+// ---------------------------------------------------------------------------
+
+// One block: the rows whose target is not `ignore`, in order. (Every row is
+// looked at by this block alone; 4096 rows take four rounds.)
+static __global__ __launch_bounds__(1024) void k_loss_rows(Params p) {
+  __shared__ int wsum[16];
+  __shared__ int base;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (threadIdx.x == 0) base = 0;
+  __syncthreads();
+  for (int64_t i0 = 0; i0 < p.M; i0 += 1024) {
+    const int64_t i = i0 + threadIdx.x;
+    const int64_t t = i < p.M ? p.target[i] : p.ignore;
+    const bool in = t != p.ignore;
+    const unsigned long long b = __ballot(in);
+    if (lane == 0) wsum[wave] = __popcll(b);
+    __syncthreads();
+    int before = base;
+    for (int w = 0; w < wave; ++w) before += wsum[w];
+    if (in) {
+      const int at = before + __popcll(b & ((1ull << lane) - 1));
+      p.row[at] = (int)i;
+      p.tgt[at] = t >= 0 && t < p.V ? (int)t : -1;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int w = 0; w < 16; ++w) base += wsum[w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *p.count = base;
+}
+
+// A wave to a row that counts: its X beside the others', and the logit of its
+// target (NaN for a target that is no word: the row's outputs become NaN).
+static __global__ __launch_bounds__(256) void k_loss_target(Params p) {
+  const int lane = threadIdx.x & 63;
+  const int at = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (at >= *p.count) return;
+  const int t = p.tgt[at];
+  const uint16_t *x = p.X + (int64_t)p.row[at] * p.K;
+  const uint16_t *w = p.W + (int64_t)max(t, 0) * p.K;
+  uint16_t *xc = p.Xc + (int64_t)at * p.K;
+  float s = 0.0f;
+  for (int64_t k = lane * 8; k < p.K; k += 512) {
+    const u32x4_t a = ldg_b128_cached(x + k), b = ldg_b128_cached(w + k);
+    *reinterpret_cast<u32x4_t *>(xc + k) = a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s = __builtin_fmaf(bf16_bits_to_f32(a[i] & 0xFFFFu), bf16_bits_to_f32(b[i] & 0xFFFFu), s);
+      s = __builtin_fmaf(bf16_bits_to_f32(a[i] >> 16), bf16_bits_to_f32(b[i] >> 16), s);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if (lane == 0) {
+    if (t < 0) s = __builtin_nanf("");
+    p.lt[at] = s;
+    p.ref[at] = s;
+    p.S[at] = 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Logits of a piece: strip maxima and sums, and E
+// ---------------------------------------------------------------------------
+
+// The tile's results: wave (wv, wt) holds words 128 wv .. + 127 (4 blocks) of
+// tokens 64 wt .. + 63 (2 blocks).
+template <bool GRAD>
+__global__ __launch_bounds__(THREADS, 2) void k_loss_logits(Params p) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  int tm, tn;
+  if (!map_tile(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn)) return;
+  const int live = *p.count - (int)p.row0;   // rows of this chunk that count
+  if (tm * TILE >= live) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wv = wave & 1, wt = wave >> 1, h = lane >> 5;
+  const int64_t v0 = p.v0 + (int64_t)tn * TILE;   // first word of the tile
+  const int64_t t0 = p.row0 + (int64_t)tm * TILE;
+  const int K = (int)p.K;
+  const rsrc_t wr = big::make_rsrc(p.W + v0 * p.K, big::clamp_bytes(min((int64_t)TILE, p.V - v0) * p.K * 2));
+  const rsrc_t xr = big::make_rsrc(p.Xc + t0 * p.K, big::clamp_bytes((int64_t)min(TILE, live - tm * TILE) * p.K * 2));
+  const SlabLoad ld(p.K, wave, lane);
+
+  f32x16_t acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
+
+  auto issue = [&](int s) {
+    uint16_t *dst = smem + (s & 1) * 2 * SLAB;
+    ld.issue(wr, dst, s * BKS, K, wave);
+    ld.issue(xr, dst + SLAB, s * BKS, K, wave);
+  };
+  const int steps = (K + BKS - 1) / BKS;
+  issue(0);
+  for (int s = 0; s < steps; ++s) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // this wave's loads of step s have landed
+    __syncthreads();                      // everyone's have, and step s - 1 is done with
+    if (s + 1 < steps) issue(s + 1);
+    const uint16_t *Ws = smem + (s & 1) * 2 * SLAB, *Xs = Ws + SLAB;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      u32x4_t a[4], b[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = frag(Ws, wv * 128 + i * 32, kk, lane);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) b[j] = frag(Xs, wt * 64 + j * 32, kk, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(a[i], b[j], acc[i][j]);
+    }
+  }
+
+  // word of register r of block i: vw + 32 i + 8 (r / 4) + r % 4
+  const int vw = wv * STRIP + 4 * h;
+  const int strip = tn * 2 + wv;
+  const int vend = (int)min((int64_t)TILE, p.V - v0);   // words of the tile that exist
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int tl = tm * TILE + wt * 64 + j * 32 + (lane & 31);   // row of the chunk
+    const bool ok = tl < live;
+    const int64_t at = p.row0 + tl;
+    const float ref = ok ? p.ref[at] : INFINITY;
+    const int64_t own = ok ? (int64_t)p.tgt[at] - v0 - vw : -1;   // register index of the target
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int at_r = 32 * i + 8 * (r >> 2) + (r & 3);
+        if (at_r == own || vw + at_r >= vend) acc[i][j][r] = -INFINITY;
+        mx = fmaxf(mx, acc[i][j][r]);
+      }
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float rs = (mx - ref) * LOG2E > REF_SLACK ? mx : ref;
+    float sum = 0.0f;
+    const float rl = rs * LOG2E;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float e = exp2_hw(__builtin_fmaf(acc[i][j][r], LOG2E, -rl));
+        acc[i][j][r] = e;
+        sum += e;
+      }
+    sum += __shfl_xor(sum, 32);
+    if (h == 0) p.strip_ref[(int64_t)strip * p.rows + tl] = rs;
+    else p.strip_sum[(int64_t)strip * p.rows + tl] = sum;
+    if constexpr (GRAD) {
+      uint16_t *dst = p.E + (int64_t)tl * p.lde + tn * TILE + wv * STRIP;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          // the lane halves trade, so that each holds 8 words in a row
+          const f32x16_t &c = acc[i][j];
+          const auto w0 = __builtin_amdgcn_permlane32_swap(pack_bf16x2(c[8 * q], c[8 * q + 1]),
+                                                           pack_bf16x2(c[8 * q + 4], c[8 * q + 5]), false, false);
+          const auto w1 = __builtin_amdgcn_permlane32_swap(pack_bf16x2(c[8 * q + 2], c[8 * q + 3]),
+                                                           pack_bf16x2(c[8 * q + 6], c[8 * q + 7]), false, false);
+          *reinterpret_cast<u32x4_t *>(dst + i * 32 + q * 16 + h * 8) = u32x4_t{w0[0], w1[0], w0[1], w1[1]};
+        }
+    }
+  }
+}
+
+// The strips of a piece into the rows' sums. 32 rows to a block, 32 threads to
+// a row. Where a strip had to take a reference of its own, the row gets the
+// largest, and its E and acc are brought onto it (E is rounded a second time).
+template <bool GRAD>
+__global__ __launch_bounds__(1024) void k_loss_join(Params p) {
+  __shared__ float red[32][33], sums[32][33];
+  __shared__ float nref[32], fac[32];
+  __shared__ int moved[32];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;   // row, strip group
+  const int live = *p.count - (int)p.row0;
+  const int tl = blockIdx.x * 32 + tx;
+  if ((int)blockIdx.x * 32 >= live) return;
+  const int strips = p.tiles_n * 2;
+  const bool ok = tl < live;
+  const int64_t at = p.row0 + tl;
+  const float ref = ok ? p.ref[at] : 0.0f;
+  float mx = ref;
+  bool nan = ref != ref, other = false;
+  if (ok)
+    for (int s = ty; s < strips; s += 32) {
+      const float r = p.strip_ref[(int64_t)s * p.rows + tl];
+      nan |= r != r;
+      other |= r != ref;
+      mx = fmaxf(mx, r);
+    }
+  red[ty][tx] = nan ? __builtin_nanf("") : mx;
+  if (ty == 0) moved[tx] = 0;
+  __syncthreads();
+  if (other) moved[tx] = 1;   // (every writer writes 1)
+  if (ty == 0) {
+    float m = red[0][tx];
+    for (int i = 1; i < 32; ++i) {
+      const float r = red[i][tx];
+      m = (m != m || r != r) ? __builtin_nanf("") : fmaxf(m, r);
+    }
+    nref[tx] = m;
+  }
+  __syncthreads();
+  const float m = nref[tx];
+  float sum = 0.0f;
+  if (ok)
+    for (int s = ty; s < strips; s += 32) {
+      const float r = p.strip_ref[(int64_t)s * p.rows + tl];
+      const float v = p.strip_sum[(int64_t)s * p.rows + tl];
+      sum += r == m ? v : v * exp2_hw((r - m) * LOG2E);
+    }
+  sums[ty][tx] = sum;
+  __syncthreads();
+  if (ty == 0 && ok) {
+    float t = 0.0f;
+    for (int i = 0; i < 32; ++i) t += sums[i][tx];
+    const float f = ref == m ? 1.0f : exp2_hw((ref - m) * LOG2E);
+    p.S[at] = p.S[at] * f + t;
+    p.ref[at] = m;
+    fac[tx] = f;
+  }
+  if constexpr (GRAD) {
+    __syncthreads();
+    for (int r = 0; r < 32; ++r) {
+      const int row = blockIdx.x * 32 + r;
+      if (row >= live || !moved[r]) continue;   // uniform
+      for (int64_t c = threadIdx.x; c < strips * STRIP; c += 1024) {
+        const float sr = p.strip_ref[(c / STRIP) * p.rows + row];
+        if (sr == nref[r]) continue;
+        uint16_t *e = p.E + (int64_t)row * p.lde + c;
+        *e = to_bf16(bf16_bits_to_f32(*e) * exp2_hw((sr - nref[r]) * LOG2E));
+      }
+      if (!p.first && fac[r] != 1.0f)
+        for (int s = 0; s < p.splits; ++s)
+          for (int64_t k = threadIdx.x; k < p.K; k += 1024) {
+            float *a = p.acc + ((int64_t)s * p.rows + row) * p.K + k;
+            *a *= fac[r];
+          }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// acc += E W_piece
+// ---------------------------------------------------------------------------
+
+// W slab: 64 words x 256 hidden columns (rows of 512 bytes, 16-byte chunk c of
+// row v at c ^ ((v & 3) << 2): the transposing read takes four rows of 64 bytes
+// at a time, which land in the four quarters of the banks).
+__device__ __forceinline__ int wat(int v, int c) { return v * TILE + ((c ^ ((v & 3) << 2)) << 3); }
+
+__device__ __forceinline__ u32x4_t frag_w(const uint16_t *lds, int v0, int col0, int lane) {
+  const int h = lane >> 5, i = lane & 15;
+  const int col = col0 + ((lane >> 4) & 1) * 16 + (i & 3) * 4;
+  const int v = v0 + 8 * h + (i >> 2);
+  const u32x2_t lo = lds_read_tr16(lds + wat(v, col >> 3) + (col & 7));
+  const u32x2_t hi = lds_read_tr16(lds + wat(v + 4, col >> 3) + (col & 7));
+  return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+}
+
+static __global__ __launch_bounds__(THREADS, 2) void k_loss_dx(Params p) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  // blocks: split fastest within an XCD's tiles
+  const int split = blockIdx.x / (((p.tiles_m * p.tiles_n + 7) / 8) * 8);
+  int tm, tn;
+  if (!map_tile(blockIdx.x % (((p.tiles_m * p.tiles_n + 7) / 8) * 8), p.tiles_m, p.tiles_n, tm, tn)) return;
+  const int live = *p.count - (int)p.row0;
+  if (tm * TILE >= live) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wk = wave & 1, wt = wave >> 1, h = lane >> 5;
+  const int c0 = tn * TILE;                 // first hidden column
+  const int K = (int)p.K;
+  const int R = (int)p.cols;
+  const int s0 = split * p.split_steps, s1 = min((R + BKS - 1) / BKS, s0 + p.split_steps);
+
+  // E: rows of the chunk (lde covers whole tiles, zero past the last word)
+  const rsrc_t er = big::make_rsrc(p.E + (int64_t)tm * TILE * p.lde, big::clamp_bytes((int64_t)TILE * p.lde * 2));
+  const SlabLoad ld(p.lde, wave, lane);
+  // W: lane's row l / 32 of a 1-KB block of two words, chunk l % 32
+  const int wrow = lane >> 5, wpos = lane & 31;
+  // block b = 8 i + wave: words 2 b, 2 b + 1
+  const int wc = wpos ^ (((2 * wave + wrow) & 3) << 2);
+  const bool wc_ok = c0 + wc * 8 < K;
+  auto issue = [&](int s) {
+    uint16_t *dst = smem + (s & 1) * 2 * SLAB;
+    const int64_t v = p.v0 + (int64_t)s * BKS;
+    const rsrc_t wr = big::make_rsrc(p.W + v * p.K, big::clamp_bytes(min((int64_t)BKS, p.v0 + p.cols - v) * p.K * 2));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int w = 2 * (8 * i + wave) + wrow;
+      load_lds16(wr, dst + (8 * i + wave) * 512, wc_ok ? (uint32_t)((w * K + c0 + wc * 8) * 2) : OOB, 0);
+    }
+    ld.issue(er, dst + SLAB, s * BKS, (int)p.lde, wave);
+  };
+
+  f32x16_t acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
+  if (s0 < s1) issue(s0);
+  for (int s = s0; s < s1; ++s) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    if (s + 1 < s1) issue(s + 1);
+    const uint16_t *Ws = smem + (s & 1) * 2 * SLAB, *Es = Ws + SLAB;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      u32x4_t a[4], b[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = frag_w(Ws, kk * 16, wk * 128 + i * 32, lane);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) b[j] = frag(Es, wt * 64 + j * 32, kk, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(a[i], b[j], acc[i][j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int tl = tm * TILE + wt * 64 + j * 32 + (lane & 31);
+    if (tl >= live) continue;
+    float *dst = p.acc + ((int64_t)split * p.rows + tl) * p.K + c0 + wk * 128 + 4 * h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (c0 + wk * 128 + i * 32 + q * 8 >= K) continue;
+        f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        f32x4_t *d = reinterpret_cast<f32x4_t *>(dst + i * 32 + q * 8);
+        if (!p.first) v += *d;
+        *d = v;
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Outputs
+// ---------------------------------------------------------------------------
+
+// Rows without a target: loss 0, lse 0, dX 0. (Before k_loss_finish; a wave to
+// a row.)
+static __global__ __launch_bounds__(256) void k_loss_ignored(Params p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (i >= p.M || p.target[i] != p.ignore) return;
+  if (lane == 0) {
+    p.loss[i] = 0.0f;
+    if (p.lse) p.lse[i] = 0.0f;
+  }
+  if (p.dX)
+    for (int64_t k = lane * 8; k < p.K; k += 512)
+      *reinterpret_cast<u32x4_t *>(p.dX + i * p.K + k) = u32x4_t{0u, 0u, 0u, 0u};
+}
+
+__device__ __forceinline__ float row_weight(const Params &p, int row, int count) {
+  return p.weight ? p.weight[row] : 1.0f / (float)count;
+}
+
+// A wave to a row of the chunk: its loss, and dX = w (acc - S W_t) / (S + s_t).
+static __global__ __launch_bounds__(256) void k_loss_finish(Params p) {
+  const int lane = threadIdx.x & 63;
+  const int tl = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int count = *p.count;
+  const int64_t at = p.row0 + tl;
+  if (at >= count || tl >= p.rows) return;
+  const int row = p.row[at];
+  const float S = p.S[at], lt = p.lt[at], ref = p.ref[at];
+  // the target's own term (1 where the reference is its logit, as it mostly is)
+  const float st = ref == lt ? 1.0f : exp2_hw((lt - ref) * LOG2E);
+  const float sum = S + st;
+  const float up = ref == lt ? log1pf(S) : logf(sum);   // lse - ref
+  if (lane == 0) {
+    p.loss[row] = ref == lt ? up : up + (ref - lt);
+    if (p.lse) p.lse[row] = up + ref;
+  }
+  if (!p.dX) return;
+  const float w = row_weight(p, row, count);
+  const float a = w / sum, b = a * S;
+  const uint16_t *wt = p.W + (int64_t)max(p.tgt[at], 0) * p.K;
+  const float *src = p.acc + (int64_t)tl * p.K;
+  for (int64_t k = lane * 8; k < p.K; k += 512) {
+    f32x4_t lo = *reinterpret_cast<const f32x4_t *>(src + k), hi = *reinterpret_cast<const f32x4_t *>(src + k + 4);
+    for (int s = 1; s < p.splits; ++s) {
+      const float *q = src + (int64_t)s * p.rows * p.K + k;
+      lo += *reinterpret_cast<const f32x4_t *>(q);
+      hi += *reinterpret_cast<const f32x4_t *>(q + 4);
+    }
+    const u32x4_t wv = ldg_b128_cached(wt + k);
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float we = bf16_bits_to_f32((wv[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+      o[e] = __builtin_fmaf(a, e < 4 ? lo[e & 3] : hi[e & 3], -(b * we));
+    }
+    *reinterpret_cast<u32x4_t *>(p.dX + (int64_t)row * p.K + k) =
+        u32x4_t{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+  }
+}
+
+// total = sum of weight times loss over the rows that count: one block, in a
+// fixed order.
+static __global__ __launch_bounds__(1024) void k_loss_total(Params p) {
+  __shared__ float red[16];
+  const int count = *p.count;
+  float s = 0.0f;
+  for (int i = threadIdx.x; i < count; i += 1024) {
+    const int row = p.row[i];
+    s += row_weight(p, row, count) * p.loss[row];
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float t = 0.0f;
+    for (int w = 0; w < 16; ++w) t += red[w];
+    *p.total = t;
+  }
+}
+
+// The kernels as the host code launches them: by address, so that they compile
+// as a unit of their own (loss.hip).
+const void *rows_kernel();
+const void *target_kernel();
+const void *logits_kernel(bool grad);
+const void *join_kernel(bool grad);
+const void *dx_kernel();
+const void *ignored_kernel();
+const void *finish_kernel();
+const void *total_kernel();
+
+}  // namespace loss
+}  // namespace lora4

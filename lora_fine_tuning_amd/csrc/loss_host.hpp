@@ -1,0 +1,144 @@
+// Host side of the vocabulary loss (included by lora4.hip behind its dispatch
+// helpers): validation, workspace layout and launch order.
+//
+//   k_loss_rows -> k_loss_target -> per chunk of rows:
+//       per piece of the vocabulary: k_loss_logits -> k_loss_join [-> k_loss_dx]
+//       k_loss_finish
+//   -> k_loss_ignored, k_loss_total
+//
+// How many rows count is known on the device alone: the grids cover all M, and
+// blocks past the last row that counts end at once.
+#pragma once
+
+namespace {
+
+// Rows of a chunk at most, and bytes of E (a chunk's rows by a piece's words): a
+// piece is wide enough that adding its part to acc in memory is small beside its
+// product, and narrow enough that E stays far below the logits' size.
+constexpr int64_t LOSS_CHUNK = 4096;
+constexpr int64_t LOSS_E_BYTES = int64_t(256) << 20;
+
+struct LossPlan {
+  int64_t chunk;       // rows of a chunk, a multiple of TILE
+  int64_t piece;       // words of a piece, a multiple of TILE
+  int splits;          // word ranges of acc's product
+  size_t off_row, off_tgt, off_xc, off_lt, off_ref, off_s, off_sref, off_ssum, off_e, off_acc, bytes;
+};
+
+// Words of a piece at most (the strips' maxima and sums, and 32-bit offsets in E).
+constexpr int64_t LOSS_PIECE = int64_t(1) << 19;
+
+// Forced width of a piece for tests (LORA4_LOSS_PIECE, in words).
+int64_t loss_piece_policy() {
+  const char *e = std::getenv("LORA4_LOSS_PIECE");
+  return e ? std::max<int64_t>(1, ceil_div(std::atoi(e), loss::TILE)) : LOSS_PIECE / loss::TILE;
+}
+
+lora4_status check_loss_sizes(int64_t M, int64_t K, int64_t V) {
+  if (M < 0 || M > (int64_t(1) << 30) || V < 1 || V > (int64_t(1) << 30) || K < 8 || K % 8 != 0 || K > (1 << 20))
+    return LORA4_ERR_SHAPE;
+  return LORA4_OK;
+}
+
+LossPlan loss_plan(bool grad, int64_t M, int64_t K, int64_t V) {
+  constexpr int64_t T = loss::TILE;
+  LossPlan pl{};
+  pl.chunk = std::min(LOSS_CHUNK, std::max<int64_t>(T, ceil_div(M, T) * T));
+  const int64_t tiles_v = ceil_div(V, T);
+  int64_t piece = std::min(tiles_v, loss_piece_policy());
+  if (grad) {
+    piece = std::max<int64_t>(1, std::min(piece, LOSS_E_BYTES / (pl.chunk * 2 * T)));
+    const int64_t tiles_k = ceil_div(K, T) * (pl.chunk / T), cus = cu_count();
+    // a tile a CU; at least 8 steps each
+    pl.splits = (int)std::max<int64_t>(1, std::min(cus / std::max<int64_t>(1, tiles_k), piece * (T / loss::BKS) / 8));
+  } else {
+    pl.splits = 1;
+  }
+  pl.piece = piece * T;
+  size_t off = 256;   // the count
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off += align256(std::max<size_t>(n, 1));
+    return at;
+  };
+  pl.off_row = take((size_t)M * 4);
+  pl.off_tgt = take((size_t)M * 4);
+  pl.off_xc = take((size_t)M * K * 2);
+  pl.off_lt = take((size_t)M * 4);
+  pl.off_ref = take((size_t)M * 4);
+  pl.off_s = take((size_t)M * 4);
+  const size_t strips = (size_t)(pl.piece / loss::STRIP) * pl.chunk * 4;
+  pl.off_sref = take(strips);
+  pl.off_ssum = take(strips);
+  if (grad) {
+    pl.off_e = take((size_t)pl.chunk * pl.piece * 2);
+    pl.off_acc = take((size_t)pl.splits * pl.chunk * K * 4);
+  }
+  pl.bytes = off;
+  return pl;
+}
+
+lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targets, const float *weights, int64_t M,
+                       int64_t K, int64_t V, int64_t ignore, float *out_loss, float *lse, float *total, uint16_t *dX,
+                       void *ws, size_t ws_bytes, hipStream_t st) {
+  TRY(check_loss_sizes(M, K, V));
+  if (!W || (M > 0 && (!X || !targets || !out_loss))) return LORA4_ERR_NULL;
+  if (!all_aligned16({X, W, targets, weights, out_loss, lse, total, dX, ws})) return LORA4_ERR_ALIGN;
+  const bool grad = dX != nullptr;
+  const LossPlan pl = loss_plan(grad, M, K, V);
+  if (!ws || ws_bytes < pl.bytes) return LORA4_ERR_WORKSPACE;
+  loss::Params p{};
+  p.X = X;
+  p.W = W;
+  p.target = targets;
+  p.weight = weights;
+  p.M = M;
+  p.K = K;
+  p.V = V;
+  p.ignore = ignore;
+  p.count = ws_at<int>(ws, 0);
+  p.row = ws_at<int>(ws, pl.off_row);
+  p.tgt = ws_at<int>(ws, pl.off_tgt);
+  p.Xc = ws_at<uint16_t>(ws, pl.off_xc);
+  p.lt = ws_at<float>(ws, pl.off_lt);
+  p.ref = ws_at<float>(ws, pl.off_ref);
+  p.S = ws_at<float>(ws, pl.off_s);
+  p.rows = (int)pl.chunk;
+  p.E = ws_at<uint16_t>(ws, pl.off_e);
+  p.lde = pl.piece;
+  p.strip_ref = ws_at<float>(ws, pl.off_sref);
+  p.strip_sum = ws_at<float>(ws, pl.off_ssum);
+  p.acc = ws_at<float>(ws, pl.off_acc);
+  p.splits = pl.splits;
+  p.loss = out_loss;
+  p.lse = lse;
+  p.total = total;
+  p.dX = dX;
+  constexpr int64_t T = loss::TILE;
+  TRY(launch_fn("loss_rows", loss::rows_kernel(), 1, 1024, 0, st, p));
+  if (M > 0) TRY(launch_fn("loss_target", loss::target_kernel(), ceil_div(M, 4), 256, 0, st, p));
+  for (int64_t row0 = 0; row0 < M; row0 += pl.chunk) {
+    p.row0 = row0;
+    const int64_t rows = std::min(pl.chunk, M - row0);
+    for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
+      p.v0 = v0;
+      p.cols = std::min(pl.piece, V - v0);
+      p.first = v0 == 0;
+      p.tiles_m = (int)ceil_div(rows, T);
+      p.tiles_n = (int)ceil_div(p.cols, T);
+      TRY(launch_fn("loss_logits", loss::logits_kernel(grad), ceil_div((int64_t)p.tiles_m * p.tiles_n, 8) * 8,
+                    loss::THREADS, loss::LDS_BYTES, st, p));
+      TRY(launch_fn("loss_join", loss::join_kernel(grad), ceil_div(rows, 32), 1024, 0, st, p));
+      if (!grad) continue;
+      p.tiles_n = (int)ceil_div(K, T);
+      p.split_steps = (int)ceil_div(ceil_div(p.cols, loss::BKS), pl.splits);
+      TRY(launch_fn("loss_dx", loss::dx_kernel(), ceil_div((int64_t)p.tiles_m * p.tiles_n, 8) * 8 * pl.splits,
+                    loss::THREADS, loss::LDS_BYTES, st, p));
+    }
+    TRY(launch_fn("loss_finish", loss::finish_kernel(), ceil_div(rows, 4), 256, 0, st, p));
+  }
+  if (M > 0) TRY(launch_fn("loss_ignored", loss::ignored_kernel(), ceil_div(M, 4), 256, 0, st, p));
+  return total ? launch_fn("loss_total", loss::total_kernel(), 1, 1024, 0, st, p) : LORA4_OK;
+}
+
+}  // namespace

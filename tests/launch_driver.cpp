@@ -96,6 +96,9 @@ void inspect(const std::string &name, void **args) {
            is(name, "k_attn_dkv_sum")) {
     const lora4::attn::Params &p = checked<lora4::attn::Params>(name, args[0]);
     if (p.G * p.Hkv != p.Hq || p.splits < 1 || (p.splits > 1 && !p.part)) fail(context.c_str(), name.c_str());
+  } else if (name.find("k_loss_") != std::string::npos) {
+    const lora4::loss::Params &p = checked<lora4::loss::Params>(name, args[0]);
+    if (p.rows < 1 || p.splits < 1 || p.lde % lora4::loss::TILE) fail(context.c_str(), name.c_str());
   } else {   // (scalars only)
     for (const char *k : {"k_attn_delta", "k_fill_u16", "k_reduce_bf16", "k_col_sum", "k_col_sum_slots", "k_quant_mxfp8"})
       if (is(name, k)) return;
@@ -460,6 +463,36 @@ void attention() {
           }
 }
 
+// The loss over the vocabulary: every launch, its refusals and sizes.
+void vocab_loss() {
+  float *F = reinterpret_cast<float *>(D);
+  const size_t most = (size_t)1 << 40;
+  for (int64_t M : {0, 1, 300, 5000})
+    for (int64_t K : {8, 2080, 8192})
+      for (int64_t V : {1, 257, 128256, 3000000})
+        for (uint16_t *dX : {D, (uint16_t *)nullptr}) {
+          context = "loss M " + std::to_string(M) + " K " + std::to_string(K) + " V " + std::to_string(V);
+          const size_t n = lora4_head_loss_workspace_bytes(dX != nullptr, M, K, V);
+          expect(lora4_head_loss(D, D, OFFS, F, M, K, V, -100, F, F, F, dX, WS, n, nullptr), LORA4_OK);
+          expect(lora4_head_loss(D, D, OFFS, nullptr, M, K, V, -100, F, F, F, dX, WS, n - 1, nullptr),
+                 LORA4_ERR_WORKSPACE);
+        }
+  context = "refusals of the loss";
+  expect(lora4_head_loss(D, D, OFFS, F, 16, 60, 100, -100, F, F, F, D, WS, most, nullptr), LORA4_ERR_SHAPE);
+  expect(lora4_head_loss(D, D, OFFS, F, std::numeric_limits<int64_t>::max(), 64, 100, -100, F, F, F, D, WS, most, nullptr),
+         LORA4_ERR_SHAPE);
+  expect(lora4_head_loss(D, nullptr, OFFS, F, 16, 64, 100, -100, F, F, F, D, WS, most, nullptr), LORA4_ERR_NULL);
+  expect(lora4_head_loss(D, D + 4, OFFS, F, 16, 64, 100, -100, F, F, F, D, WS, most, nullptr), LORA4_ERR_ALIGN);
+  for (int64_t M : {(int64_t)0, (int64_t)1, (int64_t)1 << 30, std::numeric_limits<int64_t>::max()})
+    for (int64_t K : {(int64_t)8, (int64_t)1 << 20, std::numeric_limits<int64_t>::max() - 7})
+      for (int64_t V : {(int64_t)1, (int64_t)1 << 30, std::numeric_limits<int64_t>::max()})
+        for (int grad = 0; grad < 2; ++grad) {
+          context = "loss sizes";
+          const bool ok = M <= 1 << 30 && K <= 1 << 20 && V <= 1 << 30;
+          if ((lora4_head_loss_workspace_bytes(grad, M, K, V) != 0) != ok) fail(context.c_str(), std::to_string(M).c_str());
+        }
+}
+
 // Size queries over the ends of their ranges (no call: nothing that large
 // exists), where an overflow of the planning's arithmetic would show.
 void sizes() {
@@ -513,6 +546,7 @@ int main() {
   }
   norms();
   attention();
+  vocab_loss();
   refusals();
   sizes();
   for (const auto &c : counts) std::printf("%s %d\n", c.first.c_str(), c.second);

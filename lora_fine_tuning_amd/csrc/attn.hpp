@@ -33,6 +33,8 @@
 // unfilled part) enters a product, NaN included.
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "gemm_big.hpp"
 
@@ -47,6 +49,7 @@ constexpr int KEYS = 64;      // keys of a step of these
 constexpr int BKEYS = 128;    // keys of a dK, dV tile (32 a wave)
 constexpr int BROWS = 64;     // packed query rows of a step of it
 constexpr uint32_t OOB = big::OOB;
+constexpr float SLACK = 8.0f; // binary orders a weight may exceed 1 by (see k_attn_fwd)
 constexpr float LOG2E = 1.44269504088896340736f;
 
 struct Params {
@@ -55,7 +58,7 @@ struct Params {
   int64_t Tq, Tk;
   int seqs;
   int Hq, Hkv, G, D;
-  uint32_t gmagic;            // ceil(2^32 / G), 0 for G == 1
+  uint32_t gmagic, gone;      // ceil(2^32 / G) and 0; for G == 1 0 and all ones
   float scale;
   const int64_t *qo, *ko, *kl;
   int slots;                  // row tiles (forward, dQ) or key tiles (dK, dV) of the grid
@@ -73,7 +76,7 @@ struct Params {
 
 // Query of packed row r, exact for r < 2^32 / G (which the host checks).
 __device__ __forceinline__ uint32_t row_query(const Params &p, uint32_t r) {
-  return p.gmagic ? __umulhi(r, p.gmagic) : r;
+  return __umulhi(r, p.gmagic) + (r & p.gone);
 }
 
 // One tile of the grid.
@@ -222,7 +225,26 @@ __device__ __forceinline__ u32x4_t pack8(const f32x16_t &v, int r0) {
                  pack_bf16x2(v[r0 + 6], v[r0 + 7])};
 }
 
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+// Scheduling hints: the next `n` MFMAs, LDS reads, of the block go here. The
+// compiler by itself reads each operand just before its product and waits.
+template <int N>
+__device__ __forceinline__ void sched_mfma() {
+  __builtin_amdgcn_sched_group_barrier(0x008, N, 0);
+}
+template <int N>
+__device__ __forceinline__ void sched_read() {
+  __builtin_amdgcn_sched_group_barrier(0x100, N, 0);
+}
+
+// The values of both lane halves, lower first.
+struct Halves {
+  float lo, hi;
+};
+__device__ __forceinline__ Halves both_halves(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return {__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // B operand straight from memory: this lane's row, 8 columns from 16 kk + 8 h.
@@ -263,13 +285,31 @@ __device__ __forceinline__ void store_row_f32(float *dst, const f32x16_t (&acc)[
     }
 }
 
-// Descriptor of head `head` of the keys (or values) from key k of the sequence to
-// its end.
-__device__ __forceinline__ rsrc_t kv_rsrc(const uint16_t *X, int64_t ld, const Params &p, const Tile &t, int head,
-                                          int k) {
-  const int64_t left = (int64_t)t.Lk - k;
-  return big::make_rsrc(X + (t.k0 + (left > 0 ? k : 0)) * ld + head * p.D,
-                        left > 0 ? big::clamp_bytes(((left - 1) * ld + p.D) * 2) : 0u);
+// Keys or values of one head, a tile of KEYS after another, to the sequence's end
+// (64-bit addresses: a cache may be longer than a descriptor's range).
+struct KvStream {
+  const uint16_t *at;   // first row of the next tile
+  int64_t bytes;        // from there to the end
+  int64_t step;         // elements per tile
+  __device__ __forceinline__ KvStream(const uint16_t *X, int64_t ld, const Params &p, const Tile &t, int head, int k)
+      : at(X + (t.k0 + k) * ld + head * p.D), bytes((((int64_t)t.Lk - k - 1) * ld + p.D) * 2), step(KEYS * ld) {}
+  __device__ __forceinline__ rsrc_t next() {
+    const rsrc_t r = big::make_rsrc(at, (uint32_t)(bytes >> 31) ? 0x7FFFFFFFu : (uint32_t)bytes);
+    at += step;
+    bytes -= step * 2;
+    return r;
+  }
+};
+
+// Runs body(step, stage) for the steps from s0, the stage (0, 1, 0, ..) a
+// constant: LDS addresses of both stages are immediate offsets.
+template <typename F>
+__device__ __forceinline__ void two_stages(int s0, int s1, F &&body) {
+  for (int s = s0; s < s1; ++s) {
+    body(s, std::integral_constant<int, 0>{});
+    if (++s >= s1) break;
+    body(s, std::integral_constant<int, 1>{});
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -315,26 +355,30 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
   f32x16_t acc[DC];
 #pragma unroll
   for (int i = 0; i < DC; ++i) acc[i] = f32x16_t{};
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l[2] = {0.0f, 0.0f};
   const float c = p.scale * LOG2E;
   const int lim = qi + off;   // last key this lane's row sees
 
-  auto issue = [&](int s) {
-    const int k = s * KEYS;
-    uint16_t *dst = smem + (s & 1) * 2 * TE;
-    load_kv<DC, KEYS>(kv_rsrc(p.K, p.ldk, p, t, j.head, k), dst, p.ldk, p.D, wave, lane);
-    load_kv<DC, KEYS>(kv_rsrc(p.V, p.ldv, p, t, j.head, k), dst + TE, p.ldv, p.D, wave, lane);
+  const int wend = min(kend, (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + wave * 32 + 31)) + off + 1);
+  KvStream ks(p.K, p.ldk, p, t, j.head, t0 * KEYS), vs(p.V, p.ldv, p, t, j.head, t0 * KEYS);
+  auto issue = [&](int stage) {
+    uint16_t *dst = smem + stage * 2 * TE;
+    load_kv<DC, KEYS>(ks.next(), dst, p.ldk, p.D, wave, lane);
+    load_kv<DC, KEYS>(vs.next(), dst + TE, p.ldv, p.D, wave, lane);
   };
 
-  if (t0 < nt) issue(t0);
-  for (int s = t0; s < nt; ++s) {
+  if (t0 < nt) issue(0);
+  two_stages(t0, nt, [&](int s, auto stage) {
+    constexpr int ST = decltype(stage)::value;
     __builtin_amdgcn_s_waitcnt(0x0F70);   // this wave's loads of step s have landed
     __syncthreads();                      // everyone's have, and step s - 1 is done with
-    if (s + 1 < nt) issue(s + 1);
-    const uint16_t *Ks = smem + (s & 1) * 2 * TE, *Vs = Ks + TE;
+    if (s + 1 < nt) issue(ST ^ 1);
+    const uint16_t *Ks = smem + ST * 2 * TE, *Vs = Ks + TE;
     const int k0 = s * KEYS;
+    if (k0 >= wend) return;   // (no row of the wave sees these keys)
 
     f32x16_t sc[2];
+    u32x4_t vf[DC];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       sc[kb] = f32x16_t{};
@@ -342,7 +386,22 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
       for (int kk = 0; kk < 2 * DC; ++kk)
         sc[kb] = mfma_32x32x16(frag_rows<DC>(Ks, kb * 32, kk, lane), qf[kk], sc[kb]);
     }
+#pragma unroll
+    for (int db = 0; db < DC; ++db) vf[db] = frag_cols<DC>(Vs, 0, db, lane);
+    // four reads ahead of the products, V's first operands behind the last ones
+    sched_read<4>();
+#pragma unroll
+    for (int i = 0; i < 4 * DC - 4; ++i) {
+      sched_mfma<1>();
+      sched_read<1>();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sched_mfma<1>();
+      sched_read<(2 * DC + 3) / 4>();
+    }
     if (k0 + KEYS > full) {
+      asm volatile("");   // a branch, not 32 selects in every step
       const int lk = lim - k0 - 4 * h;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -355,15 +414,20 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mt = fmaxf(mt, sc[kb][i]);
-    mt = fmaxf(mt, other_half(mt));
-    if (__ballot(mt > m)) {
+    const Halves mh = both_halves(mt);
+    mt = fmaxf(mh.lo, mh.hi);
+    // The reference m follows the running maximum only where a row's has grown by
+    // more than SLACK binary orders (always in the first step): weights up to
+    // 2^SLACK lose nothing in bf16 and fp32, and the rescaling is rare.
+    if (__ballot((mt - m) * c > SLACK)) {
       const float mn = fmaxf(m, mt);
       const float a = mn == m ? 1.0f : exp2_hw((m - mn) * c);
 #pragma unroll
       for (int i = 0; i < DC; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][e] *= a;
-      l *= a;
+      l[0] *= a;
+      l[1] *= a;
       m = mn;
     }
     const float mc = m == -INFINITY ? 0.0f : m * c;
@@ -373,29 +437,39 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
       for (int i = 0; i < 16; ++i) {
         const float e = exp2_hw(__builtin_fmaf(sc[kb][i], c, -mc));
         sc[kb][i] = e;
-        l += e;
+        l[i & 1] += e;
       }
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const u32x4_t pf = pack8(sc[b >> 1], (b & 1) * 8);
 #pragma unroll
-      for (int db = 0; db < DC; ++db) acc[db] = mfma_32x32x16(frag_cols<DC>(Vs, b * 16, db, lane), pf, acc[db]);
+      for (int db = 0; db < DC; ++db) {
+        acc[db] = mfma_32x32x16(vf[db], pf, acc[db]);
+        if (b < 3) vf[db] = frag_cols<DC>(Vs, (b + 1) * 16, db, lane);
+      }
     }
-  }
+#pragma unroll
+    for (int i = 0; i < 3 * DC; ++i) {
+      sched_mfma<1>();
+      sched_read<2>();
+    }
+    sched_mfma<DC>();
+  });
 
-  l += other_half(l);
+  const Halves lh = both_halves(l[0] + l[1]);
+  const float ls = lh.lo + lh.hi;
   if (!row_ok) return;
   if (p.splits > 1) {
     const int64_t pi = (int64_t)j.split * p.Tq * p.Hq + oi;
     store_row_f32<DC>(p.part + pi * p.D, acc, p.D, h);
     if (h == 0) {
       p.part_ml[2 * pi] = m * c;
-      p.part_ml[2 * pi + 1] = l;
+      p.part_ml[2 * pi + 1] = ls;
     }
     return;
   }
-  store_row<DC>(p.O + oi * p.D, acc, l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l), p.D, h);
-  if (p.lse && h == 0) p.lse[oi] = l == 0.0f ? -INFINITY : m * p.scale + __logf(l);
+  store_row<DC>(p.O + oi * p.D, acc, ls > 0.0f ? 1.0f / ls : (ls == 0.0f ? 0.0f : ls), p.D, h);
+  if (p.lse && h == 0) p.lse[oi] = ls == 0.0f ? -INFINITY : m * p.scale + __logf(ls);
 }
 
 // Joins the key ranges of a row: a wave to a row, two columns a lane.
@@ -490,45 +564,72 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
   const float c = p.scale * LOG2E;
   const int lim = qi + off;
 
-  auto issue = [&](int s) {
-    const int k = s * KEYS;
-    uint16_t *dst = smem + (s & 1) * 2 * TE;
-    load_kv<DC, KEYS>(kv_rsrc(p.K, p.ldk, p, t, j.head, k), dst, p.ldk, p.D, wave, lane);
-    load_kv<DC, KEYS>(kv_rsrc(p.V, p.ldv, p, t, j.head, k), dst + TE, p.ldv, p.D, wave, lane);
+  const int wend = min(kend, (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + wave * 32 + 31)) + off + 1);
+  KvStream ks(p.K, p.ldk, p, t, j.head, 0), vs(p.V, p.ldv, p, t, j.head, 0);
+  auto issue = [&](int stage) {
+    uint16_t *dst = smem + stage * 2 * TE;
+    load_kv<DC, KEYS>(ks.next(), dst, p.ldk, p.D, wave, lane);
+    load_kv<DC, KEYS>(vs.next(), dst + TE, p.ldv, p.D, wave, lane);
   };
 
   if (nt > 0) issue(0);
-  for (int s = 0; s < nt; ++s) {
+  two_stages(0, nt, [&](int s, auto stage) {
+    constexpr int ST = decltype(stage)::value;
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
-    if (s + 1 < nt) issue(s + 1);
-    const uint16_t *Ks = smem + (s & 1) * 2 * TE, *Vs = Ks + TE;
+    if (s + 1 < nt) issue(ST ^ 1);
+    const uint16_t *Ks = smem + ST * 2 * TE, *Vs = Ks + TE;
     const int k0 = s * KEYS;
+    if (k0 >= wend) return;
     const bool edge = k0 + KEYS > full;
     const int lk = lim - k0 - 4 * h;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       f32x16_t sc = f32x16_t{}, dp = f32x16_t{};
+      u32x4_t cf[DC];
 #pragma unroll
       for (int kk = 0; kk < 2 * DC; ++kk) {
         sc = mfma_32x32x16(frag_rows<DC>(Ks, kb * 32, kk, lane), qf[kk], sc);
         dp = mfma_32x32x16(frag_rows<DC>(Vs, kb * 32, kk, lane), of[kk], dp);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float ds = exp2_hw(__builtin_fmaf(sc[i], c, -lse2)) * (dp[i] - dl);
-        if (edge && kb * 32 + 8 * (i >> 2) + (i & 3) > lk) ds = 0.0f;
-        sc[i] = ds;
+      for (int db = 0; db < DC; ++db) cf[db] = frag_cols<DC>(Ks, kb * 32, db, lane);
+      sched_read<4>();
+#pragma unroll
+      for (int i = 0; i < 4 * DC - 4; ++i) {
+        sched_mfma<1>();
+        sched_read<1>();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sched_mfma<1>();
+        sched_read<(2 * DC + 3) / 4>();
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sc[i] = exp2_hw(__builtin_fmaf(sc[i], c, -lse2)) * (dp[i] - dl);
+      if (edge) {
+        asm volatile("");   // a branch, not selects in every step
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (kb * 32 + 8 * (i >> 2) + (i & 3) > lk) sc[i] = 0.0f;
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const u32x4_t df = pack8(sc, b * 8);
 #pragma unroll
-        for (int db = 0; db < DC; ++db)
-          acc[db] = mfma_32x32x16(frag_cols<DC>(Ks, kb * 32 + b * 16, db, lane), df, acc[db]);
+        for (int db = 0; db < DC; ++db) {
+          acc[db] = mfma_32x32x16(cf[db], df, acc[db]);
+          if (b == 0) cf[db] = frag_cols<DC>(Ks, kb * 32 + 16, db, lane);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < DC; ++i) {
+        sched_mfma<1>();
+        sched_read<2>();
+      }
+      sched_mfma<DC>();
     }
-  }
+  });
   if (row_ok) store_row<DC>(p.dQ + (t.q0 + qi) * p.lddq + hd, acc, p.scale, p.D, h);
 }
 
@@ -546,7 +647,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
   Job j = map_job(p);
   const Tile t = map_tile<true>(p, j.slot, BKEYS);
   if (t.tile < 0) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, lane0 = lane;
   const int h = lane >> 5;
   const int R = t.Lq * p.G;
   const int off = t.Lk - t.Lq;
@@ -580,6 +681,9 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
     const int r0 = s * BROWS;
     const int q0 = (int)row_query(p, (uint32_t)r0);
     uint16_t *dst = smem + (s & 1) * 2 * TE;
+    uint32_t ln = (uint32_t)lane0;
+    pin(ln);   // (see below)
+    const int lane = (int)ln;
     const int64_t left = (int64_t)t.Lq - q0;
     const int64_t ldo = (int64_t)p.Hq * p.D;
     const rsrc_t rq = big::make_rsrc(p.Q + (t.q0 + q0) * p.ldq, big::clamp_bytes(((left - 1) * p.ldq + ldo) * 2));
@@ -636,14 +740,20 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
     const uint16_t *Qs = smem + (s & 1) * 2 * TE, *Os = Qs + TE;
     const float *sl = stat + (s & 1) * 3 * BROWS;
     const bool edge = (int64_t)s * BROWS < full;
-#pragma unroll
+#pragma unroll 1
     for (int rb = 0; rb < 2; ++rb) {
+      // (opaque: the operand addresses are made where they are used, not kept over
+      // the loop, which has no registers to spare)
+      uint32_t ln = (uint32_t)lane0;
+      pin(ln);
+      const int lane = (int)ln, h = lane >> 5;
       f32x16_t sc = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
       for (int kk = 0; kk < 2 * DC; ++kk) {
         sc = mfma_32x32x16(frag_rows<DC>(Qs, rb * 32, kk, lane), kf[kk], sc);
-        dp = mfma_32x32x16(frag_rows<DC>(Os, rb * 32, kk, lane), vf[kk], dp);
       }
+#pragma unroll
+      for (int kk = 0; kk < 2 * DC; ++kk) dp = mfma_32x32x16(frag_rows<DC>(Os, rb * 32, kk, lane), vf[kk], dp);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = rb * 32 + 8 * i + 4 * h;
@@ -651,11 +761,17 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
         const f32x4_t d4 = *reinterpret_cast<const f32x4_t *>(sl + BROWS + row);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float pe = exp2_hw(__builtin_fmaf(sc[4 * i + e], c, -l4[e]));
-          float ds = pe * (dp[4 * i + e] - d4[e]);
-          if (edge && key > reinterpret_cast<const int *>(sl)[2 * BROWS + row + e]) pe = ds = 0.0f;
+          const float pe = exp2_hw(__builtin_fmaf(sc[4 * i + e], c, -l4[e]));
+          dp[4 * i + e] = pe * (dp[4 * i + e] - d4[e]);
           sc[4 * i + e] = pe;
-          dp[4 * i + e] = ds;
+        }
+      }
+      if (edge) {
+        asm volatile("");   // a branch, not selects in every step
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int last = reinterpret_cast<const int *>(sl)[2 * BROWS + rb * 32 + 8 * (i >> 2) + 4 * h + (i & 3)];
+          if (key > last) sc[i] = dp[i] = 0.0f;
         }
       }
 #pragma unroll

@@ -96,6 +96,7 @@ attn::Params attn_params(const lora4_attn *a, const uint16_t *Q, const uint16_t 
   p.G = a->Hq / a->Hkv;
   p.D = a->D;
   p.gmagic = p.G == 1 ? 0u : (uint32_t)(((uint64_t(1) << 32) + p.G - 1) / p.G);
+  p.gone = p.G == 1 ? ~0u : 0u;
   p.scale = a->scale;
   p.qo = a->q_offsets;
   p.ko = a->k_offsets ? a->k_offsets : a->q_offsets;

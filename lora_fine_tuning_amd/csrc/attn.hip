@@ -17,7 +17,6 @@ const void *fwd_kernel(int dc) {
   return dc == 2 ? addr(k_attn_fwd<2>) : dc == 3 ? addr(k_attn_fwd<3>) : addr(k_attn_fwd<4>);
 }
 const void *join_kernel() { return addr(k_attn_join); }
-const void *delta_kernel() { return addr(k_attn_delta); }
 const void *dq_kernel(int dc) {
   return dc == 2 ? addr(k_attn_dq<2>) : dc == 3 ? addr(k_attn_dq<3>) : addr(k_attn_dq<4>);
 }

@@ -69,7 +69,8 @@ struct Params {
   float *part_ml;             // forward: [splits][Tq Hq][2] running maximum and sum
   // backward
   const uint16_t *dO;
-  const float *delta;         // [Tq][Hq]
+  const uint16_t *Oin;        // the forward's O
+  float *stat;                // [2][Tq][Hq]: lse log2 e and delta, made by k_attn_dq
   uint16_t *dQ, *dK, *dV;
   int64_t lddq, lddk, lddv;
 };
@@ -359,7 +360,9 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
   const float c = p.scale * LOG2E;
   const int lim = qi + off;   // last key this lane's row sees
 
-  const int wend = min(kend, (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + wave * 32 + 31)) + off + 1);
+  // keys that any row of the wave sees (none where it has no rows)
+  const int wr0 = t.tile * ROWS + wave * 32;
+  const int wend = wr0 < R ? min(kend, (int)row_query(p, (uint32_t)min(R - 1, wr0 + 31)) + off + 1) : 0;
   KvStream ks(p.K, p.ldk, p, t, j.head, t0 * KEYS), vs(p.V, p.ldv, p, t, j.head, t0 * KEYS);
   auto issue = [&](int stage) {
     uint16_t *dst = smem + stage * 2 * TE;
@@ -368,7 +371,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
   };
 
   if (t0 < nt) issue(0);
-  two_stages(t0, nt, [&](int s, auto stage) {
+  two_stages(t0, nt, [&](int s, auto stage) __attribute__((always_inline)) {
     constexpr int ST = decltype(stage)::value;
     __builtin_amdgcn_s_waitcnt(0x0F70);   // this wave's loads of step s have landed
     __syncthreads();                      // everyone's have, and step s - 1 is done with
@@ -472,7 +475,9 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
   if (p.lse && h == 0) p.lse[oi] = ls == 0.0f ? -INFINITY : m * p.scale + __logf(ls);
 }
 
-// Joins the key ranges of a row: a wave to a row, two columns a lane.
+// Joins the key ranges of a row: a wave to a row; a lane to a range for its
+// maximum and sum, then to two columns.
+constexpr int MAX_SPLITS = 64;
 static __global__ __launch_bounds__(THREADS) void k_attn_join(Params p) {
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -480,24 +485,39 @@ static __global__ __launch_bounds__(THREADS) void k_attn_join(Params p) {
   if (row >= rows) return;
   const int64_t q = row / p.Hq;
   if (p.qo && (q < p.qo[0] || q >= p.qo[p.seqs])) return;   // rows of no sequence
-  float mx = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) mx = fmaxf(mx, p.part_ml[2 * (s * rows + row)]);
-  float l = 0.0f;
-  float o[2] = {0.0f, 0.0f};
-  for (int s = 0; s < p.splits; ++s) {
-    const int64_t pi = s * rows + row;
-    const float ls = p.part_ml[2 * pi + 1];
-    if (ls == 0.0f) continue;   // (a NaN is not 0)
-    const float a = exp2_hw(p.part_ml[2 * pi] - mx);
-    l += a * ls;
+  float ms = -INFINITY, ls = 0.0f;
+  if (lane < p.splits) {
+    const float *ml = p.part_ml + 2 * (lane * rows + row);
+    ms = ml[0];
+    ls = ml[1];
+  }
+  float mx = ls != 0.0f ? ms : -INFINITY;   // (a NaN is not 0)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int d = lane * 2 + e;
-      if (d < p.D) o[e] += a * p.part[pi * p.D + d];
+  for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+  const float as = ls != 0.0f ? exp2_hw(ms - mx) : 0.0f;
+  float l = as * ls;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
+  float o0 = 0.0f, o1 = 0.0f;
+  const int d = lane * 2;
+  for (int s0 = 0; s0 < p.splits; s0 += 8) {
+    f32x2_t v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      v[u] = f32x2_t{0.0f, 0.0f};
+      // (a range without keys has not been written)
+      if (s0 + u < p.splits && d < p.D && __shfl(ls, s0 + u) != 0.0f)
+        v[u] = *reinterpret_cast<const f32x2_t *>(p.part + ((s0 + u) * rows + row) * p.D + d);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float a = __shfl(as, (s0 + u) & 63);
+      o0 = __builtin_fmaf(a, v[u][0], o0);
+      o1 = __builtin_fmaf(a, v[u][1], o1);
     }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (lane * 2 < p.D) *reinterpret_cast<uint32_t *>(p.O + row * p.D + lane * 2) = pack_bf16x2(o[0] * inv, o[1] * inv);
+  if (d < p.D) *reinterpret_cast<uint32_t *>(p.O + row * p.D + d) = pack_bf16x2(o0 * inv, o1 * inv);
   if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : mx * (1.0f / LOG2E) + __logf(l);
 }
 
@@ -505,26 +525,11 @@ static __global__ __launch_bounds__(THREADS) void k_attn_join(Params p) {
 // Backward
 // ---------------------------------------------------------------------------
 
-// delta = sum over the columns of dO O: 16 lanes to a (token, head).
-static __global__ __launch_bounds__(THREADS) void k_attn_delta(const uint16_t *O, const uint16_t *dO, int64_t rows, int D,
-                                                         float *delta) {
-  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int c = (threadIdx.x & 15) * 8;
-  float s = 0.0f;
-  if (row < rows && c < D) {
-    const u32x4_t a = ldg_b128_cached(O + row * D + c), b = ldg_b128_cached(dO + row * D + c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s = __builtin_fmaf(bf16_bits_to_f32(a[i] & 0xFFFFu), bf16_bits_to_f32(b[i] & 0xFFFFu), s);
-      s = __builtin_fmaf(bf16_bits_to_f32(a[i] >> 16), bf16_bits_to_f32(b[i] >> 16), s);
-    }
-  }
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o);
-  if (row < rows && (threadIdx.x & 15) == 0) delta[row] = s;
-}
-
-// dQ: a tile of rows over its keys, as the forward.
+// dQ: a tile of rows over its keys, as the forward. It also makes the rows' delta
+// for k_attn_dkv, which runs after it: delta from the bf16 O is off by O's
+// rounding, which shows as rows of dS that do not sum to zero; their fp32 sum is
+// added to it, so that dK is free of that error (dQ keeps it: it would take the
+// product P K as well).
 template <int DC>
 __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
   using T = Lds<DC>;
@@ -550,7 +555,20 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
   const float ls = p.lse[oi];
   // a row that saw no key has no gradient: P = exp2(-inf) = 0
   const float lse2 = ls == -INFINITY ? INFINITY : ls * LOG2E;
-  const float dl = p.delta[oi];
+  float dl = 0.0f;
+#pragma unroll
+  for (int kk = 0; kk < 2 * DC; ++kk) {
+    const int col = 16 * kk + 8 * h;
+    const u32x4_t o = row_ok && col < p.D ? ldg_b128_cached(p.Oin + oi * p.D + col) : u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      dl = __builtin_fmaf(bf16_bits_to_f32(o[e] & 0xFFFFu), bf16_bits_to_f32(of[kk][e] & 0xFFFFu), dl);
+      dl = __builtin_fmaf(bf16_bits_to_f32(o[e] >> 16), bf16_bits_to_f32(of[kk][e] >> 16), dl);
+    }
+  }
+  const Halves dh = both_halves(dl);
+  dl = dh.lo + dh.hi;
+  float rest = 0.0f;   // sum of the row's dS
 
   const int q_hi = (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + ROWS - 1));
   const int q_lo = (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + wave * 32));
@@ -564,7 +582,9 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
   const float c = p.scale * LOG2E;
   const int lim = qi + off;
 
-  const int wend = min(kend, (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + wave * 32 + 31)) + off + 1);
+  // keys that any row of the wave sees (none where it has no rows)
+  const int wr0 = t.tile * ROWS + wave * 32;
+  const int wend = wr0 < R ? min(kend, (int)row_query(p, (uint32_t)min(R - 1, wr0 + 31)) + off + 1) : 0;
   KvStream ks(p.K, p.ldk, p, t, j.head, 0), vs(p.V, p.ldv, p, t, j.head, 0);
   auto issue = [&](int stage) {
     uint16_t *dst = smem + stage * 2 * TE;
@@ -573,7 +593,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
   };
 
   if (nt > 0) issue(0);
-  two_stages(0, nt, [&](int s, auto stage) {
+  two_stages(0, nt, [&](int s, auto stage) __attribute__((always_inline)) {
     constexpr int ST = decltype(stage)::value;
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
@@ -614,6 +634,8 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
           if (kb * 32 + 8 * (i >> 2) + (i & 3) > lk) sc[i] = 0.0f;
       }
 #pragma unroll
+      for (int i = 0; i < 16; ++i) rest += sc[i];
+#pragma unroll
       for (int b = 0; b < 2; ++b) {
         const u32x4_t df = pack8(sc, b * 8);
 #pragma unroll
@@ -630,7 +652,13 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
       sched_mfma<DC>();
     }
   });
-  if (row_ok) store_row<DC>(p.dQ + (t.q0 + qi) * p.lddq + hd, acc, p.scale, p.D, h);
+  const Halves rh = both_halves(rest);
+  if (!row_ok) return;
+  if (h == 0) {
+    p.stat[oi] = lse2;
+    p.stat[p.Tq * p.Hq + oi] = dl + (rh.lo + rh.hi);
+  }
+  store_row<DC>(p.dQ + (t.q0 + qi) * p.lddq + hd, acc, p.scale, p.D, h);
 }
 
 // dK, dV: a tile of keys (32 a wave, K and V in registers) over the packed rows
@@ -641,8 +669,8 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
   constexpr int TE = BROWS * T::RW;
   constexpr int RPI = 64 / T::CH, NI = BROWS / RPI / 4;
-  // Q and dO of two steps, then lse (times log2 e), delta and last key of the rows
-  float *stat = reinterpret_cast<float *>(smem + 4 * TE);   // [2][3][BROWS]
+  // Q and dO of two steps, then lse (times log2 e) and delta of their rows
+  float *stat = reinterpret_cast<float *>(smem + 4 * TE);   // [2][2][BROWS]
 
   Job j = map_job(p);
   const Tile t = map_tile<true>(p, j.slot, BKEYS);
@@ -669,6 +697,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
     s0 = min(s1, s0 + j.split * per);
     s1 = min(s1, s0 + per);
   }
+  constexpr int AHEAD = 3;   // reads ahead of their products
   // from this row on every row sees every key of the wave
   const int64_t full = (int64_t)max(0, kt + wave * 32 + 31 - off) * p.G;
 
@@ -677,10 +706,12 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
   for (int i = 0; i < DC; ++i) dk[i] = dv[i] = f32x16_t{};
   const float c = p.scale * LOG2E;
 
-  auto issue = [&](int s) {
+  // The wave's first row with a key to see of its own.
+  const int64_t mine = (int64_t)max(0, kt + wave * 32 - off) * p.G;
+  auto issue = [&](int s, int stage) {
     const int r0 = s * BROWS;
     const int q0 = (int)row_query(p, (uint32_t)r0);
-    uint16_t *dst = smem + (s & 1) * 2 * TE;
+    uint16_t *dst = smem + stage * 2 * TE;
     uint32_t ln = (uint32_t)lane0;
     pin(ln);   // (see below)
     const int lane = (int)ln;
@@ -698,47 +729,27 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
       load_lds16(rq, dst + (i * 4 + wave) * 512, ok ? ((q - q0) * (uint32_t)p.ldq + hd) * 2 : OOB);
       load_lds16(ro, dst + TE + (i * 4 + wave) * 512, ok ? ((q - q0) * (uint32_t)ldo + hd) * 2 : OOB);
     }
-  };
-  // the rows' statistics of step s, a row to a thread
-  float st_l = 0.0f, st_d = 0.0f;
-  int st_k = 0;
-  auto stats = [&](int s) {
-    const int r = s * BROWS + (int)threadIdx.x;
-    st_l = INFINITY;   // P = 0
-    st_d = 0.0f;
-    st_k = -1;
-    if (threadIdx.x < BROWS && r < R) {
-      const int q = (int)row_query(p, (uint32_t)r);
-      const int64_t oi = (t.q0 + q) * p.Hq + j.head * p.G + (r - q * p.G);
-      const float ls = p.lse[oi];
-      if (ls != -INFINITY) st_l = ls * LOG2E;
-      st_d = p.delta[oi];
-      st_k = q + off;
-    }
-  };
-  auto put_stats = [&](int s) {
-    if (threadIdx.x < BROWS) {
-      float *d = stat + (s & 1) * 3 * BROWS + threadIdx.x;
-      d[0] = st_l;
-      d[BROWS] = st_d;
-      reinterpret_cast<int *>(d)[2 * BROWS] = st_k;
+    // a row to a lane: the first wave loads lse, the second delta (rows that are
+    // not there: zeros, as Q and dO, which make zeros of their products)
+    if (wave < 2) {
+      const uint32_t q = row_query(p, (uint32_t)(r0 + lane));
+      const uint32_t at = (q - q0) * (uint32_t)p.Hq + (uint32_t)(j.head * p.G + (r0 + lane) - (int)q * p.G);
+      const rsrc_t rs = big::make_rsrc(p.stat + (wave * p.Tq + t.q0 + q0) * p.Hq, big::clamp_bytes(left * p.Hq * 4));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void *)(stat + (stage * 2 + wave) * BROWS), 4,
+          r0 + lane < R ? at * 4 : OOB, 0, 0, 0);
     }
   };
 
-  if (s0 < s1) {
-    issue(s0);
-    stats(s0);
-    put_stats(s0);
-  }
-  for (int s = s0; s < s1; ++s) {
+  if (s0 < s1) issue(s0, 0);
+  two_stages(s0, s1, [&](int s, auto stage) __attribute__((always_inline)) {
+    constexpr int ST = decltype(stage)::value;
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
-    if (s + 1 < s1) {
-      issue(s + 1);
-      stats(s + 1);
-    }
-    const uint16_t *Qs = smem + (s & 1) * 2 * TE, *Os = Qs + TE;
-    const float *sl = stat + (s & 1) * 3 * BROWS;
+    if (s + 1 < s1) issue(s + 1, ST ^ 1);
+    if ((int64_t)(s + 1) * BROWS <= mine) return;   // (no row sees the wave's keys)
+    const uint16_t *Qs = smem + ST * 2 * TE, *Os = Qs + TE;
+    const float *sl = stat + ST * 2 * BROWS;
     const bool edge = (int64_t)s * BROWS < full;
 #pragma unroll 1
     for (int rb = 0; rb < 2; ++rb) {
@@ -749,13 +760,13 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
       const int lane = (int)ln, h = lane >> 5;
       f32x16_t sc = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
-      for (int kk = 0; kk < 2 * DC; ++kk) {
-        sc = mfma_32x32x16(frag_rows<DC>(Qs, rb * 32, kk, lane), kf[kk], sc);
-      }
+      for (int kk = 0; kk < 2 * DC; ++kk) sc = mfma_32x32x16(frag_rows<DC>(Qs, rb * 32, kk, lane), kf[kk], sc);
 #pragma unroll
       for (int kk = 0; kk < 2 * DC; ++kk) dp = mfma_32x32x16(frag_rows<DC>(Os, rb * 32, kk, lane), vf[kk], dp);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (i > 0) __builtin_amdgcn_sched_barrier(0);
         const int row = rb * 32 + 8 * i + 4 * h;
         const f32x4_t l4 = *reinterpret_cast<const f32x4_t *>(sl + row);
         const f32x4_t d4 = *reinterpret_cast<const f32x4_t *>(sl + BROWS + row);
@@ -770,12 +781,13 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
         asm volatile("");   // a branch, not selects in every step
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int last = reinterpret_cast<const int *>(sl)[2 * BROWS + rb * 32 + 8 * (i >> 2) + 4 * h + (i & 3)];
-          if (key > last) sc[i] = dp[i] = 0.0f;
+          const uint32_t r = (uint32_t)(s * BROWS + rb * 32 + 8 * (i >> 2) + 4 * h + (i & 3));
+          if (key > (int)row_query(p, r) + off) sc[i] = dp[i] = 0.0f;
         }
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
+        __builtin_amdgcn_sched_barrier(0);
         const u32x4_t pf = pack8(sc, b * 8), df = pack8(dp, b * 8);
 #pragma unroll
         for (int db = 0; db < DC; ++db) {
@@ -784,8 +796,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
         }
       }
     }
-    if (s + 1 < s1) put_stats(s + 1);
-  }
+  });
   if (!key_ok) return;
   if (p.splits > 1) {
     const int64_t n = p.Tk * p.Hkv * p.D;
@@ -827,7 +838,6 @@ static __global__ __launch_bounds__(THREADS) void k_attn_dkv_sum(Params p) {
 int col_blocks(int D);
 const void *fwd_kernel(int dc);
 const void *join_kernel();
-const void *delta_kernel();
 const void *dq_kernel(int dc);
 const void *dkv_kernel(int dc);
 const void *dkv_sum_kernel();

@@ -3,7 +3,7 @@
 //
 //   forward  : k_attn_fwd, over ranges of the keys where the row tiles alone do
 //              not fill the chip, then k_attn_join
-//   backward : k_attn_delta -> k_attn_dq, k_attn_dkv (over ranges of the rows
+//   backward : k_attn_dq (and delta) -> k_attn_dkv (over ranges of the rows
 //              where the key tiles do not fill the chip, then k_attn_dkv_sum)
 #pragma once
 
@@ -32,6 +32,7 @@ lora4_status check_attn_sizes(int64_t Tq, int64_t Tk, int64_t seqs, int32_t Hq, 
 // Blocks that keep the chip busy: two a CU.
 int64_t attn_full_grid() { return 2 * (int64_t)cu_count(); }
 
+int64_t tune(const char *n, int64_t d) { const char *e = std::getenv(n); return e ? std::atoll(e) : d; }
 AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int Hkv, int D) {
   AttnPlan pl{};
   const int64_t G = Hq / Hkv;
@@ -44,7 +45,7 @@ AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int 
   if (which == 0) {
     const int64_t blocks = std::max<int64_t>(1, std::max(Tq * G / attn::ROWS, std::min(seqs, Tq)) * Hkv);
     const int64_t most = std::max<int64_t>(1, keys / (4 * attn::KEYS));
-    pl.splits = (int)std::min<int64_t>(std::min<int64_t>(64, most), std::max<int64_t>(1, attn_full_grid() / blocks));
+    pl.splits = (int)std::min<int64_t>(std::min<int64_t>(attn::MAX_SPLITS, most), std::max<int64_t>(1, tune("TA", 4) * attn_full_grid() / 4 / blocks));
     pl.bytes = 256;
     if (pl.splits > 1) {
       pl.off_part = align256((size_t)pl.splits * Tq * Hq * 8);
@@ -54,8 +55,8 @@ AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int 
     const int64_t blocks = std::max<int64_t>(1, std::max(Tk / attn::BKEYS, std::min(seqs, Tk)) * Hkv);
     const int64_t most = std::max<int64_t>(1, rows / (8 * attn::BROWS));
     pl.ksplits = (int)std::min<int64_t>(std::min<int64_t>(16, most),
-                                        std::max<int64_t>(1, ceil_div(2 * attn_full_grid(), blocks)));
-    pl.off_part = align256((size_t)std::max<int64_t>(1, Tq * Hq) * 4);
+                                        std::max<int64_t>(1, ceil_div(tune("TB", 4) * attn_full_grid() / 2, blocks)));
+    pl.off_part = align256((size_t)std::max<int64_t>(1, Tq * Hq) * 8);
     pl.bytes = pl.off_part + (pl.ksplits > 1 ? align256((size_t)pl.ksplits * 2 * Tk * Hkv * D * 4) : 0);
   }
   return pl;
@@ -107,7 +108,7 @@ attn::Params attn_params(const lora4_attn *a, const uint16_t *Q, const uint16_t 
 
 // LDS of a step's two tiles, twice, and (dK, dV) the rows' statistics.
 size_t attn_lds(int dc, bool stats) {
-  return (size_t)4 * 64 * (dc <= 2 ? 128 : 256) + (stats ? 2 * 3 * attn::BROWS * 4 : 0);
+  return (size_t)4 * 64 * (dc <= 2 ? 128 : 256) + (stats ? 2 * 2 * attn::BROWS * 4 : 0);
 }
 
 lora4_status attn_forward(const lora4_attn *a, const uint16_t *Q, const uint16_t *K, const uint16_t *V, uint16_t *O,
@@ -146,10 +147,10 @@ lora4_status attn_backward(const lora4_attn *a, const uint16_t *Q, const uint16_
   if (pl.slots * a->Hkv > INT32_MAX || pl.kslots * a->Hkv * pl.ksplits > INT32_MAX) return LORA4_ERR_SHAPE;
   if (!ws || ws_bytes < pl.bytes) return LORA4_ERR_WORKSPACE;
   attn::Params p = attn_params(a, Q, K, V);
-  float *delta = ws_at<float>(ws, 0);
   p.lse = const_cast<float *>(lse);
   p.dO = dO;
-  p.delta = delta;
+  p.Oin = O;
+  p.stat = ws_at<float>(ws, 0);
   p.dQ = dQ;
   p.dK = dK;
   p.dV = dV;
@@ -158,9 +159,6 @@ lora4_status attn_backward(const lora4_attn *a, const uint16_t *Q, const uint16_
   p.lddv = lddv;
   p.part = ws_at<float>(ws, pl.off_part);
   if (a->Tq > 0) {
-    const int64_t rows = a->Tq * a->Hq;
-    TRY(launch_fn("attn_delta", attn::delta_kernel(), ceil_div(rows, 16), attn::THREADS, 0, st, O, dO, rows, (int)a->D,
-                  delta));
     p.slots = (int)pl.slots;
     TRY(launch_fn("attn_dq", attn::dq_kernel(pl.dc), pl.slots * a->Hkv, attn::THREADS, attn_lds(pl.dc, false), st, p));
   }

@@ -58,7 +58,9 @@ def forward(Q, K, V, scale, q_ranges, k_ranges):
 
 
 def backward(Q, K, V, O, dO, scale, q_ranges, k_ranges):
-    """{"dQ", "dK", "dV"}, with delta from the given O, and I_dQ, I_dK, I_dV: the
+    """{"dQ", "dK", "dV"}: delta = sum dO O of the given O for dQ, and for dK what it
+    stands for, the sum of P (dO V^T) over the keys (the two differ by O's
+    rounding, where the given O is rounded). I_dQ, I_dK, I_dV: the
     sums of absolute values that the roundings of dS and P enter; E_dQ, E_dK, E_dV:
     what fp32 arithmetic may cost (the weights' error, and that of dP and delta,
     sums of D exact products each, whose difference may cancel)."""
@@ -71,17 +73,21 @@ def backward(Q, K, V, O, dO, scale, q_ranges, k_ranges):
             g = h // (Hq // Hkv)
             q, k, do = Q[a:b, h], K[c:d, g], dO[a:b, h]
             P, lse = _weights(q, k, scale)
-            dS = P * (do @ V[c:d, g].T - (do * O[a:b, h]).sum(axis=1, keepdims=True)) * scale
+            dP = do @ V[c:d, g].T
+            dS = P * (dP - (do * O[a:b, h]).sum(axis=1, keepdims=True)) * scale
+            dSk = P * (dP - (P * dP).sum(axis=1, keepdims=True)) * scale
             r = weight_error(q, k, lse, scale)[:, None]
             terms = np.abs(do) @ np.abs(V[c:d, g]).T + np.abs(do * O[a:b, h]).sum(axis=1, keepdims=True)
             e = r * np.abs(dS) + P * terms * scale * Q.shape[2] * 2.0 ** -24 + TINY * (1 + scale * (1 + terms))
             o["E_dQ"][a:b, h] = e @ np.abs(k) + TINY
+            # (its delta: weights off by r each, which do not sum to 1 then, and n terms)
+            e = e + P * scale * ((r + (d - c) * 2.0 ** -24) * (P * terms).sum(axis=1, keepdims=True))
             o["E_dK"][c:d, g] += e.T @ np.abs(q) + TINY
             o["E_dV"][c:d, g] += (r * P + TINY).T @ np.abs(do) + TINY
             o["dQ"][a:b, h] = dS @ k
-            o["dK"][c:d, g] += dS.T @ q
+            o["dK"][c:d, g] += dSk.T @ q
             o["dV"][c:d, g] += P.T @ do
             o["I_dQ"][a:b, h] = np.abs(dS) @ np.abs(k)
-            o["I_dK"][c:d, g] += np.abs(dS).T @ np.abs(q)
+            o["I_dK"][c:d, g] += np.abs(dSk).T @ np.abs(q)
             o["I_dV"][c:d, g] += P.T @ np.abs(do)
     return o

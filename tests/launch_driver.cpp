@@ -100,7 +100,7 @@ void inspect(const std::string &name, void **args) {
     const lora4::loss::Params &p = checked<lora4::loss::Params>(name, args[0]);
     if (p.rows < 1 || p.splits < 1 || p.lde % lora4::loss::TILE) fail(context.c_str(), name.c_str());
   } else {   // (scalars only)
-    for (const char *k : {"k_attn_delta", "k_fill_u16", "k_reduce_bf16", "k_col_sum", "k_col_sum_slots", "k_quant_mxfp8"})
+    for (const char *k : {"k_fill_u16", "k_reduce_bf16", "k_col_sum", "k_col_sum_slots", "k_quant_mxfp8"})
       if (is(name, k)) return;
     fail("a kernel this driver does not know", name.c_str());
   }

@@ -124,6 +124,57 @@ __device__ __forceinline__ u32x4_t frag(const uint16_t *lds, int row0, int kk, i
   return lds_read_b128(lds + tile64_swz(row0 + (lane & 31), 2 * kk + (lane >> 5)));
 }
 
+// The main loop of both products. Operands of one 16-deep piece are read from LDS
+// while the products of the piece before run, and the step's one barrier stands
+// between its third and its last piece: there the next step's slabs have landed,
+// and everyone has read the last piece of this step's, so that the loads after
+// next go into its stage. No product waits at the barrier.
+//   issue(step, stage): the step's loads (8 instructions);
+//   read(stage, kk, frags): the operands of piece kk; mma(frags).
+template <int READS, typename Frags, typename Issue, typename Read, typename Mma>
+__device__ __forceinline__ void pipeline(int s0, int s1, Issue &&issue, Read &&read, Mma &&mma) {
+  if (s0 >= s1) return;
+  Frags f0, f1;
+  issue(s0, 0);
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+  __syncthreads();
+  if (s0 + 1 < s1) issue(s0 + 1, 1);
+  read(0, 0, f0);
+  auto hints = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // MFMA
+      __builtin_amdgcn_sched_group_barrier(0x100, (READS + 5) / 6, 0);   // LDS reads
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int stage = 0;
+#pragma unroll 1
+  for (int s = s0; s < s1; ++s, stage ^= 1) {
+    read(stage, 1, f1);
+    mma(f0);
+    hints();
+    read(stage, 2, f0);
+    mma(f1);
+    hints();
+    read(stage, 3, f1);
+    mma(f0);
+    hints();
+    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (s + 2 < s1) issue(s + 2, stage);
+    read(stage ^ 1, 0, f0);   // (past the last step: not used)
+    mma(f1);
+    hints();
+  }
+}
+
+struct Frags {
+  u32x4_t a[4], b[2];
+};
+
 // ---------------------------------------------------------------------------
 // The rows that count
 // ---------------------------------------------------------------------------
@@ -216,31 +267,27 @@ __global__ __launch_bounds__(THREADS, 2) void k_loss_logits(Params p) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
 
-  auto issue = [&](int s) {
-    uint16_t *dst = smem + (s & 1) * 2 * SLAB;
-    ld.issue(wr, dst, s * BKS, K, wave);
-    ld.issue(xr, dst + SLAB, s * BKS, K, wave);
+  auto mma = [&](const Frags &f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(f.a[i], f.b[j], acc[i][j]);
   };
-  const int steps = (K + BKS - 1) / BKS;
-  issue(0);
-  for (int s = 0; s < steps; ++s) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // this wave's loads of step s have landed
-    __syncthreads();                      // everyone's have, and step s - 1 is done with
-    if (s + 1 < steps) issue(s + 1);
-    const uint16_t *Ws = smem + (s & 1) * 2 * SLAB, *Xs = Ws + SLAB;
+  pipeline<6, Frags>(
+      0, (K + BKS - 1) / BKS,
+      [&](int s, int stage) __attribute__((always_inline)) {
+        uint16_t *dst = smem + stage * 2 * SLAB;
+        ld.issue(wr, dst, s * BKS, K, wave);
+        ld.issue(xr, dst + SLAB, s * BKS, K, wave);
+      },
+      [&](int stage, int kk, Frags &f) __attribute__((always_inline)) {
+        const uint16_t *Ws = smem + stage * 2 * SLAB, *Xs = Ws + SLAB;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      u32x4_t a[4], b[2];
+        for (int i = 0; i < 4; ++i) f.a[i] = frag(Ws, wv * 128 + i * 32, kk, lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = frag(Ws, wv * 128 + i * 32, kk, lane);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) b[j] = frag(Xs, wt * 64 + j * 32, kk, lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(a[i], b[j], acc[i][j]);
-    }
-  }
+        for (int j = 0; j < 2; ++j) f.b[j] = frag(Xs, wt * 64 + j * 32, kk, lane);
+      },
+      mma);
 
   // word of register r of block i: vw + 32 i + 8 (r / 4) + r % 4
   const int vw = wv * STRIP + 4 * h;
@@ -413,42 +460,38 @@ static __global__ __launch_bounds__(THREADS, 2) void k_loss_dx(Params p) {
   // block b = 8 i + wave: words 2 b, 2 b + 1
   const int wc = wpos ^ (((2 * wave + wrow) & 3) << 2);
   const bool wc_ok = c0 + wc * 8 < K;
-  auto issue = [&](int s) {
-    uint16_t *dst = smem + (s & 1) * 2 * SLAB;
-    const int64_t v = p.v0 + (int64_t)s * BKS;
-    const rsrc_t wr = big::make_rsrc(p.W + v * p.K, big::clamp_bytes(min((int64_t)BKS, p.v0 + p.cols - v) * p.K * 2));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int w = 2 * (8 * i + wave) + wrow;
-      load_lds16(wr, dst + (8 * i + wave) * 512, wc_ok ? (uint32_t)((w * K + c0 + wc * 8) * 2) : OOB, 0);
-    }
-    ld.issue(er, dst + SLAB, s * BKS, (int)p.lde, wave);
-  };
-
   f32x16_t acc[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
-  if (s0 < s1) issue(s0);
-  for (int s = s0; s < s1; ++s) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
-    if (s + 1 < s1) issue(s + 1);
-    const uint16_t *Ws = smem + (s & 1) * 2 * SLAB, *Es = Ws + SLAB;
+  auto mma = [&](const Frags &f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      u32x4_t a[4], b[2];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = frag_w(Ws, kk * 16, wk * 128 + i * 32, lane);
+      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(f.a[i], f.b[j], acc[i][j]);
+  };
+  pipeline<10, Frags>(
+      s0, s1,
+      [&](int s, int stage) __attribute__((always_inline)) {
+        uint16_t *dst = smem + stage * 2 * SLAB;
+        const int64_t v = p.v0 + (int64_t)s * BKS;
+        const rsrc_t wr = big::make_rsrc(p.W + v * p.K, big::clamp_bytes(min((int64_t)BKS, p.v0 + p.cols - v) * p.K * 2));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) b[j] = frag(Es, wt * 64 + j * 32, kk, lane);
+        for (int i = 0; i < 4; ++i) {
+          const int w = 2 * (8 * i + wave) + wrow;
+          load_lds16(wr, dst + (8 * i + wave) * 512, wc_ok ? (uint32_t)((w * K + c0 + wc * 8) * 2) : OOB, 0);
+        }
+        ld.issue(er, dst + SLAB, s * BKS, (int)p.lde, wave);
+      },
+      [&](int stage, int kk, Frags &f) __attribute__((always_inline)) {
+        const uint16_t *Ws = smem + stage * 2 * SLAB, *Es = Ws + SLAB;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) f.a[i] = frag_w(Ws, kk * 16, wk * 128 + i * 32, lane);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(a[i], b[j], acc[i][j]);
-    }
-  }
+        for (int j = 0; j < 2; ++j) f.b[j] = frag(Es, wt * 64 + j * 32, kk, lane);
+      },
+      mma);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int tl = tm * TILE + wt * 64 + j * 32 + (lane & 31);

@@ -66,12 +66,12 @@ struct Params {
   int64_t row0;             // first (of the rows that count)
   int rows;                 // rows of the chunk (a multiple of TILE)
   int64_t v0;               // first word
-  int64_t cols;             // words (the last piece ends with V)
+  int64_t cols, piece;      // words, and those of all pieces but the last
   uint16_t *E;              // [rows][lde]
   int64_t lde;              // a multiple of TILE
   float *strip_ref, *strip_sum;   // [strips][rows]
-  float *acc;               // [splits][rows][K]
-  int splits, split_steps;
+  float *acc;               // [splits][live rows, whole tiles][K]
+  int cus;                  // blocks that run side by side (one a CU)
   int first;                // first piece: acc is written, not added to
   int tiles_m, tiles_n;
   // outputs
@@ -210,10 +210,20 @@ static __global__ __launch_bounds__(1024) void k_loss_rows(Params p) {
 }
 
 // A wave to a row that counts: its X beside the others', and the logit of its
-// target (NaN for a target that is no word: the row's outputs become NaN).
+// target (NaN for a target that is no word: the row's outputs become NaN). And a
+// wave to a row that does not: loss, lse and dX of row i are zero.
 static __global__ __launch_bounds__(256) void k_loss_target(Params p) {
   const int lane = threadIdx.x & 63;
   const int at = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (at < p.M && p.target[at] == p.ignore) {
+    if (lane == 0) {
+      p.loss[at] = 0.0f;
+      if (p.lse) p.lse[at] = 0.0f;
+    }
+    if (p.dX)
+      for (int64_t k = lane * 8; k < p.K; k += 512)
+        *reinterpret_cast<u32x4_t *>(p.dX + (int64_t)at * p.K + k) = u32x4_t{0u, 0u, 0u, 0u};
+  }
   if (at >= *p.count) return;
   const int t = p.tgt[at];
   const uint16_t *x = p.X + (int64_t)p.row[at] * p.K;
@@ -299,16 +309,24 @@ __global__ __launch_bounds__(THREADS, 2) void k_loss_logits(Params p) {
     const bool ok = tl < live;
     const int64_t at = p.row0 + tl;
     const float ref = ok ? p.ref[at] : INFINITY;
-    const int64_t own = ok ? (int64_t)p.tgt[at] - v0 - vw : -1;   // register index of the target
+    // the target as a word of this lane's (its register), where it is one
+    const int64_t rel = ok ? (int64_t)p.tgt[at] - v0 - vw : -1;
+    const int own = rel >= 0 && rel < STRIP ? (int)rel : -1;
+    if (__ballot(own >= 0) || vend < TILE) {   // (few strips hold a target or the vocabulary's end)
+      asm volatile("");   // a branch, not selects in every tile
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int at_r = 32 * i + 8 * (r >> 2) + (r & 3);
+          if (at_r == own || vw + at_r >= vend) acc[i][j][r] = -INFINITY;
+        }
+    }
     float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int at_r = 32 * i + 8 * (r >> 2) + (r & 3);
-        if (at_r == own || vw + at_r >= vend) acc[i][j][r] = -INFINITY;
-        mx = fmaxf(mx, acc[i][j][r]);
-      }
+      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[i][j][r]);
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     const float rs = (mx - ref) * LOG2E > REF_SLACK ? mx : ref;
     float sum = 0.0f;
@@ -342,18 +360,37 @@ __global__ __launch_bounds__(THREADS, 2) void k_loss_logits(Params p) {
   }
 }
 
-// The strips of a piece into the rows' sums. 32 rows to a block, 32 threads to
-// a row. Where a strip had to take a reference of its own, the row gets the
+// Word ranges of the product acc += E W, from the rows that count (which the device alone
+// knows): as many as the CUs take in one round, of at least 8 steps each.
+struct Split {
+  int n, steps;      // ranges, 64-word steps of a range
+  int64_t stride;    // elements of acc between ranges
+};
+__device__ __forceinline__ Split split_of(const Params &p, int live, int64_t cols) {
+  const int tiles_m = (min(live, p.rows) + TILE - 1) / TILE;
+  const int tiles = max(1, tiles_m * (int)((p.K + TILE - 1) / TILE));
+  const int steps = (int)((cols + BKS - 1) / BKS);
+  Split s;
+  s.n = max(1, min(p.cus / tiles, steps / 8));
+  s.steps = (steps + s.n - 1) / s.n;
+  s.stride = (int64_t)tiles_m * TILE * p.K;
+  return s;
+}
+
+// The strips of a piece into the rows' sums. NR rows to a block, 1024 / NR threads
+// to a row (32 rows read whole lines; few rows have more threads each: 8 rows of
+// 1002 strips 31 us with 32 threads a row). Where a strip had to take a reference of its own, the row gets the
 // largest, and its E and acc are brought onto it (E is rounded a second time).
-template <bool GRAD>
+template <bool GRAD, int NR>
 __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
-  __shared__ float red[32][33], sums[32][33];
-  __shared__ float nref[32], fac[32];
-  __shared__ int moved[32];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;   // row, strip group
+  constexpr int NT = 1024 / NR;
+  __shared__ float red[NT][NR + 1], sums[NT][NR + 1];
+  __shared__ float nref[NR], fac[NR];
+  __shared__ int moved[NR];
+  const int tx = threadIdx.x % NR, ty = threadIdx.x / NR;   // row, strip group
   const int live = *p.count - (int)p.row0;
-  const int tl = blockIdx.x * 32 + tx;
-  if ((int)blockIdx.x * 32 >= live) return;
+  const int tl = blockIdx.x * NR + tx;
+  if ((int)blockIdx.x * NR >= live) return;
   const int strips = p.tiles_n * 2;
   const bool ok = tl < live;
   const int64_t at = p.row0 + tl;
@@ -361,47 +398,60 @@ __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
   float mx = ref;
   bool nan = ref != ref, other = false;
   if (ok)
-    for (int s = ty; s < strips; s += 32) {
-      const float r = p.strip_ref[(int64_t)s * p.rows + tl];
-      nan |= r != r;
-      other |= r != ref;
-      mx = fmaxf(mx, r);
+    for (int s0 = ty; s0 < strips; s0 += 4 * NT) {
+      float r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        r[u] = s0 + u * NT < strips ? p.strip_ref[(int64_t)(s0 + u * NT) * p.rows + tl] : ref;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        nan |= r[u] != r[u];
+        other |= r[u] != ref;
+        mx = fmaxf(mx, r[u]);
+      }
     }
   red[ty][tx] = nan ? __builtin_nanf("") : mx;
   if (ty == 0) moved[tx] = 0;
   __syncthreads();
   if (other) moved[tx] = 1;   // (every writer writes 1)
-  if (ty == 0) {
-    float m = red[0][tx];
-    for (int i = 1; i < 32; ++i) {
-      const float r = red[i][tx];
-      m = (m != m || r != r) ? __builtin_nanf("") : fmaxf(m, r);
+  for (int n = NT / 2; n > 0; n /= 2) {
+    if (ty < n) {
+      const float a = red[ty][tx], b = red[ty + n][tx];
+      red[ty][tx] = (a != a || b != b) ? __builtin_nanf("") : fmaxf(a, b);
     }
-    nref[tx] = m;
+    __syncthreads();
   }
-  __syncthreads();
-  const float m = nref[tx];
+  const float m = red[0][tx];
+  if (ty == 0) nref[tx] = m;
   float sum = 0.0f;
   if (ok)
-    for (int s = ty; s < strips; s += 32) {
-      const float r = p.strip_ref[(int64_t)s * p.rows + tl];
-      const float v = p.strip_sum[(int64_t)s * p.rows + tl];
-      sum += r == m ? v : v * exp2_hw((r - m) * LOG2E);
+    for (int s0 = ty; s0 < strips; s0 += 4 * NT) {
+      float r[4], v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = (int64_t)(s0 + u * NT) * p.rows + tl;
+        r[u] = s0 + u * NT < strips ? p.strip_ref[i] : m;
+        v[u] = s0 + u * NT < strips ? p.strip_sum[i] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum += r[u] == m ? v[u] : v[u] * exp2_hw((r[u] - m) * LOG2E);
     }
   sums[ty][tx] = sum;
   __syncthreads();
+  for (int n = NT / 2; n > 0; n /= 2) {
+    if (ty < n) sums[ty][tx] += sums[ty + n][tx];
+    __syncthreads();
+  }
   if (ty == 0 && ok) {
-    float t = 0.0f;
-    for (int i = 0; i < 32; ++i) t += sums[i][tx];
     const float f = ref == m ? 1.0f : exp2_hw((ref - m) * LOG2E);
-    p.S[at] = p.S[at] * f + t;
+    p.S[at] = p.S[at] * f + sums[0][tx];
     p.ref[at] = m;
     fac[tx] = f;
   }
   if constexpr (GRAD) {
     __syncthreads();
-    for (int r = 0; r < 32; ++r) {
-      const int row = blockIdx.x * 32 + r;
+    for (int r = 0; r < NR; ++r) {
+      const int row = blockIdx.x * NR + r;
       if (row >= live || !moved[r]) continue;   // uniform
       for (int64_t c = threadIdx.x; c < strips * STRIP; c += 1024) {
         const float sr = p.strip_ref[(c / STRIP) * p.rows + row];
@@ -409,12 +459,11 @@ __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
         uint16_t *e = p.E + (int64_t)row * p.lde + c;
         *e = to_bf16(bf16_bits_to_f32(*e) * exp2_hw((sr - nref[r]) * LOG2E));
       }
-      if (!p.first && fac[r] != 1.0f)
-        for (int s = 0; s < p.splits; ++s)
-          for (int64_t k = threadIdx.x; k < p.K; k += 1024) {
-            float *a = p.acc + ((int64_t)s * p.rows + row) * p.K + k;
-            *a *= fac[r];
-          }
+      if (!p.first && fac[r] != 1.0f) {
+        const Split sp = split_of(p, live, p.piece);
+        for (int s = 0; s < sp.n; ++s)
+          for (int64_t k = threadIdx.x; k < p.K; k += 1024) p.acc[s * sp.stride + (int64_t)row * p.K + k] *= fac[r];
+      }
     }
   }
 }
@@ -439,18 +488,20 @@ __device__ __forceinline__ u32x4_t frag_w(const uint16_t *lds, int v0, int col0,
 
 static __global__ __launch_bounds__(THREADS, 2) void k_loss_dx(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
-  // blocks: split fastest within an XCD's tiles
-  const int split = blockIdx.x / (((p.tiles_m * p.tiles_n + 7) / 8) * 8);
+  const int live = min(*p.count - (int)p.row0, p.rows);
+  if (live <= 0) return;
+  // the piece's ranges, in the first piece's number (the last one may be shorter)
+  const Split sp = split_of(p, live, p.piece);
+  const int tiles_m = (live + TILE - 1) / TILE, per = (tiles_m * p.tiles_n + 7) / 8 * 8;
+  const int split = blockIdx.x / per;
   int tm, tn;
-  if (!map_tile(blockIdx.x % (((p.tiles_m * p.tiles_n + 7) / 8) * 8), p.tiles_m, p.tiles_n, tm, tn)) return;
-  const int live = *p.count - (int)p.row0;
-  if (tm * TILE >= live) return;
+  if (split >= sp.n || !map_tile(blockIdx.x % per, tiles_m, p.tiles_n, tm, tn)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wk = wave & 1, wt = wave >> 1, h = lane >> 5;
   const int c0 = tn * TILE;                 // first hidden column
   const int K = (int)p.K;
   const int R = (int)p.cols;
-  const int s0 = split * p.split_steps, s1 = min((R + BKS - 1) / BKS, s0 + p.split_steps);
+  const int s0 = split * sp.steps, s1 = min((R + BKS - 1) / BKS, s0 + sp.steps);
 
   // E: rows of the chunk (lde covers whole tiles, zero past the last word)
   const rsrc_t er = big::make_rsrc(p.E + (int64_t)tm * TILE * p.lde, big::clamp_bytes((int64_t)TILE * p.lde * 2));
@@ -496,7 +547,7 @@ static __global__ __launch_bounds__(THREADS, 2) void k_loss_dx(Params p) {
   for (int j = 0; j < 2; ++j) {
     const int tl = tm * TILE + wt * 64 + j * 32 + (lane & 31);
     if (tl >= live) continue;
-    float *dst = p.acc + ((int64_t)split * p.rows + tl) * p.K + c0 + wk * 128 + 4 * h;
+    float *dst = p.acc + split * sp.stride + (int64_t)tl * p.K + c0 + wk * 128 + 4 * h;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -513,21 +564,6 @@ static __global__ __launch_bounds__(THREADS, 2) void k_loss_dx(Params p) {
 // ---------------------------------------------------------------------------
 // Outputs
 // ---------------------------------------------------------------------------
-
-// Rows without a target: loss 0, lse 0, dX 0. (Before k_loss_finish; a wave to
-// a row.)
-static __global__ __launch_bounds__(256) void k_loss_ignored(Params p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (i >= p.M || p.target[i] != p.ignore) return;
-  if (lane == 0) {
-    p.loss[i] = 0.0f;
-    if (p.lse) p.lse[i] = 0.0f;
-  }
-  if (p.dX)
-    for (int64_t k = lane * 8; k < p.K; k += 512)
-      *reinterpret_cast<u32x4_t *>(p.dX + i * p.K + k) = u32x4_t{0u, 0u, 0u, 0u};
-}
 
 __device__ __forceinline__ float row_weight(const Params &p, int row, int count) {
   return p.weight ? p.weight[row] : 1.0f / (float)count;
@@ -555,10 +591,11 @@ static __global__ __launch_bounds__(256) void k_loss_finish(Params p) {
   const float a = w / sum, b = a * S;
   const uint16_t *wt = p.W + (int64_t)max(p.tgt[at], 0) * p.K;
   const float *src = p.acc + (int64_t)tl * p.K;
+  const Split sp = split_of(p, (int)min((int64_t)p.rows, count - p.row0), p.piece);
   for (int64_t k = lane * 8; k < p.K; k += 512) {
     f32x4_t lo = *reinterpret_cast<const f32x4_t *>(src + k), hi = *reinterpret_cast<const f32x4_t *>(src + k + 4);
-    for (int s = 1; s < p.splits; ++s) {
-      const float *q = src + (int64_t)s * p.rows * p.K + k;
+    for (int s = 1; s < sp.n; ++s) {
+      const float *q = src + s * sp.stride + k;
       lo += *reinterpret_cast<const f32x4_t *>(q);
       hi += *reinterpret_cast<const f32x4_t *>(q + 4);
     }
@@ -600,9 +637,8 @@ static __global__ __launch_bounds__(1024) void k_loss_total(Params p) {
 const void *rows_kernel();
 const void *target_kernel();
 const void *logits_kernel(bool grad);
-const void *join_kernel(bool grad);
+const void *join_kernel(bool grad, int rows);
 const void *dx_kernel();
-const void *ignored_kernel();
 const void *finish_kernel();
 const void *total_kernel();
 

@@ -4,7 +4,7 @@
 //   k_loss_rows -> k_loss_target -> per chunk of rows:
 //       per piece of the vocabulary: k_loss_logits -> k_loss_join [-> k_loss_dx]
 //       k_loss_finish
-//   -> k_loss_ignored, k_loss_total
+//   -> k_loss_total
 //
 // How many rows count is known on the device alone: the grids cover all M, and
 // blocks past the last row that counts end at once.
@@ -21,7 +21,6 @@ constexpr int64_t LOSS_E_BYTES = int64_t(256) << 20;
 struct LossPlan {
   int64_t chunk;       // rows of a chunk, a multiple of TILE
   int64_t piece;       // words of a piece, a multiple of TILE
-  int splits;          // word ranges of acc's product
   size_t off_row, off_tgt, off_xc, off_lt, off_ref, off_s, off_sref, off_ssum, off_e, off_acc, bytes;
 };
 
@@ -48,11 +47,6 @@ LossPlan loss_plan(bool grad, int64_t M, int64_t K, int64_t V) {
   int64_t piece = std::min(tiles_v, loss_piece_policy());
   if (grad) {
     piece = std::max<int64_t>(1, std::min(piece, LOSS_E_BYTES / (pl.chunk * 2 * T)));
-    const int64_t tiles_k = ceil_div(K, T) * (pl.chunk / T), cus = cu_count();
-    // a tile a CU; at least 8 steps each
-    pl.splits = (int)std::max<int64_t>(1, std::min(cus / std::max<int64_t>(1, tiles_k), piece * (T / loss::BKS) / 8));
-  } else {
-    pl.splits = 1;
   }
   pl.piece = piece * T;
   size_t off = 256;   // the count
@@ -72,7 +66,8 @@ LossPlan loss_plan(bool grad, int64_t M, int64_t K, int64_t V) {
   pl.off_ssum = take(strips);
   if (grad) {
     pl.off_e = take((size_t)pl.chunk * pl.piece * 2);
-    pl.off_acc = take((size_t)pl.splits * pl.chunk * K * 4);
+    // the chunk's rows once, or as many ranges of fewer as fill the CUs (split_of)
+    pl.off_acc = take((size_t)std::max(pl.chunk, cu_count() / ceil_div(K, T) * T) * K * 4);
   }
   pl.bytes = off;
   return pl;
@@ -109,7 +104,8 @@ lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targ
   p.strip_ref = ws_at<float>(ws, pl.off_sref);
   p.strip_sum = ws_at<float>(ws, pl.off_ssum);
   p.acc = ws_at<float>(ws, pl.off_acc);
-  p.splits = pl.splits;
+  p.piece = pl.piece;
+  p.cus = cu_count();
   p.loss = out_loss;
   p.lse = lse;
   p.total = total;
@@ -128,16 +124,18 @@ lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targ
       p.tiles_n = (int)ceil_div(p.cols, T);
       TRY(launch_fn("loss_logits", loss::logits_kernel(grad), ceil_div((int64_t)p.tiles_m * p.tiles_n, 8) * 8,
                     loss::THREADS, loss::LDS_BYTES, st, p));
-      TRY(launch_fn("loss_join", loss::join_kernel(grad), ceil_div(rows, 32), 1024, 0, st, p));
+      const int nr = rows <= 256 ? 4 : 32;
+      TRY(launch_fn("loss_join", loss::join_kernel(grad, nr), ceil_div(rows, nr), 1024, 0, st, p));
       if (!grad) continue;
       p.tiles_n = (int)ceil_div(K, T);
-      p.split_steps = (int)ceil_div(ceil_div(p.cols, loss::BKS), pl.splits);
-      TRY(launch_fn("loss_dx", loss::dx_kernel(), ceil_div((int64_t)p.tiles_m * p.tiles_n, 8) * 8 * pl.splits,
+      // all tiles once, or ranges of fewer, up to a block a CU (split_of), the tiles
+      // of each range rounded up to the 8 XCDs
+      const int64_t tiles = ceil_div((int64_t)p.tiles_m * p.tiles_n, 8) * 8;
+      TRY(launch_fn("loss_dx", loss::dx_kernel(), std::max(tiles, p.cus + 7 * ceil_div(p.cus, p.tiles_n)),
                     loss::THREADS, loss::LDS_BYTES, st, p));
     }
     TRY(launch_fn("loss_finish", loss::finish_kernel(), ceil_div(rows, 4), 256, 0, st, p));
   }
-  if (M > 0) TRY(launch_fn("loss_ignored", loss::ignored_kernel(), ceil_div(M, 4), 256, 0, st, p));
   return total ? launch_fn("loss_total", loss::total_kernel(), 1, 1024, 0, st, p) : LORA4_OK;
 }
 

@@ -19,15 +19,21 @@ namespace {
 // ---------------------------------------------------------------------------
 
 template <typename... Args>
+lora4_status launch_grid(const char *name, const void *fn, dim3 grid, int threads, size_t lds, hipStream_t st,
+                         Args... args) {
+  if (lds > 64 * 1024) TRY(set_lds_limit(fn, lds));
+  void *argv[] = {(void *)&args...};
+  return launch_timed(name, st, [&] {
+    (void)hipLaunchKernel(fn, grid, dim3((unsigned)threads), argv, lds, st);
+  });
+}
+
+template <typename... Args>
 lora4_status launch_fn(const char *name, const void *fn, int64_t blocks, int threads, size_t lds, hipStream_t st,
                        Args... args) {
   if (blocks <= 0) return LORA4_OK;
   if (blocks > INT32_MAX) return LORA4_ERR_SHAPE;
-  if (lds > 64 * 1024) TRY(set_lds_limit(fn, lds));
-  void *argv[] = {(void *)&args...};
-  return launch_timed(name, st, [&] {
-    (void)hipLaunchKernel(fn, dim3((unsigned)blocks), dim3((unsigned)threads), argv, lds, st);
-  });
+  return launch_grid(name, fn, dim3((unsigned)blocks), threads, lds, st, args...);
 }
 
 bool all_aligned16(std::initializer_list<const void *> ps) {

@@ -22,8 +22,10 @@
 // Rows without a target (prompts, padding) are left out before the products:
 // the rows that count are copied together once (k_loss_rows).
 //
-// Both products run 256 x 256 tiles of eight waves on v_mfma_f32_32x32x16_bf16,
-// operands by direct loads into two LDS stages of 64-deep slabs. The vocabulary
+// Both products run on v_mfma_f32_32x32x16_bf16, operands by direct loads into LDS
+// stages of 64-deep slabs: tiles of 256 x 256 by eight waves with two stages, or,
+// for few tokens or few words, 64 tokens x 128 by four waves with three stages,
+// two blocks to a CU. The vocabulary
 // (the hidden columns) is the first operand, so that a lane's results belong to
 // one token: its row's maximum and sum are lane-local but for one exchange, and
 // its stores are contiguous.
@@ -38,12 +40,24 @@ namespace loss {
 using big::OOB;
 using big::rsrc_t;
 
-constexpr int THREADS = 512;
-constexpr int TILE = 256;            // tokens, and vocabulary or hidden columns, of a tile
 constexpr int BKS = 64;              // reduction step
-constexpr int STRIP = 128;           // vocabulary of a wave: one maximum and sum per row
-constexpr int SLAB = TILE * BKS;     // elements of one operand's stage
-constexpr size_t LDS_BYTES = 4 * SLAB * 2;
+
+// A tile: WV x WT waves, each of AV x 2 blocks of 32 x 32; the first operand is the
+// words (hidden columns), the second the tokens.
+template <int WV_, int WT_, int AV_, int STAGES_>
+struct Shape {
+  static constexpr int WV = WV_, WT = WT_, AV = AV_, STAGES = STAGES_;
+  static constexpr int NW = WV * WT, THREADS = 64 * NW;
+  static constexpr int VT = 32 * AV * WV, TT = 64 * WT;   // words, tokens
+  static constexpr int STRIP = 32 * AV;                   // words of a wave: one maximum and sum per row
+  static constexpr int SLAB_V = VT * BKS, SLAB_T = TT * BKS, STAGE = SLAB_V + SLAB_T;   // elements
+  static constexpr size_t LDS_BYTES = (size_t)STAGES * STAGE * 2;
+  static constexpr int PER_CU = NW == 8 ? 1 : 2;
+};
+using Big = Shape<2, 4, 4, 2>;
+using Small = Shape<4, 1, 1, 3>;
+constexpr int TILE = 256;            // pieces of the vocabulary are multiples of it
+
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float REF_SLACK = 64.0f;   // binary orders a logit may lie above its row's reference
 
@@ -64,14 +78,16 @@ struct Params {
   float *S;                 // [M] sum over the other words
   // a chunk of them and a piece of the vocabulary
   int64_t row0;             // first (of the rows that count)
-  int rows;                 // rows of the chunk (a multiple of TILE)
+  int rows;                 // rows of the chunk (a multiple of the tiles')
   int64_t v0;               // first word
   int64_t cols, piece;      // words, and those of all pieces but the last
   uint16_t *E;              // [rows][lde]
   int64_t lde;              // a multiple of TILE
+  int strip, strips;        // words of a strip, strips of the piece's tiles
   float *strip_ref, *strip_sum;   // [strips][rows]
   float *acc;               // [splits][live rows, whole tiles][K]
-  int cus;                  // blocks that run side by side (one a CU)
+  int dt, dv;               // tokens and hidden columns of acc's tiles
+  int side;                 // blocks of acc's product that run side by side
   int first;                // first piece: acc is written, not added to
   int tiles_m, tiles_n;
   // outputs
@@ -85,37 +101,41 @@ __device__ __forceinline__ void load_lds16(const rsrc_t &r, uint16_t *dst, uint3
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
 }
 
-// Tile t of the grid: consecutive blocks go to consecutive XCDs, each of which
-// takes a contiguous range of the tiles in grouped order (runs of RUN row tiles
-// walked column by column), so that its blocks share both operands in its L2.
-constexpr int RUN = 8;
-__device__ __forceinline__ bool map_tile(int id, int tiles_m, int tiles_n, int &tm, int &tn) {
-  const int n = tiles_m * tiles_n, per = (n + 7) / 8;
+// Item of the grid: consecutive blocks go to consecutive XCDs, each of which takes
+// a contiguous range of the n items, so that its blocks share operands in its L2.
+__device__ __forceinline__ int xcd_item(int id, int n) {
+  const int per = (n + 7) / 8;
   const int t = (id & 7) * per + (id >> 3);
-  if ((id >> 3) >= per || t >= n) return false;
+  return (id >> 3) < per && t < n ? t : -1;
+}
+
+// Tile t in grouped order: runs of RUN row tiles walked column by column.
+constexpr int RUN = 8;
+__device__ __forceinline__ void grouped(int t, int tiles_m, int tiles_n, int &tm, int &tn) {
   const int g = t / (RUN * tiles_n), r = t - g * RUN * tiles_n;
   const int rows = min(RUN, tiles_m - g * RUN);
   tn = r / rows;
   tm = g * RUN + (r - tn * rows);
-  return true;
 }
 
-// A 256 x 64 slab (rows of ld elements, the reduction contiguous) into the
-// tile64 layout. The 32 1-KB blocks go to the 8 waves in turn.
+// A ROWS x 64 slab (rows of ld elements, the reduction contiguous) into the
+// tile64 layout. The 1-KB blocks (8 rows) go to the NW waves in turn.
+template <int ROWS, int NW>
 struct SlabLoad {
-  uint32_t voff[4];
-  int chunk;        // logical 16-byte chunk this lane fetches (the same in all blocks)
+  static constexpr int N = ROWS / 8 / NW;   // loads of a wave
+  uint32_t voff[N];
+  int chunk;        // logical 16-byte chunk this lane fetches (the same in all blocks: NW is even)
   __device__ __forceinline__ SlabLoad(int64_t ld, int wave, int lane) {
     const int rl = lane >> 3;
-    // block b = 8 i + wave: rows 8 b .. 8 b + 7
+    // block b = NW i + wave: rows 8 b .. 8 b + 7
     chunk = (lane & 7) ^ ((((wave & 1) << 2) | (rl >> 1)) & 7);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) voff[i] = (uint32_t)((((8 * i + wave) * 8 + rl) * ld + chunk * 8) * 2);
+    for (int i = 0; i < N; ++i) voff[i] = (uint32_t)((((NW * i + wave) * 8 + rl) * ld + chunk * 8) * 2);
   }
   __device__ __forceinline__ void issue(const rsrc_t &r, uint16_t *lds, int k0, int R, int wave) const {
     const bool edge = k0 + chunk * 8 >= R;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_lds16(r, lds + (8 * i + wave) * 512, edge ? OOB : voff[i], k0 * 2);
+    for (int i = 0; i < N; ++i) load_lds16(r, lds + (NW * i + wave) * 512, edge ? OOB : voff[i], k0 * 2);
   }
 };
 
@@ -129,29 +149,36 @@ __device__ __forceinline__ u32x4_t frag(const uint16_t *lds, int row0, int kk, i
 // between its third and its last piece: there the next step's slabs have landed,
 // and everyone has read the last piece of this step's, so that the loads after
 // next go into its stage. No product waits at the barrier.
-//   issue(step, stage): the step's loads (8 instructions);
-//   read(stage, kk, frags): the operands of piece kk; mma(frags).
-template <int READS, typename Frags, typename Issue, typename Read, typename Mma>
+//   issue(step, stage): the step's loads, LOADS instructions of every wave (also
+//     past the last step, where nothing is in range, so that the loads in flight
+//     at each wait are a constant); read(stage, kk, frags): the operands of piece
+//     kk; mma(frags).
+constexpr int wait_imm(int vm, int lgkm) { return (vm & 15) | (7 << 4) | (lgkm << 8) | ((vm >> 4) << 14); }
+
+template <int STAGES, int LOADS, int MFMAS, int READS, typename Frags, typename Issue, typename Read, typename Mma>
 __device__ __forceinline__ void pipeline(int s0, int s1, Issue &&issue, Read &&read, Mma &&mma) {
   if (s0 >= s1) return;
   Frags f0, f1;
-  issue(s0, 0);
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-  __syncthreads();
-  if (s0 + 1 < s1) issue(s0 + 1, 1);
-  read(0, 0, f0);
-  auto hints = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // MFMA
-      __builtin_amdgcn_sched_group_barrier(0x100, (READS + 5) / 6, 0);   // LDS reads
+  for (int i = 0; i < STAGES; ++i) issue(s0 + i, i);
+  __builtin_amdgcn_s_waitcnt(wait_imm((STAGES - 1) * LOADS, 15));
+  __syncthreads();
+  read(0, 0, f0);
+  // MFMAs with the next piece's reads spread over them
+  auto hints = [&]() __attribute__((always_inline)) {
+    constexpr int GROUPS = MFMAS > 2 ? MFMAS - 2 : 1;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                         // MFMA
+      __builtin_amdgcn_sched_group_barrier(0x100, (READS + GROUPS - 1) / GROUPS, 0);   // LDS reads
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, MFMAS - GROUPS, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
   int stage = 0;
 #pragma unroll 1
-  for (int s = s0; s < s1; ++s, stage ^= 1) {
+  for (int s = s0; s < s1; ++s) {
+    const int next = stage + 1 == STAGES ? 0 : stage + 1;
     read(stage, 1, f1);
     mma(f0);
     hints();
@@ -161,18 +188,21 @@ __device__ __forceinline__ void pipeline(int s0, int s1, Issue &&issue, Read &&r
     read(stage, 3, f1);
     mma(f0);
     hints();
-    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(wait_imm((STAGES - 2) * LOADS, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    if (s + 2 < s1) issue(s + 2, stage);
-    read(stage ^ 1, 0, f0);   // (past the last step: not used)
+    issue(s + STAGES, stage);
+    read(next, 0, f0);   // (past the last step: not used)
     mma(f1);
     hints();
+    stage = next;
   }
+  __builtin_amdgcn_s_waitcnt(wait_imm(0, 15));   // (no load into LDS outlives the block)
 }
 
+template <int AV>
 struct Frags {
-  u32x4_t a[4], b[2];
+  u32x4_t a[AV], b[2];
 };
 
 // ---------------------------------------------------------------------------
@@ -253,69 +283,72 @@ static __global__ __launch_bounds__(256) void k_loss_target(Params p) {
 // Logits of a piece: strip maxima and sums, and E
 // ---------------------------------------------------------------------------
 
-// The tile's results: wave (wv, wt) holds words 128 wv .. + 127 (4 blocks) of
+// The tile's results: wave (wv, wt) holds the words of a strip, AV blocks, of
 // tokens 64 wt .. + 63 (2 blocks).
-template <bool GRAD>
-__global__ __launch_bounds__(THREADS, 2) void k_loss_logits(Params p) {
+template <bool GRAD, typename T>
+__global__ __launch_bounds__(T::THREADS, 2) void k_loss_logits(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  const int item = xcd_item(blockIdx.x, p.tiles_m * p.tiles_n);
+  if (item < 0) return;
   int tm, tn;
-  if (!map_tile(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn)) return;
-  const int live = *p.count - (int)p.row0;   // rows of this chunk that count
-  if (tm * TILE >= live) return;
+  grouped(item, p.tiles_m, p.tiles_n, tm, tn);
+  const int live = min(*p.count - (int)p.row0, p.rows);   // rows of this chunk that count
+  if (tm * T::TT >= live) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int wv = wave & 1, wt = wave >> 1, h = lane >> 5;
-  const int64_t v0 = p.v0 + (int64_t)tn * TILE;   // first word of the tile
-  const int64_t t0 = p.row0 + (int64_t)tm * TILE;
+  const int wv = wave % T::WV, wt = wave / T::WV, h = lane >> 5;
+  const int64_t v0 = p.v0 + (int64_t)tn * T::VT;   // first word of the tile
+  const int64_t t0 = p.row0 + (int64_t)tm * T::TT;
   const int K = (int)p.K;
-  const rsrc_t wr = big::make_rsrc(p.W + v0 * p.K, big::clamp_bytes(min((int64_t)TILE, p.V - v0) * p.K * 2));
-  const rsrc_t xr = big::make_rsrc(p.Xc + t0 * p.K, big::clamp_bytes((int64_t)min(TILE, live - tm * TILE) * p.K * 2));
-  const SlabLoad ld(p.K, wave, lane);
+  const rsrc_t wr = big::make_rsrc(p.W + v0 * p.K, big::clamp_bytes(min((int64_t)T::VT, p.V - v0) * p.K * 2));
+  const rsrc_t xr = big::make_rsrc(p.Xc + t0 * p.K, big::clamp_bytes((int64_t)min(T::TT, live - tm * T::TT) * p.K * 2));
+  const SlabLoad<T::VT, T::NW> lw(p.K, wave, lane);
+  const SlabLoad<T::TT, T::NW> lx(p.K, wave, lane);
 
-  f32x16_t acc[4][2];
+  f32x16_t acc[T::AV][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < T::AV; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
 
-  auto mma = [&](const Frags &f) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(f.a[i], f.b[j], acc[i][j]);
-  };
-  pipeline<6, Frags>(
+  using F = Frags<T::AV>;
+  pipeline<T::STAGES, lw.N + lx.N, 2 * T::AV, T::AV + 2, F>(
       0, (K + BKS - 1) / BKS,
       [&](int s, int stage) __attribute__((always_inline)) {
-        uint16_t *dst = smem + stage * 2 * SLAB;
-        ld.issue(wr, dst, s * BKS, K, wave);
-        ld.issue(xr, dst + SLAB, s * BKS, K, wave);
+        uint16_t *dst = smem + stage * T::STAGE;
+        lw.issue(wr, dst, s * BKS, K, wave);
+        lx.issue(xr, dst + T::SLAB_V, s * BKS, K, wave);
       },
-      [&](int stage, int kk, Frags &f) __attribute__((always_inline)) {
-        const uint16_t *Ws = smem + stage * 2 * SLAB, *Xs = Ws + SLAB;
+      [&](int stage, int kk, F &f) __attribute__((always_inline)) {
+        const uint16_t *Ws = smem + stage * T::STAGE, *Xs = Ws + T::SLAB_V;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f.a[i] = frag(Ws, wv * 128 + i * 32, kk, lane);
+        for (int i = 0; i < T::AV; ++i) f.a[i] = frag(Ws, wv * T::STRIP + i * 32, kk, lane);
 #pragma unroll
         for (int j = 0; j < 2; ++j) f.b[j] = frag(Xs, wt * 64 + j * 32, kk, lane);
       },
-      mma);
+      [&](const F &f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < T::AV; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(f.a[i], f.b[j], acc[i][j]);
+      });
 
   // word of register r of block i: vw + 32 i + 8 (r / 4) + r % 4
-  const int vw = wv * STRIP + 4 * h;
-  const int strip = tn * 2 + wv;
-  const int vend = (int)min((int64_t)TILE, p.V - v0);   // words of the tile that exist
+  const int vw = wv * T::STRIP + 4 * h;
+  const int strip = tn * T::WV + wv;
+  const int vend = (int)min((int64_t)T::VT, p.V - v0);   // words of the tile that exist
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int tl = tm * TILE + wt * 64 + j * 32 + (lane & 31);   // row of the chunk
+    const int tl = tm * T::TT + wt * 64 + j * 32 + (lane & 31);   // row of the chunk
     const bool ok = tl < live;
     const int64_t at = p.row0 + tl;
     const float ref = ok ? p.ref[at] : INFINITY;
     // the target as a word of this lane's (its register), where it is one
     const int64_t rel = ok ? (int64_t)p.tgt[at] - v0 - vw : -1;
-    const int own = rel >= 0 && rel < STRIP ? (int)rel : -1;
-    if (__ballot(own >= 0) || vend < TILE) {   // (few strips hold a target or the vocabulary's end)
+    const int own = rel >= 0 && rel < T::STRIP ? (int)rel : -1;
+    if (__ballot(own >= 0) || vend < T::VT) {   // (few strips hold a target or the vocabulary's end)
       asm volatile("");   // a branch, not selects in every tile
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < T::AV; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int at_r = 32 * i + 8 * (r >> 2) + (r & 3);
@@ -324,7 +357,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_loss_logits(Params p) {
     }
     float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < T::AV; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[i][j][r]);
     mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -332,7 +365,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_loss_logits(Params p) {
     float sum = 0.0f;
     const float rl = rs * LOG2E;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < T::AV; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const float e = exp2_hw(__builtin_fmaf(acc[i][j][r], LOG2E, -rl));
@@ -343,9 +376,10 @@ __global__ __launch_bounds__(THREADS, 2) void k_loss_logits(Params p) {
     if (h == 0) p.strip_ref[(int64_t)strip * p.rows + tl] = rs;
     else p.strip_sum[(int64_t)strip * p.rows + tl] = sum;
     if constexpr (GRAD) {
-      uint16_t *dst = p.E + (int64_t)tl * p.lde + tn * TILE + wv * STRIP;
+      if (!ok) continue;   // (both halves of a row)
+      uint16_t *dst = p.E + (int64_t)tl * p.lde + tn * T::VT + wv * T::STRIP;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < T::AV; ++i)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           // the lane halves trade, so that each holds 8 words in a row
@@ -361,19 +395,19 @@ __global__ __launch_bounds__(THREADS, 2) void k_loss_logits(Params p) {
 }
 
 // Word ranges of the product acc += E W, from the rows that count (which the device alone
-// knows): as many as the CUs take in one round, of at least 8 steps each.
+// knows): as many as the chip takes in one round, of at least 8 steps each.
 struct Split {
   int n, steps;      // ranges, 64-word steps of a range
   int64_t stride;    // elements of acc between ranges
 };
 __device__ __forceinline__ Split split_of(const Params &p, int live, int64_t cols) {
-  const int tiles_m = (min(live, p.rows) + TILE - 1) / TILE;
-  const int tiles = max(1, tiles_m * (int)((p.K + TILE - 1) / TILE));
+  const int tiles_m = (min(live, p.rows) + p.dt - 1) / p.dt;
+  const int tiles = max(1, tiles_m * (int)((p.K + p.dv - 1) / p.dv));
   const int steps = (int)((cols + BKS - 1) / BKS);
   Split s;
-  s.n = max(1, min(p.cus / tiles, steps / 8));
+  s.n = max(1, min(p.side / tiles, steps / 8));
   s.steps = (steps + s.n - 1) / s.n;
-  s.stride = (int64_t)tiles_m * TILE * p.K;
+  s.stride = (int64_t)tiles_m * p.dt * p.K;
   return s;
 }
 
@@ -391,7 +425,7 @@ __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
   const int live = *p.count - (int)p.row0;
   const int tl = blockIdx.x * NR + tx;
   if ((int)blockIdx.x * NR >= live) return;
-  const int strips = p.tiles_n * 2;
+  const int strips = p.strips;
   const bool ok = tl < live;
   const int64_t at = p.row0 + tl;
   const float ref = ok ? p.ref[at] : 0.0f;
@@ -453,8 +487,8 @@ __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
     for (int r = 0; r < NR; ++r) {
       const int row = blockIdx.x * NR + r;
       if (row >= live || !moved[r]) continue;   // uniform
-      for (int64_t c = threadIdx.x; c < strips * STRIP; c += 1024) {
-        const float sr = p.strip_ref[(c / STRIP) * p.rows + row];
+      for (int64_t c = threadIdx.x; c < (int64_t)strips * p.strip; c += 1024) {
+        const float sr = p.strip_ref[(c / p.strip) * p.rows + row];
         if (sr == nref[r]) continue;
         uint16_t *e = p.E + (int64_t)row * p.lde + c;
         *e = to_bf16(bf16_bits_to_f32(*e) * exp2_hw((sr - nref[r]) * LOG2E));
@@ -472,87 +506,100 @@ __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
 // acc += E W_piece
 // ---------------------------------------------------------------------------
 
-// W slab: 64 words x 256 hidden columns (rows of 512 bytes, 16-byte chunk c of
-// row v at c ^ ((v & 3) << 2): the transposing read takes four rows of 64 bytes
+// W slab: 64 words x VT hidden columns (rows of 512 or 256 bytes, 16-byte chunk c
+// of row v at c ^ ((v & 3) << 2): the transposing read takes four rows of 64 bytes
 // at a time, which land in the four quarters of the banks).
-__device__ __forceinline__ int wat(int v, int c) { return v * TILE + ((c ^ ((v & 3) << 2)) << 3); }
+template <int VT>
+__device__ __forceinline__ int wat(int v, int c) {
+  return v * VT + ((c ^ ((v & 3) << 2)) << 3);
+}
 
+template <int VT>
 __device__ __forceinline__ u32x4_t frag_w(const uint16_t *lds, int v0, int col0, int lane) {
   const int h = lane >> 5, i = lane & 15;
   const int col = col0 + ((lane >> 4) & 1) * 16 + (i & 3) * 4;
   const int v = v0 + 8 * h + (i >> 2);
-  const u32x2_t lo = lds_read_tr16(lds + wat(v, col >> 3) + (col & 7));
-  const u32x2_t hi = lds_read_tr16(lds + wat(v + 4, col >> 3) + (col & 7));
+  const u32x2_t lo = lds_read_tr16(lds + wat<VT>(v, col >> 3) + (col & 7));
+  const u32x2_t hi = lds_read_tr16(lds + wat<VT>(v + 4, col >> 3) + (col & 7));
   return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
 }
 
-static __global__ __launch_bounds__(THREADS, 2) void k_loss_dx(Params p) {
+template <typename T>
+__global__ __launch_bounds__(T::THREADS, 2) void k_loss_dx(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
   const int live = min(*p.count - (int)p.row0, p.rows);
   if (live <= 0) return;
   // the piece's ranges, in the first piece's number (the last one may be shorter)
   const Split sp = split_of(p, live, p.piece);
-  const int tiles_m = (live + TILE - 1) / TILE, per = (tiles_m * p.tiles_n + 7) / 8 * 8;
-  const int split = blockIdx.x / per;
+  const int tiles_m = (live + T::TT - 1) / T::TT, tiles = tiles_m * p.tiles_n;
+  // (range by range: an XCD's blocks are tiles of one or two ranges, which share
+  // their words' W and E; the tiles of each range over all XCDs took 1.5 times as
+  // long, 933 rows of 2080 over 50021 words)
+  const int item = xcd_item(blockIdx.x, tiles * sp.n);
+  if (item < 0) return;
+  const int split = item / tiles;
   int tm, tn;
-  if (split >= sp.n || !map_tile(blockIdx.x % per, tiles_m, p.tiles_n, tm, tn)) return;
+  grouped(item - split * tiles, tiles_m, p.tiles_n, tm, tn);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int wk = wave & 1, wt = wave >> 1, h = lane >> 5;
-  const int c0 = tn * TILE;                 // first hidden column
+  const int wk = wave % T::WV, wt = wave / T::WV, h = lane >> 5;
+  const int c0 = tn * T::VT;                // first hidden column
   const int K = (int)p.K;
   const int R = (int)p.cols;
   const int s0 = split * sp.steps, s1 = min((R + BKS - 1) / BKS, s0 + sp.steps);
 
-  // E: rows of the chunk (lde covers whole tiles, zero past the last word)
-  const rsrc_t er = big::make_rsrc(p.E + (int64_t)tm * TILE * p.lde, big::clamp_bytes((int64_t)TILE * p.lde * 2));
-  const SlabLoad ld(p.lde, wave, lane);
-  // W: lane's row l / 32 of a 1-KB block of two words, chunk l % 32
-  const int wrow = lane >> 5, wpos = lane & 31;
-  // block b = 8 i + wave: words 2 b, 2 b + 1
-  const int wc = wpos ^ (((2 * wave + wrow) & 3) << 2);
-  const bool wc_ok = c0 + wc * 8 < K;
-  f32x16_t acc[4][2];
+  // E: the tile's rows that count (lde covers whole tiles, zero past the last word)
+  const rsrc_t er = big::make_rsrc(p.E + (int64_t)tm * T::TT * p.lde,
+                                   big::clamp_bytes((int64_t)min(T::TT, live - tm * T::TT) * p.lde * 2));
+  const SlabLoad<T::TT, T::NW> le(p.lde, wave, lane);
+  // W: a 1-KB block is WR words; lane's word lane / CPR of it, chunk lane % CPR
+  constexpr int CPR = T::VT / 8, WR = 64 / CPR, WN = BKS / WR / T::NW;
+  const int wrow = lane / CPR, wpos = lane % CPR;
+
+  f32x16_t acc[T::AV][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < T::AV; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
-  auto mma = [&](const Frags &f) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(f.a[i], f.b[j], acc[i][j]);
-  };
-  pipeline<10, Frags>(
+  using F = Frags<T::AV>;
+  pipeline<T::STAGES, WN + le.N, 2 * T::AV, 2 * T::AV + 2, F>(
       s0, s1,
       [&](int s, int stage) __attribute__((always_inline)) {
-        uint16_t *dst = smem + stage * 2 * SLAB;
-        const int64_t v = p.v0 + (int64_t)s * BKS;
-        const rsrc_t wr = big::make_rsrc(p.W + v * p.K, big::clamp_bytes(min((int64_t)BKS, p.v0 + p.cols - v) * p.K * 2));
+        uint16_t *dst = smem + stage * T::STAGE;
+        const int64_t v = p.v0 + (int64_t)s * BKS, left = p.v0 + p.cols - v;
+        const rsrc_t wr = big::make_rsrc(p.W + (left > 0 ? v : 0) * p.K,
+                                         big::clamp_bytes(min((int64_t)BKS, left) * p.K * 2));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int w = 2 * (8 * i + wave) + wrow;
-          load_lds16(wr, dst + (8 * i + wave) * 512, wc_ok ? (uint32_t)((w * K + c0 + wc * 8) * 2) : OOB, 0);
+        for (int i = 0; i < WN; ++i) {
+          const int w = WR * (T::NW * i + wave) + wrow;
+          const int c = c0 + (wpos ^ ((w & 3) << 2)) * 8;
+          load_lds16(wr, dst + (T::NW * i + wave) * 512, c < K ? (uint32_t)((w * K + c) * 2) : OOB, 0);
         }
-        ld.issue(er, dst + SLAB, s * BKS, (int)p.lde, wave);
+        le.issue(er, dst + T::SLAB_V, s * BKS, (int)p.lde, wave);
       },
-      [&](int stage, int kk, Frags &f) __attribute__((always_inline)) {
-        const uint16_t *Ws = smem + stage * 2 * SLAB, *Es = Ws + SLAB;
+      [&](int stage, int kk, F &f) __attribute__((always_inline)) {
+        const uint16_t *Ws = smem + stage * T::STAGE, *Es = Ws + T::SLAB_V;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f.a[i] = frag_w(Ws, kk * 16, wk * 128 + i * 32, lane);
+        for (int i = 0; i < T::AV; ++i) f.a[i] = frag_w<T::VT>(Ws, kk * 16, wk * T::STRIP + i * 32, lane);
 #pragma unroll
         for (int j = 0; j < 2; ++j) f.b[j] = frag(Es, wt * 64 + j * 32, kk, lane);
       },
-      mma);
+      [&](const F &f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < T::AV; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16(f.a[i], f.b[j], acc[i][j]);
+      });
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int tl = tm * TILE + wt * 64 + j * 32 + (lane & 31);
+    const int tl = tm * T::TT + wt * 64 + j * 32 + (lane & 31);
     if (tl >= live) continue;
-    float *dst = p.acc + split * sp.stride + (int64_t)tl * p.K + c0 + wk * 128 + 4 * h;
+    const int col = c0 + wk * T::STRIP + 4 * h;
+    float *dst = p.acc + split * sp.stride + (int64_t)tl * p.K + col;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < T::AV; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (c0 + wk * 128 + i * 32 + q * 8 >= K) continue;
+        if (col + i * 32 + q * 8 >= K) continue;
         f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         f32x4_t *d = reinterpret_cast<f32x4_t *>(dst + i * 32 + q * 8);
         if (!p.first) v += *d;
@@ -569,7 +616,8 @@ __device__ __forceinline__ float row_weight(const Params &p, int row, int count)
   return p.weight ? p.weight[row] : 1.0f / (float)count;
 }
 
-// A wave to a row of the chunk: its loss, and dX = w (acc - S W_t) / (S + s_t).
+// A wave to 512 columns of a row of the chunk (column block blockIdx.y): dX = w
+// (acc - S W_t) / (S + s_t), and by the first the row's loss.
 static __global__ __launch_bounds__(256) void k_loss_finish(Params p) {
   const int lane = threadIdx.x & 63;
   const int tl = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -581,34 +629,42 @@ static __global__ __launch_bounds__(256) void k_loss_finish(Params p) {
   // the target's own term (1 where the reference is its logit, as it mostly is)
   const float st = ref == lt ? 1.0f : exp2_hw((lt - ref) * LOG2E);
   const float sum = S + st;
-  const float up = ref == lt ? log1pf(S) : logf(sum);   // lse - ref
-  if (lane == 0) {
+  if (blockIdx.y == 0 && lane == 0) {
+    const float up = ref == lt ? log1pf(S) : logf(sum);   // lse - ref
     p.loss[row] = ref == lt ? up : up + (ref - lt);
     if (p.lse) p.lse[row] = up + ref;
   }
-  if (!p.dX) return;
+  const int64_t k = blockIdx.y * 512 + lane * 8;
+  if (!p.dX || k >= p.K) return;
   const float w = row_weight(p, row, count);
   const float a = w / sum, b = a * S;
-  const uint16_t *wt = p.W + (int64_t)max(p.tgt[at], 0) * p.K;
-  const float *src = p.acc + (int64_t)tl * p.K;
+  const u32x4_t wv = ldg_b128_cached(p.W + (int64_t)max(p.tgt[at], 0) * p.K + k);
   const Split sp = split_of(p, (int)min((int64_t)p.rows, count - p.row0), p.piece);
-  for (int64_t k = lane * 8; k < p.K; k += 512) {
-    f32x4_t lo = *reinterpret_cast<const f32x4_t *>(src + k), hi = *reinterpret_cast<const f32x4_t *>(src + k + 4);
-    for (int s = 1; s < sp.n; ++s) {
-      const float *q = src + s * sp.stride + k;
-      lo += *reinterpret_cast<const f32x4_t *>(q);
-      hi += *reinterpret_cast<const f32x4_t *>(q + 4);
-    }
-    const u32x4_t wv = ldg_b128_cached(wt + k);
-    float o[8];
+  const float *src = p.acc + (int64_t)tl * p.K + k;
+  f32x4_t lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
+  for (int s0 = 0; s0 < sp.n; s0 += 4) {
+    f32x4_t q[4][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float we = bf16_bits_to_f32((wv[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-      o[e] = __builtin_fmaf(a, e < 4 ? lo[e & 3] : hi[e & 3], -(b * we));
+    for (int u = 0; u < 4; ++u) {
+      const float *at_u = src + (int64_t)min(s0 + u, sp.n - 1) * sp.stride;
+      q[u][0] = *reinterpret_cast<const f32x4_t *>(at_u);
+      q[u][1] = *reinterpret_cast<const f32x4_t *>(at_u + 4);
     }
-    *reinterpret_cast<u32x4_t *>(p.dX + (int64_t)row * p.K + k) =
-        u32x4_t{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (s0 + u < sp.n) {
+        lo += q[u][0];
+        hi += q[u][1];
+      }
   }
+  float o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float we = bf16_bits_to_f32((wv[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+    o[e] = __builtin_fmaf(a, e < 4 ? lo[e & 3] : hi[e & 3], -(b * we));
+  }
+  *reinterpret_cast<u32x4_t *>(p.dX + (int64_t)row * p.K + k) =
+      u32x4_t{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
 }
 
 // total = sum of weight times loss over the rows that count: one block, in a
@@ -636,9 +692,9 @@ static __global__ __launch_bounds__(1024) void k_loss_total(Params p) {
 // as a unit of their own (loss.hip).
 const void *rows_kernel();
 const void *target_kernel();
-const void *logits_kernel(bool grad);
+const void *logits_kernel(bool grad, bool small);
 const void *join_kernel(bool grad, int rows);
-const void *dx_kernel();
+const void *dx_kernel(bool small);
 const void *finish_kernel();
 const void *total_kernel();
 

@@ -18,8 +18,65 @@ namespace {
 constexpr int64_t LOSS_CHUNK = 4096;
 constexpr int64_t LOSS_E_BYTES = int64_t(256) << 20;
 
+// The tiles of a launch.
+struct LossTiles {
+  bool small;
+  int tt, vt, wv, strip, per_cu, threads;
+  size_t lds;
+};
+template <typename T>
+LossTiles loss_tiles_of(bool small) {
+  return {small, T::TT, T::VT, T::WV, T::STRIP, T::PER_CU, T::THREADS, T::LDS_BYTES};
+}
+
+// Forced tiles for tests and measurements (LORA4_LOSS_TILES): small or big.
+int loss_tiles_policy() {
+  const char *e = std::getenv("LORA4_LOSS_TILES");
+  return !e ? 0 : std::strcmp(e, "small") == 0 ? 1 : std::strcmp(e, "big") == 0 ? 2 : 0;
+}
+
+// Microseconds of a 64-deep step and of a tile's start and end, by tile: big tiles
+// do eight times the work of small ones in 2.4 times the time, one to a CU instead
+// of two, and want many steps and tiles enough for every CU. Measured beside the
+// estimate (small / big, us): logits of 512 tokens, 4096 -> 32000 205 / 137, of 256
+// 108 / 123, of 1000, 4600 -> 2070 60 / 125, of 2753, 792 -> 5813 62 / 38; gradients
+// of the same 198 / 141, 106 / 85, 45 / 34, 64 / 49, of 300 tokens, 24639 -> 1024
+// 33 / 42.
+double loss_round_us(bool small, double steps) {
+  return small ? 0.8 * steps + 4.0 : 1.75 * steps + 9.0;
+}
+
+// The tiles of the logits: `rows` tokens by V words over K.
+LossTiles loss_logits_tiles(int64_t rows, int64_t K, int64_t V) {
+  const LossTiles t[2] = {loss_tiles_of<loss::Big>(false), loss_tiles_of<loss::Small>(true)};
+  if (const int f = loss_tiles_policy()) return t[f == 1];
+  double us[2];
+  for (int i = 0; i < 2; ++i) {
+    const int64_t tiles = ceil_div(rows, t[i].tt) * ceil_div(V, t[i].vt);
+    us[i] = (double)ceil_div(tiles, t[i].per_cu * cu_count()) * loss_round_us(i == 1, (double)ceil_div(K, loss::BKS));
+  }
+  return t[us[1] < us[0]];
+}
+
+// The tiles of acc: `rows` tokens by K columns over `words`, in the ranges of
+// split_of; the ranges are read again when they are summed.
+LossTiles loss_acc_tiles(int64_t rows, int64_t K, int64_t words) {
+  const LossTiles t[2] = {loss_tiles_of<loss::Big>(false), loss_tiles_of<loss::Small>(true)};
+  if (const int f = loss_tiles_policy()) return t[f == 1];
+  double us[2];
+  for (int i = 0; i < 2; ++i) {
+    const int64_t tiles = std::max<int64_t>(1, ceil_div(rows, t[i].tt) * ceil_div(K, t[i].vt));
+    const int64_t side = t[i].per_cu * cu_count(), steps = ceil_div(words, loss::BKS);
+    const int64_t n = std::max<int64_t>(1, std::min(side / tiles, steps / 8));
+    us[i] = (double)ceil_div(tiles * n, side) * loss_round_us(i == 1, (double)ceil_div(steps, n)) +
+            1e-6 * (double)n * (double)rows * (double)K;
+  }
+  return t[us[1] < us[0]];
+}
+
 struct LossPlan {
-  int64_t chunk;       // rows of a chunk, a multiple of TILE
+  LossTiles lt, dt;    // tiles of the logits and of acc
+  int64_t chunk;       // rows of a chunk, a multiple of the tiles'
   int64_t piece;       // words of a piece, a multiple of TILE
   size_t off_row, off_tgt, off_xc, off_lt, off_ref, off_s, off_sref, off_ssum, off_e, off_acc, bytes;
 };
@@ -42,7 +99,10 @@ lora4_status check_loss_sizes(int64_t M, int64_t K, int64_t V) {
 LossPlan loss_plan(bool grad, int64_t M, int64_t K, int64_t V) {
   constexpr int64_t T = loss::TILE;
   LossPlan pl{};
-  pl.chunk = std::min(LOSS_CHUNK, std::max<int64_t>(T, ceil_div(M, T) * T));
+  pl.lt = loss_logits_tiles(std::min(M, LOSS_CHUNK), K, V);
+  pl.dt = loss_acc_tiles(std::min(M, LOSS_CHUNK), K, V);
+  const int64_t unit = std::max(pl.lt.tt, pl.dt.tt);
+  pl.chunk = std::min(LOSS_CHUNK, std::max<int64_t>(unit, ceil_div(M, unit) * unit));
   const int64_t tiles_v = ceil_div(V, T);
   int64_t piece = std::min(tiles_v, loss_piece_policy());
   if (grad) {
@@ -61,13 +121,13 @@ LossPlan loss_plan(bool grad, int64_t M, int64_t K, int64_t V) {
   pl.off_lt = take((size_t)M * 4);
   pl.off_ref = take((size_t)M * 4);
   pl.off_s = take((size_t)M * 4);
-  const size_t strips = (size_t)(pl.piece / loss::STRIP) * pl.chunk * 4;
+  const size_t strips = (size_t)(pl.piece / pl.lt.strip) * pl.chunk * 4;
   pl.off_sref = take(strips);
   pl.off_ssum = take(strips);
   if (grad) {
     pl.off_e = take((size_t)pl.chunk * pl.piece * 2);
-    // the chunk's rows once, or as many ranges of fewer as fill the CUs (split_of)
-    pl.off_acc = take((size_t)std::max(pl.chunk, cu_count() / ceil_div(K, T) * T) * K * 4);
+    // the chunk's rows once, or as many ranges of fewer as fill the chip (split_of)
+    pl.off_acc = take((size_t)std::max(pl.chunk, pl.dt.per_cu * cu_count() / ceil_div(K, pl.dt.vt) * pl.dt.tt) * K * 4);
   }
   pl.bytes = off;
   return pl;
@@ -105,12 +165,14 @@ lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targ
   p.strip_sum = ws_at<float>(ws, pl.off_ssum);
   p.acc = ws_at<float>(ws, pl.off_acc);
   p.piece = pl.piece;
-  p.cus = cu_count();
+  p.strip = pl.lt.strip;
+  p.dt = pl.dt.tt;
+  p.dv = pl.dt.vt;
+  p.side = pl.dt.per_cu * cu_count();
   p.loss = out_loss;
   p.lse = lse;
   p.total = total;
   p.dX = dX;
-  constexpr int64_t T = loss::TILE;
   TRY(launch_fn("loss_rows", loss::rows_kernel(), 1, 1024, 0, st, p));
   if (M > 0) TRY(launch_fn("loss_target", loss::target_kernel(), ceil_div(M, 4), 256, 0, st, p));
   for (int64_t row0 = 0; row0 < M; row0 += pl.chunk) {
@@ -120,21 +182,22 @@ lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targ
       p.v0 = v0;
       p.cols = std::min(pl.piece, V - v0);
       p.first = v0 == 0;
-      p.tiles_m = (int)ceil_div(rows, T);
-      p.tiles_n = (int)ceil_div(p.cols, T);
-      TRY(launch_fn("loss_logits", loss::logits_kernel(grad), ceil_div((int64_t)p.tiles_m * p.tiles_n, 8) * 8,
-                    loss::THREADS, loss::LDS_BYTES, st, p));
+      p.tiles_m = (int)ceil_div(rows, pl.lt.tt);
+      p.tiles_n = (int)ceil_div(p.cols, pl.lt.vt);
+      p.strips = p.tiles_n * pl.lt.wv;
+      TRY(launch_fn("loss_logits", loss::logits_kernel(grad, pl.lt.small),
+                    ceil_div((int64_t)p.tiles_m * p.tiles_n, 8) * 8, pl.lt.threads, pl.lt.lds, st, p));
       const int nr = rows <= 256 ? 4 : 32;
       TRY(launch_fn("loss_join", loss::join_kernel(grad, nr), ceil_div(rows, nr), 1024, 0, st, p));
       if (!grad) continue;
-      p.tiles_n = (int)ceil_div(K, T);
-      // all tiles once, or ranges of fewer, up to a block a CU (split_of), the tiles
-      // of each range rounded up to the 8 XCDs
-      const int64_t tiles = ceil_div((int64_t)p.tiles_m * p.tiles_n, 8) * 8;
-      TRY(launch_fn("loss_dx", loss::dx_kernel(), std::max(tiles, p.cus + 7 * ceil_div(p.cus, p.tiles_n)),
-                    loss::THREADS, loss::LDS_BYTES, st, p));
+      p.tiles_m = (int)ceil_div(rows, pl.dt.tt);
+      p.tiles_n = (int)ceil_div(K, pl.dt.vt);
+      // all tiles once, or ranges of fewer up to what runs side by side (split_of)
+      const int64_t items = std::max<int64_t>((int64_t)p.tiles_m * p.tiles_n, p.side);
+      TRY(launch_fn("loss_dx", loss::dx_kernel(pl.dt.small), ceil_div(items, 8) * 8, pl.dt.threads, pl.dt.lds, st, p));
     }
-    TRY(launch_fn("loss_finish", loss::finish_kernel(), ceil_div(rows, 4), 256, 0, st, p));
+    TRY(launch_grid("loss_finish", loss::finish_kernel(), dim3((unsigned)ceil_div(rows, 4), grad ? (unsigned)ceil_div(K, 512) : 1u),
+                    256, 0, st, p));
   }
   return total ? launch_fn("loss_total", loss::total_kernel(), 1, 1024, 0, st, p) : LORA4_OK;
 }

@@ -98,7 +98,7 @@ void inspect(const std::string &name, void **args) {
     if (p.G * p.Hkv != p.Hq || p.splits < 1 || (p.splits > 1 && !p.part)) fail(context.c_str(), name.c_str());
   } else if (name.find("k_loss_") != std::string::npos) {
     const lora4::loss::Params &p = checked<lora4::loss::Params>(name, args[0]);
-    if (p.rows < 1 || p.cus < 1 || p.lde % lora4::loss::TILE) fail(context.c_str(), name.c_str());
+    if (p.rows < 1 || p.side < 1 || p.strip < 1 || p.lde % lora4::loss::TILE) fail(context.c_str(), name.c_str());
   } else {   // (scalars only)
     for (const char *k : {"k_fill_u16", "k_reduce_bf16", "k_col_sum", "k_col_sum_slots", "k_quant_mxfp8"})
       if (is(name, k)) return;

@@ -115,6 +115,16 @@ def test_pieces_of_the_vocabulary(monkeypatch, piece):
     run_case(70, 520, 777, seed=4, weights=True, grad=False)
 
 
+@pytest.mark.parametrize("tiles", ["small", "big"])
+@pytest.mark.parametrize("M,K,V", [(1, 8, 1), (5, 72, 130), (130, 520, 1000), (300, 256, 5003), (70, 2080, 129)])
+def test_either_tiles(monkeypatch, tiles, M, K, V):
+    monkeypatch.setenv("LORA4_LOSS_TILES", tiles)
+    run_case(M, K, V, seed=M + V, weights=True)
+    monkeypatch.setenv("LORA4_LOSS_PIECE", "256")
+    run_case(M, K, V, seed=M + V + 1)
+    run_case(M, K, V, seed=M + V + 2, grad=False)
+
+
 def test_chunks_of_the_rows():
     run_case(4100, 40, 300, seed=5)
     run_case(9000, 16, 500, seed=6, weights=True, ignored=0.6)

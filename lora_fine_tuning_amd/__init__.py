@@ -1104,9 +1104,7 @@ def backward_epilogue(base, X, dY, A, B, s, P=None, activation="none", Z=None, w
 # Attention
 # ---------------------------------------------------------------------------
 
-def _heads(t, name, dev=None, shape=None):
-    """Checks a bf16 tensor [T, H, D] whose tokens hold their heads contiguously
-    (columns of one projection's output among them); returns its token stride."""
+def _bad_heads(t, name, dev, shape):
     import torch
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a 3-D tensor [tokens, heads, D]")
@@ -1116,6 +1114,17 @@ def _heads(t, name, dev=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _heads(t, name, dev=None, shape=None):
+    """Checks a bf16 tensor [T, H, D] whose tokens hold their heads contiguously
+    (columns of one projection's output among them); returns its token stride."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.dim() == 3 and t.dtype is torch.bfloat16
+            and (shape is None or t.shape == shape) and (dev is None or t.device == dev)):
+        _bad_heads(t, name, dev, shape)
+    if t.is_contiguous():
+        return t.shape[1] * t.shape[2]
     T, H, D = t.shape
     if t.numel() == 0:
         return H * D
@@ -1144,6 +1153,8 @@ def _attention_args(Q, K, V, scale, q_offsets, k_offsets, k_lengths):
         raise ValueError(f"{Hq} query heads do not share {Hkv} key heads evenly")
     seqs = 1
     if q_offsets is not None:
+        if not isinstance(q_offsets, torch.Tensor):
+            raise ValueError("q_offsets must be a torch tensor")
         seqs = q_offsets.numel() - 1
         _need(q_offsets, "q_offsets", (max(seqs, 1) + 1,), torch.int64, dev)
         if k_offsets is not None:

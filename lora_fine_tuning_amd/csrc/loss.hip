@@ -12,7 +12,7 @@ const void *addr(K *k) {
 }  // namespace
 
 const void *rows_kernel() { return addr(k_loss_rows); }
-const void *target_kernel() { return addr(k_loss_target); }
+const void *target_kernel(bool find) { return find ? addr(k_loss_target<true>) : addr(k_loss_target<false>); }
 const void *logits_kernel(bool grad, bool small) {
   if (small) return grad ? addr(k_loss_logits<true, Small>) : addr(k_loss_logits<false, Small>);
   return grad ? addr(k_loss_logits<true, Big>) : addr(k_loss_logits<false, Big>);

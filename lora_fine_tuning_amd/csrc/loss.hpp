@@ -84,10 +84,11 @@ struct Params {
   uint16_t *E;              // [rows][lde]
   int64_t lde;              // a multiple of TILE
   int strip, strips;        // words of a strip, strips of the piece's tiles
-  float *strip_ref, *strip_sum;   // [strips][rows]
+  float *strip_ref, *strip_sum;   // [strips][live rows]
   float *acc;               // [splits][live rows, whole tiles][K]
   int dt, dv;               // tokens and hidden columns of acc's tiles
   int side;                 // blocks of acc's product that run side by side
+  int total_block;          // k_loss_finish makes total
   int first;                // first piece: acc is written, not added to
   int tiles_m, tiles_n;
   // outputs
@@ -209,42 +210,78 @@ struct Frags {
 // The rows that count
 // ---------------------------------------------------------------------------
 
-// One block: the rows whose target is not `ignore`, in order. (Every row is
-// looked at by this block alone; 4096 rows take four rounds.)
-static __global__ __launch_bounds__(1024) void k_loss_rows(Params p) {
-  __shared__ int wsum[16];
-  __shared__ int base;
+// Rows of a batch whose blocks find the rows that count each for themselves, in
+// one round of their threads a quarter of it (a launch less; the targets are read
+// from the L2).
+constexpr int SHORT = 1024;
+
+// The rows whose target is not `ignore`, in order: one block of NT threads looks at
+// [0, M) and calls put(index among them, row, target) for each; returns their
+// number. Every thread of the block takes part.
+template <int NT, typename Put>
+__device__ __forceinline__ int find_rows(const Params &p, int *wsum, Put &&put) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (threadIdx.x == 0) base = 0;
-  __syncthreads();
-  for (int64_t i0 = 0; i0 < p.M; i0 += 1024) {
+  int base = 0;
+  for (int64_t i0 = 0; i0 < p.M; i0 += NT) {
     const int64_t i = i0 + threadIdx.x;
     const int64_t t = i < p.M ? p.target[i] : p.ignore;
     const bool in = t != p.ignore;
     const unsigned long long b = __ballot(in);
+    __syncthreads();   // (the round before is done with wsum)
     if (lane == 0) wsum[wave] = __popcll(b);
     __syncthreads();
     int before = base;
-    for (int w = 0; w < wave; ++w) before += wsum[w];
-    if (in) {
-      const int at = before + __popcll(b & ((1ull << lane) - 1));
-      p.row[at] = (int)i;
-      p.tgt[at] = t >= 0 && t < p.V ? (int)t : -1;
+    for (int w = 0; w < NT / 64; ++w) {
+      if (w < wave) before += wsum[w];
+      base += wsum[w];
     }
-    __syncthreads();
-    if (threadIdx.x == 0)
-      for (int w = 0; w < 16; ++w) base += wsum[w];
-    __syncthreads();
+    if (in) put(before + __popcll(b & ((1ull << lane) - 1)), (int)i, t >= 0 && t < p.V ? (int)t : -1);
   }
-  if (threadIdx.x == 0) *p.count = base;
+  return base;
+}
+
+// One block.
+static __global__ __launch_bounds__(1024) void k_loss_rows(Params p) {
+  __shared__ int wsum[16];
+  const int n = find_rows<1024>(p, wsum, [&](int at, int row, int tgt) {
+    p.row[at] = row;
+    p.tgt[at] = tgt;
+  });
+  if (threadIdx.x == 0) *p.count = n;
 }
 
 // A wave to a row that counts: its X beside the others', and the logit of its
 // target (NaN for a target that is no word: the row's outputs become NaN). And a
-// wave to a row that does not: loss, lse and dX of row i are zero.
-static __global__ __launch_bounds__(256) void k_loss_target(Params p) {
-  const int lane = threadIdx.x & 63;
-  const int at = blockIdx.x * 4 + (threadIdx.x >> 6);
+// wave to a row that does not: loss, lse and dX of row i are zero. FIND: without
+// k_loss_rows before it (M <= SHORT).
+template <bool FIND>
+__global__ __launch_bounds__(256) void k_loss_target(Params p) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int at = blockIdx.x * 4 + wave;
+  int count, row = 0, t = 0;
+  if constexpr (FIND) {
+    __shared__ int wsum[4], mine[4][2];
+    count = find_rows<256>(p, wsum, [&](int i, int r, int g) {
+      if (blockIdx.x == 0) {
+        p.row[i] = r;
+        p.tgt[i] = g;
+      }
+      if (i / 4 == (int)blockIdx.x) {
+        mine[i & 3][0] = r;
+        mine[i & 3][1] = g;
+      }
+    });
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = count;
+    __syncthreads();
+    row = mine[wave][0];
+    t = mine[wave][1];
+  } else {
+    count = *p.count;
+    if (at < count) {
+      row = p.row[at];
+      t = p.tgt[at];
+    }
+  }
   if (at < p.M && p.target[at] == p.ignore) {
     if (lane == 0) {
       p.loss[at] = 0.0f;
@@ -254,9 +291,8 @@ static __global__ __launch_bounds__(256) void k_loss_target(Params p) {
       for (int64_t k = lane * 8; k < p.K; k += 512)
         *reinterpret_cast<u32x4_t *>(p.dX + (int64_t)at * p.K + k) = u32x4_t{0u, 0u, 0u, 0u};
   }
-  if (at >= *p.count) return;
-  const int t = p.tgt[at];
-  const uint16_t *x = p.X + (int64_t)p.row[at] * p.K;
+  if (at >= count) return;
+  const uint16_t *x = p.X + (int64_t)row * p.K;
   const uint16_t *w = p.W + (int64_t)max(t, 0) * p.K;
   uint16_t *xc = p.Xc + (int64_t)at * p.K;
   float s = 0.0f;
@@ -282,6 +318,9 @@ static __global__ __launch_bounds__(256) void k_loss_target(Params p) {
 // ---------------------------------------------------------------------------
 // Logits of a piece: strip maxima and sums, and E
 // ---------------------------------------------------------------------------
+
+// Rows between strips: those that count (lines of few rows hold many strips).
+__device__ __forceinline__ int strip_ld(int live) { return (live + 7) & ~7; }
 
 // The tile's results: wave (wv, wt) holds the words of a strip, AV blocks, of
 // tokens 64 wt .. + 63 (2 blocks).
@@ -373,8 +412,10 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_loss_logits(Params p) {
         sum += e;
       }
     sum += __shfl_xor(sum, 32);
-    if (h == 0) p.strip_ref[(int64_t)strip * p.rows + tl] = rs;
-    else p.strip_sum[(int64_t)strip * p.rows + tl] = sum;
+    if (ok) {
+      if (h == 0) p.strip_ref[(int64_t)strip * strip_ld(live) + tl] = rs;
+      else p.strip_sum[(int64_t)strip * strip_ld(live) + tl] = sum;
+    }
     if constexpr (GRAD) {
       if (!ok) continue;   // (both halves of a row)
       uint16_t *dst = p.E + (int64_t)tl * p.lde + tn * T::VT + wv * T::STRIP;
@@ -422,7 +463,7 @@ __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
   __shared__ float nref[NR], fac[NR];
   __shared__ int moved[NR];
   const int tx = threadIdx.x % NR, ty = threadIdx.x / NR;   // row, strip group
-  const int live = *p.count - (int)p.row0;
+  const int live = min(*p.count - (int)p.row0, p.rows), ld = strip_ld(live);
   const int tl = blockIdx.x * NR + tx;
   if ((int)blockIdx.x * NR >= live) return;
   const int strips = p.strips;
@@ -436,7 +477,7 @@ __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
       float r[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        r[u] = s0 + u * NT < strips ? p.strip_ref[(int64_t)(s0 + u * NT) * p.rows + tl] : ref;
+        r[u] = s0 + u * NT < strips ? p.strip_ref[(int64_t)(s0 + u * NT) * ld + tl] : ref;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         nan |= r[u] != r[u];
@@ -463,7 +504,7 @@ __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
       float r[4], v[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int64_t i = (int64_t)(s0 + u * NT) * p.rows + tl;
+        const int64_t i = (int64_t)(s0 + u * NT) * ld + tl;
         r[u] = s0 + u * NT < strips ? p.strip_ref[i] : m;
         v[u] = s0 + u * NT < strips ? p.strip_sum[i] : 0.0f;
       }
@@ -488,7 +529,7 @@ __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
       const int row = blockIdx.x * NR + r;
       if (row >= live || !moved[r]) continue;   // uniform
       for (int64_t c = threadIdx.x; c < (int64_t)strips * p.strip; c += 1024) {
-        const float sr = p.strip_ref[(c / p.strip) * p.rows + row];
+        const float sr = p.strip_ref[(c / p.strip) * ld + row];
         if (sr == nref[r]) continue;
         uint16_t *e = p.E + (int64_t)row * p.lde + c;
         *e = to_bf16(bf16_bits_to_f32(*e) * exp2_hw((sr - nref[r]) * LOG2E));
@@ -616,23 +657,58 @@ __device__ __forceinline__ float row_weight(const Params &p, int row, int count)
   return p.weight ? p.weight[row] : 1.0f / (float)count;
 }
 
+// Loss and lse - ref of a row. The target's own term is 1 where the reference is
+// its logit, as it mostly is.
+struct RowLoss {
+  float loss, up, sum;
+};
+__device__ __forceinline__ RowLoss row_loss(const Params &p, int64_t at) {
+  const float S = p.S[at], lt = p.lt[at], ref = p.ref[at];
+  RowLoss r;
+  r.sum = S + (ref == lt ? 1.0f : exp2_hw((lt - ref) * LOG2E));
+  r.up = ref == lt ? log1pf(S) : logf(r.sum);
+  r.loss = ref == lt ? r.up : r.up + (ref - lt);
+  return r;
+}
+
+// total = sum of weight times loss over the rows that count: one block of NT
+// threads, in a fixed order.
+template <int NT>
+__device__ __forceinline__ void sum_total(const Params &p, int count) {
+  __shared__ float red[NT / 64];
+  float s = 0.0f;
+  for (int i = threadIdx.x; i < count; i += NT) s += row_weight(p, p.row[i], count) * row_loss(p, i).loss;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float t = 0.0f;
+    for (int w = 0; w < NT / 64; ++w) t += red[w];
+    *p.total = t;
+  }
+}
+
 // A wave to 512 columns of a row of the chunk (column block blockIdx.y): dX = w
-// (acc - S W_t) / (S + s_t), and by the first the row's loss.
+// (acc - S W_t) / (S + s_t), and by the first the row's loss. The last block in x,
+// where there is one more than the rows need, makes total.
 static __global__ __launch_bounds__(256) void k_loss_finish(Params p) {
   const int lane = threadIdx.x & 63;
   const int tl = blockIdx.x * 4 + (threadIdx.x >> 6);
   const int count = *p.count;
+  if (p.total_block && blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y == 0) sum_total<256>(p, count);
+    return;
+  }
   const int64_t at = p.row0 + tl;
   if (at >= count || tl >= p.rows) return;
   const int row = p.row[at];
-  const float S = p.S[at], lt = p.lt[at], ref = p.ref[at];
-  // the target's own term (1 where the reference is its logit, as it mostly is)
-  const float st = ref == lt ? 1.0f : exp2_hw((lt - ref) * LOG2E);
-  const float sum = S + st;
+  const float S = p.S[at];
+  const RowLoss r = row_loss(p, at);
+  const float sum = r.sum;
   if (blockIdx.y == 0 && lane == 0) {
-    const float up = ref == lt ? log1pf(S) : logf(sum);   // lse - ref
-    p.loss[row] = ref == lt ? up : up + (ref - lt);
-    if (p.lse) p.lse[row] = up + ref;
+    p.loss[row] = r.loss;
+    if (p.lse) p.lse[row] = r.up + p.ref[at];
   }
   const int64_t k = blockIdx.y * 512 + lane * 8;
   if (!p.dX || k >= p.K) return;
@@ -667,31 +743,13 @@ static __global__ __launch_bounds__(256) void k_loss_finish(Params p) {
       u32x4_t{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
 }
 
-// total = sum of weight times loss over the rows that count: one block, in a
-// fixed order.
-static __global__ __launch_bounds__(1024) void k_loss_total(Params p) {
-  __shared__ float red[16];
-  const int count = *p.count;
-  float s = 0.0f;
-  for (int i = threadIdx.x; i < count; i += 1024) {
-    const int row = p.row[i];
-    s += row_weight(p, row, count) * p.loss[row];
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float t = 0.0f;
-    for (int w = 0; w < 16; ++w) t += red[w];
-    *p.total = t;
-  }
-}
+// total by itself, of several chunks.
+static __global__ __launch_bounds__(1024) void k_loss_total(Params p) { sum_total<1024>(p, *p.count); }
 
 // The kernels as the host code launches them: by address, so that they compile
 // as a unit of their own (loss.hip).
 const void *rows_kernel();
-const void *target_kernel();
+const void *target_kernel(bool find);
 const void *logits_kernel(bool grad, bool small);
 const void *join_kernel(bool grad, int rows);
 const void *dx_kernel(bool small);

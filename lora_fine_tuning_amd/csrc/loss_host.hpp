@@ -1,10 +1,10 @@
 // Host side of the vocabulary loss (included by lora4.hip behind its dispatch
 // helpers): validation, workspace layout and launch order.
 //
-//   k_loss_rows -> k_loss_target -> per chunk of rows:
+//   [k_loss_rows ->] k_loss_target -> per chunk of rows:
 //       per piece of the vocabulary: k_loss_logits -> k_loss_join [-> k_loss_dx]
 //       k_loss_finish
-//   -> k_loss_total
+//   [-> k_loss_total]
 //
 // How many rows count is known on the device alone: the grids cover all M, and
 // blocks past the last row that counts end at once.
@@ -173,8 +173,10 @@ lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targ
   p.lse = lse;
   p.total = total;
   p.dX = dX;
-  TRY(launch_fn("loss_rows", loss::rows_kernel(), 1, 1024, 0, st, p));
-  if (M > 0) TRY(launch_fn("loss_target", loss::target_kernel(), ceil_div(M, 4), 256, 0, st, p));
+  const bool find = M > 0 && M <= loss::SHORT;
+  if (!find) TRY(launch_fn("loss_rows", loss::rows_kernel(), 1, 1024, 0, st, p));
+  if (M > 0) TRY(launch_fn("loss_target", loss::target_kernel(find), ceil_div(M, 4), 256, 0, st, p));
+  p.total_block = total && M > 0 && M <= pl.chunk;   // (every row's sum is there by then)
   for (int64_t row0 = 0; row0 < M; row0 += pl.chunk) {
     p.row0 = row0;
     const int64_t rows = std::min(pl.chunk, M - row0);
@@ -196,10 +198,10 @@ lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targ
       const int64_t items = std::max<int64_t>((int64_t)p.tiles_m * p.tiles_n, p.side);
       TRY(launch_fn("loss_dx", loss::dx_kernel(pl.dt.small), ceil_div(items, 8) * 8, pl.dt.threads, pl.dt.lds, st, p));
     }
-    TRY(launch_grid("loss_finish", loss::finish_kernel(), dim3((unsigned)ceil_div(rows, 4), grad ? (unsigned)ceil_div(K, 512) : 1u),
+    TRY(launch_grid("loss_finish", loss::finish_kernel(), dim3((unsigned)(ceil_div(rows, 4) + p.total_block), grad ? (unsigned)ceil_div(K, 512) : 1u),
                     256, 0, st, p));
   }
-  return total ? launch_fn("loss_total", loss::total_kernel(), 1, 1024, 0, st, p) : LORA4_OK;
+  return total && !p.total_block ? launch_fn("loss_total", loss::total_kernel(), 1, 1024, 0, st, p) : LORA4_OK;
 }
 
 }  // namespace

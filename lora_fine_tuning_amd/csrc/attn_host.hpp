@@ -32,7 +32,6 @@ lora4_status check_attn_sizes(int64_t Tq, int64_t Tk, int64_t seqs, int32_t Hq, 
 // Blocks that keep the chip busy: two a CU.
 int64_t attn_full_grid() { return 2 * (int64_t)cu_count(); }
 
-int64_t tune(const char *n, int64_t d) { const char *e = std::getenv(n); return e ? std::atoll(e) : d; }
 AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int Hkv, int D) {
   AttnPlan pl{};
   const int64_t G = Hq / Hkv;
@@ -45,7 +44,12 @@ AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int 
   if (which == 0) {
     const int64_t blocks = std::max<int64_t>(1, std::max(Tq * G / attn::ROWS, std::min(seqs, Tq)) * Hkv);
     const int64_t most = std::max<int64_t>(1, keys / (4 * attn::KEYS));
-    pl.splits = (int)std::min<int64_t>(std::min<int64_t>(attn::MAX_SPLITS, most), std::max<int64_t>(1, tune("TA", 4) * attn_full_grid() / 4 / blocks));
+    // Single tokens (rows of one wave) over caches of different fill: eight blocks a
+    // CU, so that a long cache does not end last (24 tokens over 5 to 32 thousand keys,
+    // 64 heads: 367 us, with two a CU 429). Else two, more only add to the join
+    // (3 chunks of 333 tokens, 14 heads: 36 us, with four a CU 40, with one 43).
+    const int64_t full = (rows <= 32 ? 4 : 1) * attn_full_grid();
+    pl.splits = (int)std::min<int64_t>(std::min<int64_t>(attn::MAX_SPLITS, most), std::max<int64_t>(1, full / blocks));
     pl.bytes = 256;
     if (pl.splits > 1) {
       pl.off_part = align256((size_t)pl.splits * Tq * Hq * 8);
@@ -54,8 +58,11 @@ AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int 
   } else {
     const int64_t blocks = std::max<int64_t>(1, std::max(Tk / attn::BKEYS, std::min(seqs, Tk)) * Hkv);
     const int64_t most = std::max<int64_t>(1, rows / (8 * attn::BROWS));
+    // Four blocks a CU where the key tiles give fewer: the first keys of a sequence
+    // are seen by all of its rows, the last by few (packed 4096 tokens, 8 key heads:
+    // 1, 2, 4, 8 ranges 229, 144 + 17, 116 + 28, 115 + 42 us with their sums).
     pl.ksplits = (int)std::min<int64_t>(std::min<int64_t>(16, most),
-                                        std::max<int64_t>(1, ceil_div(tune("TB", 4) * attn_full_grid() / 2, blocks)));
+                                        std::max<int64_t>(1, ceil_div(2 * attn_full_grid(), blocks)));
     pl.off_part = align256((size_t)std::max<int64_t>(1, Tq * Hq) * 8);
     pl.bytes = pl.off_part + (pl.ksplits > 1 ? align256((size_t)pl.ksplits * 2 * Tk * Hkv * D * 4) : 0);
   }

@@ -251,7 +251,8 @@ static __global__ __launch_bounds__(1024) void k_loss_rows(Params p) {
 }
 
 // A wave to a row that counts: its X beside the others', and the logit of its
-// target (NaN for a target that is no word: the row's outputs become NaN). And a
+// target (NaN for a target that is no word or whose logit is +infinity: the row's
+// outputs become NaN). And a
 // wave to a row that does not: loss, lse and dX of row i are zero. FIND: without
 // k_loss_rows before it (M <= SHORT).
 template <bool FIND>
@@ -308,7 +309,7 @@ __global__ __launch_bounds__(256) void k_loss_target(Params p) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
   if (lane == 0) {
-    if (t < 0) s = __builtin_nanf("");
+    if (t < 0 || s == INFINITY) s = __builtin_nanf("");
     p.lt[at] = s;
     p.ref[at] = s;
     p.S[at] = 0.0f;
@@ -402,7 +403,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void k_loss_logits(Params p) {
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     const float rs = (mx - ref) * LOG2E > REF_SLACK ? mx : ref;
     float sum = 0.0f;
-    const float rl = rs * LOG2E;
+    const float rl = rs == -INFINITY ? 0.0f : rs * LOG2E;   // (a strip of -infinity alone: zeros)
 #pragma unroll
     for (int i = 0; i < T::AV; ++i)
 #pragma unroll
@@ -668,6 +669,7 @@ __device__ __forceinline__ RowLoss row_loss(const Params &p, int64_t at) {
   r.sum = S + (ref == lt ? 1.0f : exp2_hw((lt - ref) * LOG2E));
   r.up = ref == lt ? log1pf(S) : logf(r.sum);
   r.loss = ref == lt ? r.up : r.up + (ref - lt);
+  if (ref == -INFINITY) r.loss = r.sum = __builtin_nanf("");   // no logit above -infinity
   return r;
 }
 

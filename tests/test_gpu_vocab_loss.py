@@ -228,3 +228,75 @@ def test_another_stream_and_a_captured_graph():
         eager = L.head_loss(X, W, t, want_lse=True)
         for n in ref:
             assert torch.equal(out[n], eager[n]), (i, n)
+
+
+def test_a_head_past_32_bit_offsets():
+    """600000 words of 4096: 4.9 GB, the last words beyond 2^31 elements, in two
+    pieces. The reference in float64 on the GPU, in ranges of the vocabulary."""
+    M, K, V = 3, 4096, 600000
+    g = torch.Generator(device=DEV).manual_seed(3)
+    W = torch.empty(V, K, dtype=torch.bfloat16, device=DEV)
+    for i in range(0, V, 100000):
+        W[i:i + 100000] = torch.randn((100000, K), generator=g, device=DEV) * 0.02
+    X = torch.randn((M, K), generator=g, device=DEV).to(torch.bfloat16)
+    t = torch.tensor([V - 1, 7, 550000], device=DEV)
+    o = L.head_loss(X, W, t, want_lse=True)
+    alone = L.head_loss(X, W, t, want_grad=False)
+    l = torch.cat([X.double() @ W[i:i + 50000].double().t() for i in range(0, V, 50000)], 1)
+    lse = torch.logsumexp(l, 1)
+    p = torch.exp(l - lse[:, None])
+    p[torch.arange(M), t] -= 1
+    dX = sum(p[:, i:i + 50000] @ W[i:i + 50000].double() for i in range(0, V, 50000)) / M
+    loss = lse - l[torch.arange(M), t]
+    for r in (o, alone):
+        assert torch.all((r["loss"].double() - loss).abs() <= 1e-5 * loss)
+    err = (o["dX"].double() - dX).norm() / dX.norm()
+    assert float(err) <= TOL
+
+
+def test_two_calls_at_once():
+    rng = np.random.default_rng(14)
+    jobs = []
+    for M, K, V in ((200, 256, 3000), (5, 512, 900)):
+        a = (to_dev(normal(rng, (M, K))), to_dev(normal(rng, (V, K), 0.2)), torch.from_numpy(rng.integers(0, V, M)).to(DEV))
+        jobs.append((a, L.head_loss(*a)))
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    got = [[] for _ in jobs]
+    for _ in range(5):
+        for i, (s, (a, _)) in enumerate(zip(streams, jobs)):
+            with torch.cuda.stream(s):
+                got[i].append(L.head_loss(*a))
+    torch.cuda.synchronize()
+    for g, (_, ref) in zip(got, jobs):
+        assert all(torch.equal(x[n], ref[n]) for x in g for n in ("loss", "total", "dX"))
+
+
+def test_gradient_against_differences():
+    """d total along a direction, by the float64 loss around the bf16 inputs: off by
+    at most 2 u of the sum of the gradient's terms."""
+    rng = np.random.default_rng(15)
+    X, W, t = normal(rng, (60, 96)), normal(rng, (700, 96), 0.2), rng.integers(0, 700, 60)
+    t[::7] = -100
+    g = f64(to_host(L.head_loss(to_dev(X), to_dev(W), torch.from_numpy(t).to(DEV))["dX"]))
+    d = rng.standard_normal(g.shape)
+    f = lambda x: vocab_loss.loss(x, f64(W), t)["total"]
+    num = (f(f64(X) + 1e-5 * d) - f(f64(X) - 1e-5 * d)) / 2e-5
+    assert abs(num - (g * d).sum()) <= 2 * 2.0 ** -8 * np.abs(g * d).sum()
+
+
+def test_infinite_logits():
+    """A target whose logit is -infinity costs infinity, one of +infinity NaN; the
+    other rows are as without them."""
+    rng = np.random.default_rng(16)
+    X, W = normal(rng, (4, 64)), normal(rng, (50, 64))
+    W[10] = 0
+    t = np.array([3, 10, 10, 5])
+    W2 = W.copy()
+    W2[10, 0] = 0xFF80                    # -inf times X[., 0]
+    X[1, 0], X[2, 0], X[0, 0], X[3, 0] = 0x3F80, 0xBF80, 0x3F80, 0x3F80   # 1, -1, 1, 1
+    o = L.head_loss(to_dev(X), to_dev(W2), torch.from_numpy(t).to(DEV), weights=torch.ones(4, device=DEV), want_grad=False)
+    l = o["loss"].cpu().numpy()
+    assert np.isposinf(l[1]) and np.isnan(l[2])
+    ref = vocab_loss.loss(f64(X)[[0, 3]], np.delete(f64(W), 10, 0), np.array([3, 5]))["loss"]
+    assert np.allclose(l[[0, 3]], ref, rtol=1e-5)

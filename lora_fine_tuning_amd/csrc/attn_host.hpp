@@ -59,10 +59,13 @@ AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int 
     const int64_t blocks = std::max<int64_t>(1, std::max(Tk / attn::BKEYS, std::min(seqs, Tk)) * Hkv);
     const int64_t most = std::max<int64_t>(1, rows / (8 * attn::BROWS));
     // Four blocks a CU where the key tiles give fewer: the first keys of a sequence
-    // are seen by all of its rows, the last by few (packed 4096 tokens, 8 key heads:
-    // 1, 2, 4, 8 ranges 229, 144 + 17, 116 + 28, 115 + 42 us with their sums).
+    // are seen by all of its rows, the last by few, and the long blocks start first
+    // (packed 4096 tokens, 8 key heads: 1, 2, 4, 8 ranges 229, 144, 104, 125 us, their
+    // sums 0, 17, 28, 101). One more where it leaves each 256 steps, whose partials
+    // are little beside them (8192 tokens, 64 heads: 2 ranges 2439 + 30, 3 2330 + 45).
     pl.ksplits = (int)std::min<int64_t>(std::min<int64_t>(16, most),
                                         std::max<int64_t>(1, ceil_div(2 * attn_full_grid(), blocks)));
+    if (rows / attn::BROWS / (pl.ksplits + 1) >= 256) ++pl.ksplits;
     pl.off_part = align256((size_t)std::max<int64_t>(1, Tq * Hq) * 8);
     pl.bytes = pl.off_part + (pl.ksplits > 1 ? align256((size_t)pl.ksplits * 2 * Tk * Hkv * D * 4) : 0);
   }

@@ -249,12 +249,14 @@ __device__ __forceinline__ Halves both_halves(float x) {
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // B operand straight from memory: this lane's row, 8 columns from 16 kk + 8 h.
+// Columns past D take the row's first ones: the other operand is zero there. (All
+// loads without a condition: a branch to each cost more than the loads.)
 template <int DC>
-__device__ __forceinline__ void load_row_frags(u32x4_t (&f)[2 * DC], const uint16_t *row, bool ok, int D, int h) {
+__device__ __forceinline__ void load_row_frags(u32x4_t (&f)[2 * DC], const uint16_t *row, int D, int h) {
 #pragma unroll
   for (int kk = 0; kk < 2 * DC; ++kk) {
     const int c = 16 * kk + 8 * h;
-    f[kk] = ok && c < D ? ldg_b128_cached(row + c) : u32x4_t{0u, 0u, 0u, 0u};
+    f[kk] = ldg_b128_cached(row + (c < D ? c : 0));
   }
 }
 
@@ -338,7 +340,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
   const int qi = (int)row_query(p, (uint32_t)(row_ok ? r : R - 1));
   const int64_t oi = (t.q0 + qi) * p.Hq + j.head * p.G + ((row_ok ? r : R - 1) - qi * p.G);   // (token, head)
   u32x4_t qf[2 * DC];
-  load_row_frags<DC>(qf, p.Q + (t.q0 + qi) * p.ldq + (oi - (t.q0 + qi) * p.Hq) * p.D, row_ok, p.D, h);
+  load_row_frags<DC>(qf, p.Q + (t.q0 + qi) * p.ldq + (oi - (t.q0 + qi) * p.Hq) * p.D, p.D, h);
 
   // keys that the block's last row sees, and that all of the wave's rows see
   const int q_hi = (int)row_query(p, (uint32_t)min(R - 1, t.tile * ROWS + ROWS - 1));
@@ -380,15 +382,14 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
     const int k0 = s * KEYS;
     if (k0 >= wend) return;   // (no row of the wave sees these keys)
 
+    __builtin_amdgcn_s_setprio(1);   // products before the other wave's softmax (1 % of a long prompt)
     f32x16_t sc[2];
     u32x4_t vf[DC];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      sc[kb] = f32x16_t{};
+    for (int kk = 0; kk < 2 * DC; ++kk)
 #pragma unroll
-      for (int kk = 0; kk < 2 * DC; ++kk)
-        sc[kb] = mfma_32x32x16(frag_rows<DC>(Ks, kb * 32, kk, lane), qf[kk], sc[kb]);
-    }
+      for (int kb = 0; kb < 2; ++kb)
+        sc[kb] = mfma_32x32x16(frag_rows<DC>(Ks, kb * 32, kk, lane), qf[kk], kk == 0 ? f32x16_t{} : sc[kb]);
 #pragma unroll
     for (int db = 0; db < DC; ++db) vf[db] = frag_cols<DC>(Vs, 0, db, lane);
     // four reads ahead of the products, V's first operands behind the last ones
@@ -403,6 +404,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
       sched_mfma<1>();
       sched_read<(2 * DC + 3) / 4>();
     }
+    __builtin_amdgcn_s_setprio(0);
     if (k0 + KEYS > full) {
       asm volatile("");   // a branch, not 32 selects in every step
       const int lk = lim - k0 - 4 * h;
@@ -442,6 +444,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
         sc[kb][i] = e;
         l[i & 1] += e;
       }
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const u32x4_t pf = pack8(sc[b >> 1], (b & 1) * 8);
@@ -457,6 +460,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
       sched_read<2>();
     }
     sched_mfma<DC>();
+    __builtin_amdgcn_s_setprio(0);
   });
 
   const Halves lh = both_halves(l[0] + l[1]);
@@ -550,8 +554,8 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
   const int64_t oi = (t.q0 + qi) * p.Hq + j.head * p.G + ((row_ok ? r : R - 1) - qi * p.G);
   const int64_t hd = (oi - (t.q0 + qi) * p.Hq) * p.D;   // the head's first column
   u32x4_t qf[2 * DC], of[2 * DC];
-  load_row_frags<DC>(qf, p.Q + (t.q0 + qi) * p.ldq + hd, row_ok, p.D, h);
-  load_row_frags<DC>(of, p.dO + oi * p.D, row_ok, p.D, h);
+  load_row_frags<DC>(qf, p.Q + (t.q0 + qi) * p.ldq + hd, p.D, h);
+  load_row_frags<DC>(of, p.dO + oi * p.D, p.D, h);
   const float ls = p.lse[oi];
   // a row that saw no key has no gradient: P = exp2(-inf) = 0
   const float lse2 = ls == -INFINITY ? INFINITY : ls * LOG2E;
@@ -559,7 +563,8 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
 #pragma unroll
   for (int kk = 0; kk < 2 * DC; ++kk) {
     const int col = 16 * kk + 8 * h;
-    const u32x4_t o = row_ok && col < p.D ? ldg_b128_cached(p.Oin + oi * p.D + col) : u32x4_t{0u, 0u, 0u, 0u};
+    u32x4_t o = ldg_b128_cached(p.Oin + oi * p.D + (col < p.D ? col : 0));
+    if (col >= p.D) o = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       dl = __builtin_fmaf(bf16_bits_to_f32(o[e] & 0xFFFFu), bf16_bits_to_f32(of[kk][e] & 0xFFFFu), dl);
@@ -685,8 +690,8 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
   const bool key_ok = key < t.Lk;
   const int64_t kr = t.k0 + (key_ok ? key : t.Lk - 1);
   u32x4_t kf[2 * DC], vf[2 * DC];
-  load_row_frags<DC>(kf, p.K + kr * p.ldk + j.head * p.D, key_ok, p.D, h);
-  load_row_frags<DC>(vf, p.V + kr * p.ldv + j.head * p.D, key_ok, p.D, h);
+  load_row_frags<DC>(kf, p.K + kr * p.ldk + j.head * p.D, p.D, h);
+  load_row_frags<DC>(vf, p.V + kr * p.ldv + j.head * p.D, p.D, h);
 
   // rows from the first query that sees the tile's first key
   const int64_t r_lo = (int64_t)max(0, kt - off) * p.G;
@@ -760,9 +765,10 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
       const int lane = (int)ln, h = lane >> 5;
       f32x16_t sc = f32x16_t{}, dp = f32x16_t{};
 #pragma unroll
-      for (int kk = 0; kk < 2 * DC; ++kk) sc = mfma_32x32x16(frag_rows<DC>(Qs, rb * 32, kk, lane), kf[kk], sc);
-#pragma unroll
-      for (int kk = 0; kk < 2 * DC; ++kk) dp = mfma_32x32x16(frag_rows<DC>(Os, rb * 32, kk, lane), vf[kk], dp);
+      for (int kk = 0; kk < 2 * DC; ++kk) {
+        sc = mfma_32x32x16(frag_rows<DC>(Qs, rb * 32, kk, lane), kf[kk], sc);
+        dp = mfma_32x32x16(frag_rows<DC>(Os, rb * 32, kk, lane), vf[kk], dp);
+      }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

@@ -15,7 +15,10 @@ them; so do ``rmsnorm``, ``gated_forward`` (gate and up projections, activation
 and product) and ``forward_epilogue`` (the linear with bias, activation and
 residual), with their backward passes ``rmsnorm_backward``, ``gated_backward``
 and ``backward_epilogue``: a pre-norm block's feed-forward half is rmsnorm ->
-gated_forward -> forward_epilogue with the residual stream added.
+gated_forward -> forward_epilogue with the residual stream added. Its attention
+half is rmsnorm -> forward (q, k and v as one base) -> ``attention`` ->
+forward_epilogue, with ``attention_backward``; ``head_loss`` is the loss over the
+vocabulary behind the last norm, with the gradient that starts the way back.
 """
 
 import ctypes
@@ -780,6 +783,14 @@ def _bf16_on(t, name, shape, dev):
         _need(t, name, shape, torch.bfloat16, dev)
 
 
+def _int64_on(t, name, n, dev):
+    """_need for an int64 tensor [n], with one test where nothing is wrong."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int64 and t.shape == (n,) and t.is_contiguous()
+            and t.device == dev):
+        _need(t, name, (n,), torch.int64, dev)
+
+
 def _given(ws, dev):
     """Checks a caller's workspace tensor; whether it is large enough the
     library says (LORA4_ERR_WORKSPACE)."""
@@ -1156,15 +1167,15 @@ def _attention_args(Q, K, V, scale, q_offsets, k_offsets, k_lengths):
         if not isinstance(q_offsets, torch.Tensor):
             raise ValueError("q_offsets must be a torch tensor")
         seqs = q_offsets.numel() - 1
-        _need(q_offsets, "q_offsets", (max(seqs, 1) + 1,), torch.int64, dev)
+        _int64_on(q_offsets, "q_offsets", max(seqs, 1) + 1, dev)
         if k_offsets is not None:
-            _need(k_offsets, "k_offsets", (seqs + 1,), torch.int64, dev)
+            _int64_on(k_offsets, "k_offsets", seqs + 1, dev)
         elif Tq != Tk:
             raise ValueError("without k_offsets the keys are the queries' tokens: K must have as many as Q")
     elif k_offsets is not None:
         raise ValueError("k_offsets are only taken with q_offsets")
     if k_lengths is not None:
-        _need(k_lengths, "k_lengths", (seqs,), torch.int64, dev)
+        _int64_on(k_lengths, "k_lengths", seqs, dev)
     return lora4_attn(Tq, Tk, seqs, Hq, Hkv, D, float(scale), ldq, ldk, ldv, _ptr(q_offsets), _ptr(k_offsets),
                       _ptr(k_lengths))
 
@@ -1191,7 +1202,7 @@ def attention(Q, K, V, scale, q_offsets=None, k_offsets=None, k_lengths=None, wa
     if O is not None:
         _need(O, "O", Q.shape, torch.bfloat16, dev)
     else:
-        O = torch.empty(Q.shape, dtype=torch.bfloat16, device=dev)
+        O = torch.empty_like(Q, memory_format=torch.contiguous_format)
     if lse is not None:
         _need(lse, "lse", Q.shape[:2], torch.float32, dev)
     elif want_lse:
@@ -1217,15 +1228,17 @@ def attention_backward(Q, K, V, O, lse, dO, scale, q_offsets=None, k_offsets=Non
     out = out or {}
     a = _attention_args(Q, K, V, scale, q_offsets, k_offsets, k_lengths)
     dev = Q.device
-    _need(O, "O", Q.shape, torch.bfloat16, dev)
-    _need(dO, "dO", Q.shape, torch.bfloat16, dev)
+    _bf16_on(O, "O", Q.shape, dev)
+    _bf16_on(dO, "dO", Q.shape, dev)
     _need(lse, "lse", Q.shape[:2], torch.float32, dev)
     grads, lds = [], []
     for name, ref in (("dQ", Q), ("dK", K), ("dV", V)):
         t = out.get(name)
         if t is None:
-            t = torch.empty(ref.shape, dtype=torch.bfloat16, device=dev)
-        lds.append(_heads(t, name, dev, ref.shape))
+            t = torch.empty_like(ref, memory_format=torch.contiguous_format)
+            lds.append(ref.shape[1] * ref.shape[2])
+        else:
+            lds.append(_heads(t, name, dev, ref.shape))
         grads.append(t)
     stream, guard = _on_device(dev)
     with guard:
@@ -1265,13 +1278,14 @@ def head_loss(X, W, targets, weights=None, ignore_index=-100, want_grad=True, wa
     dev = X.device
     _bf16_on(X, "X", (M, K), dev)
     _bf16_on(W, "W", (V, K), dev)
-    _need(targets, "targets", (M,), torch.int64, dev)
+    _int64_on(targets, "targets", M, dev)
     if weights is not None:
         _need(weights, "weights", (M,), torch.float32, dev)
-    for name, shape, dtype in (("loss", (M,), torch.float32), ("lse", (M,), torch.float32),
-                               ("total", (1,), torch.float32), ("dX", (M, K), torch.bfloat16)):
-        if out.get(name) is not None:
-            _need(out[name], name, shape, dtype, dev)
+    if out:
+        for name, shape, dtype in (("loss", (M,), torch.float32), ("lse", (M,), torch.float32),
+                                   ("total", (1,), torch.float32), ("dX", (M, K), torch.bfloat16)):
+            if out.get(name) is not None:
+                _need(out[name], name, shape, dtype, dev)
     loss, total = out.get("loss"), out.get("total")
     if loss is None:
         loss = torch.empty((M,), dtype=torch.float32, device=dev)

@@ -532,8 +532,9 @@ static __global__ __launch_bounds__(THREADS) void k_attn_join(Params p) {
 // dQ: a tile of rows over its keys, as the forward. It also makes the rows' delta
 // for k_attn_dkv, which runs after it: delta from the bf16 O is off by O's
 // rounding, which shows as rows of dS that do not sum to zero; their fp32 sum is
-// added to it, so that dK is free of that error (dQ keeps it: it would take the
-// product P K as well).
+// added to it, so that dK is free of that error. dQ keeps it (it would take the
+// product P K as well) but in the rows that see at most 32 keys, where it weighs
+// most (its part of dQ falls as 1 / sqrt(keys)): their delta is the sum of P dP.
 template <int DC>
 __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
   using T = Lds<DC>;
@@ -629,6 +630,17 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
       for (int i = 0; i < 4; ++i) {
         sched_mfma<1>();
         sched_read<(2 * DC + 3) / 4>();
+      }
+      if (kb == 0 && s == 0 && full <= 32) {
+        // rows that see no key past these 32: delta from P and dP themselves
+        float d = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (8 * (i >> 2) + (i & 3) <= lk) d = __builtin_fmaf(exp2_hw(__builtin_fmaf(sc[i], c, -lse2)), dp[i], d);
+          asm volatile("" : "+v"(d));   // (one at a time: registers)
+        }
+        const Halves both = both_halves(d);
+        if (lim < 32) dl = both.lo + both.hi;
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) sc[i] = exp2_hw(__builtin_fmaf(sc[i], c, -lse2)) * (dp[i] - dl);

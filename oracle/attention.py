@@ -26,6 +26,8 @@ def _weights(q, k, scale):
 # zero: it is off by at most this, absolutely.
 TINY = 2.0 ** -126
 
+EXACT = 32   # keys of a row whose delta dQ takes from P and dP
+
 
 def weight_error(q, k, lse, scale):
     """[Lq]: how far a weight P computed in fp32 may be off, relative to itself.
@@ -58,9 +60,10 @@ def forward(Q, K, V, scale, q_ranges, k_ranges):
 
 
 def backward(Q, K, V, O, dO, scale, q_ranges, k_ranges):
-    """{"dQ", "dK", "dV"}: delta = sum dO O of the given O for dQ, and for dK what it
-    stands for, the sum of P (dO V^T) over the keys (the two differ by O's
-    rounding, where the given O is rounded). I_dQ, I_dK, I_dV: the
+    """{"dQ", "dK", "dV"}: delta = sum dO O of the given O for dQ of rows that see
+    more than EXACT keys, and for all others and dK what it stands for, the sum of
+    P (dO V^T) over the keys (the two differ by O's rounding, where the given O is
+    rounded). I_dQ, I_dK, I_dV: the
     sums of absolute values that the roundings of dS and P enter; E_dQ, E_dK, E_dV:
     what fp32 arithmetic may cost (the weights' error, and that of dP and delta,
     sums of D exact products each, whose difference may cancel)."""
@@ -74,14 +77,17 @@ def backward(Q, K, V, O, dO, scale, q_ranges, k_ranges):
             q, k, do = Q[a:b, h], K[c:d, g], dO[a:b, h]
             P, lse = _weights(q, k, scale)
             dP = do @ V[c:d, g].T
-            dS = P * (dP - (do * O[a:b, h]).sum(axis=1, keepdims=True)) * scale
-            dSk = P * (dP - (P * dP).sum(axis=1, keepdims=True)) * scale
+            few = (np.arange(b - a) + (d - c) - (b - a) < EXACT)[:, None]
+            exact = (P * dP).sum(axis=1, keepdims=True)
+            dS = P * (dP - np.where(few, exact, (do * O[a:b, h]).sum(axis=1, keepdims=True))) * scale
+            dSk = P * (dP - exact) * scale
             r = weight_error(q, k, lse, scale)[:, None]
             terms = np.abs(do) @ np.abs(V[c:d, g]).T + np.abs(do * O[a:b, h]).sum(axis=1, keepdims=True)
             e = r * np.abs(dS) + P * terms * scale * Q.shape[2] * 2.0 ** -24 + TINY * (1 + scale * (1 + terms))
-            o["E_dQ"][a:b, h] = e @ np.abs(k) + TINY
-            # (its delta: weights off by r each, which do not sum to 1 then, and n terms)
-            e = e + P * scale * ((r + (d - c) * 2.0 ** -24) * (P * terms).sum(axis=1, keepdims=True))
+            # (the exact delta: weights off by r each, which do not sum to 1 then, and n terms)
+            ek = e + P * scale * ((r + (d - c) * 2.0 ** -24) * (P * terms).sum(axis=1, keepdims=True))
+            o["E_dQ"][a:b, h] = np.where(few, ek, e) @ np.abs(k) + TINY
+            e = ek
             o["E_dK"][c:d, g] += e.T @ np.abs(q) + TINY
             o["E_dV"][c:d, g] += (r * P + TINY).T @ np.abs(do) + TINY
             o["dQ"][a:b, h] = dS @ k

@@ -210,9 +210,8 @@ struct Frags {
 // The rows that count
 // ---------------------------------------------------------------------------
 
-// Rows of a batch whose blocks find the rows that count each for themselves, in
-// one round of their threads a quarter of it (a launch less; the targets are read
-// from the L2).
+// Rows of a batch whose blocks find the rows that count each for themselves, four
+// rows to a thread (a launch less, 3-5 us; the targets are read from the L2).
 constexpr int SHORT = 1024;
 
 // The rows whose target is not `ignore`, in order: one block of NT threads looks at
@@ -252,9 +251,10 @@ static __global__ __launch_bounds__(1024) void k_loss_rows(Params p) {
 
 // A wave to a row that counts: its X beside the others', and the logit of its
 // target (NaN for a target that is no word or whose logit is +infinity: the row's
-// outputs become NaN). And a
-// wave to a row that does not: loss, lse and dX of row i are zero. FIND: without
-// k_loss_rows before it (M <= SHORT).
+// outputs become NaN). And a wave to a row that does not: loss, lse and dX of row i
+// are zero. FIND: without k_loss_rows before it (M <= SHORT). Bound by latency and
+// X's bytes, which are written once more: 4096 rows of 4096 20 us, 2048 of 5120 14, 8
+// rows 7.
 template <bool FIND>
 __global__ __launch_bounds__(256) void k_loss_target(Params p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -324,7 +324,17 @@ __global__ __launch_bounds__(256) void k_loss_target(Params p) {
 __device__ __forceinline__ int strip_ld(int live) { return (live + 7) & ~7; }
 
 // The tile's results: wave (wv, wt) holds the words of a strip, AV blocks, of
-// tokens 64 wt .. + 63 (2 blocks).
+// tokens 64 wt .. + 63 (2 blocks). The epilogue takes the strip's maximum and the sum
+// of exp(l - reference) of every row in registers, in fp32, and with GRAD stores E, which
+// is rounded to bf16 for its product with W (2^-8 of each term, as the operand that a
+// softmax rounded to bf16 would be).
+//
+// Bound by the matrix cores at the clock the card holds under them (products in flight
+// 61 % of the cycles at 1.9 GHz): 3686 rows, 4096 -> 32768 with E 831-866 us, 1.14-1.19
+// PFLOP/s (a library product of the same operands, whose logits are then in memory,
+// 1.39); 2048 rows, 5120 -> 32003 without 534-548, 1.22-1.26 PFLOP/s. Few rows, by the
+// head's bytes: 8 rows, 4096 -> 128256 170-195 us, 5.4-6.2 TB/s. 32-deep stages, five of
+// them, took 865 us where two of 64 took 840.
 template <bool GRAD, typename T>
 __global__ __launch_bounds__(T::THREADS, 2) void k_loss_logits(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
@@ -455,8 +465,9 @@ __device__ __forceinline__ Split split_of(const Params &p, int live, int64_t col
 
 // The strips of a piece into the rows' sums. NR rows to a block, 1024 / NR threads
 // to a row (32 rows read whole lines; few rows have more threads each: 8 rows of
-// 1002 strips 31 us with 32 threads a row). Where a strip had to take a reference of its own, the row gets the
-// largest, and its E and acc are brought onto it (E is rounded a second time).
+// 1002 strips 10 us with 256 threads a row, 31 with 32). Where a strip had to take a
+// reference of its own, the row gets the largest, and its E and acc are brought onto
+// it (E is rounded a second time). Bound by latency: 3686 rows of 256 strips 11 us.
 template <bool GRAD, int NR>
 __global__ __launch_bounds__(1024) void k_loss_join(Params p) {
   constexpr int NT = 1024 / NR;
@@ -566,6 +577,12 @@ __device__ __forceinline__ u32x4_t frag_w(const uint16_t *lds, int v0, int col0,
   return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
 }
 
+// acc of a tile of tokens and hidden columns over a range of the piece's words, fp32,
+// added to the pieces' before it. The head is read as it lies, the reduction over its
+// rows, by transposing LDS reads. Bound by the matrix cores (61 % of the cycles at 1.9
+// GHz): 3686 rows, 32768 words, 4096 columns 764-785 us, 1.26-1.30 PFLOP/s (a library
+// product 1.23); 933 rows, 50021 words, 2080 columns in 7 ranges on their XCDs 199 us,
+// with ranges on any XCD 352. Two stages of 64; five of 32 took 808 us beside 777.
 template <typename T>
 __global__ __launch_bounds__(T::THREADS, 2) void k_loss_dx(Params p) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
@@ -692,7 +709,8 @@ __device__ __forceinline__ void sum_total(const Params &p, int count) {
 }
 
 // A wave to 512 columns of a row of the chunk (column block blockIdx.y): dX = w
-// (acc - S W_t) / (S + s_t), and by the first the row's loss. The last block in x,
+// (acc - S W_t) / (S + s_t), and by the first the row's loss. Bound by acc's bytes
+// (3686 rows of 4096 23 us). The last block in x,
 // where there is one more than the rows need, makes total.
 static __global__ __launch_bounds__(256) void k_loss_finish(Params p) {
   const int lane = threadIdx.x & 63;

@@ -38,10 +38,10 @@ int loss_tiles_policy() {
 // Microseconds of a 64-deep step and of a tile's start and end, by tile: big tiles
 // do eight times the work of small ones in 2.4 times the time, one to a CU instead
 // of two, and want many steps and tiles enough for every CU. Measured beside the
-// estimate (small / big, us): logits of 512 tokens, 4096 -> 32000 205 / 137, of 256
-// 108 / 123, of 1000, 4600 -> 2070 60 / 125, of 2753, 792 -> 5813 62 / 38; gradients
-// of the same 198 / 141, 106 / 85, 45 / 34, 64 / 49, of 300 tokens, 24639 -> 1024
-// 33 / 42.
+// estimate (small / big, us): logits of 512 tokens, 4096 -> 32000 212 / 118, of 256
+// 111 / 109, of 1000, 4600 -> 2070 61 / 107, of 2753, 792 -> 5813 59 / 36; gradients
+// of the same 193 / 126, 104 / 80, 43 / 34, 63 / 43, of 300 tokens, 24639 -> 1024
+// 27 / 35.
 double loss_round_us(bool small, double steps) {
   return small ? 0.8 * steps + 4.0 : 1.75 * steps + 9.0;
 }

@@ -591,9 +591,9 @@ lora4_status lora4_attention_backward(const lora4_attn *attn, const uint16_t *Q,
  * Logits are summed in fp32; the exponentials are rounded to bf16 for their
  * product with W (the target's own, p_t - 1, is not), which is summed in fp32.
  * A NaN in a row of X stays in that row; an infinity or NaN in W reaches every
- * row; a logit of +infinity makes its row's loss and dX NaN. The same inputs give the same bits on every call. M may be 0. Errors:
- * LORA4_ERR_SHAPE, LORA4_ERR_NULL, LORA4_ERR_ALIGN, LORA4_ERR_WORKSPACE,
- * LORA4_ERR_HIP. */
+ * row; a logit of +infinity makes its row's loss and dX NaN. The same inputs
+ * give the same bits on every call. M may be 0. Errors: LORA4_ERR_SHAPE,
+ * LORA4_ERR_NULL, LORA4_ERR_ALIGN, LORA4_ERR_WORKSPACE, LORA4_ERR_HIP. */
 size_t lora4_head_loss_workspace_bytes(int grad, int64_t M, int64_t K, int64_t V);
 lora4_status lora4_head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targets, const float *weights,
                              int64_t M, int64_t K, int64_t V, int64_t ignore_index, float *loss, float *lse,

@@ -198,8 +198,8 @@ lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targ
       const int64_t items = std::max<int64_t>((int64_t)p.tiles_m * p.tiles_n, p.side);
       TRY(launch_fn("loss_dx", loss::dx_kernel(pl.dt.small), ceil_div(items, 8) * 8, pl.dt.threads, pl.dt.lds, st, p));
     }
-    TRY(launch_grid("loss_finish", loss::finish_kernel(), dim3((unsigned)(ceil_div(rows, 4) + p.total_block), grad ? (unsigned)ceil_div(K, 512) : 1u),
-                    256, 0, st, p));
+    const dim3 grid((unsigned)(ceil_div(rows, 4) + p.total_block), grad ? (unsigned)ceil_div(K, 512) : 1u);
+    TRY(launch_grid("loss_finish", loss::finish_kernel(), grid, 256, 0, st, p));
   }
   return total && !p.total_block ? launch_fn("loss_total", loss::total_kernel(), 1, 1024, 0, st, p) : LORA4_OK;
 }

@@ -71,3 +71,23 @@ def test_gradients_against_differences(Lq, Lk):
         up[i], dn[i] = x[i] + eps * d, x[i] - eps * d
         num = (f(*up) - f(*dn)) / (2 * eps)
         assert abs(num - (g[n] * d).sum()) <= 1e-8 * max(1.0, np.abs(g[n] * d).sum())
+
+
+def test_rows_of_few_keys_do_not_take_delta_from_the_given_output():
+    Q, K, V, dO = _case(6, 40, 40, 2, 1, 8)
+    r = [(0, 40)]
+    O = attention.forward(Q, K, V, 0.5, r, r)["O"]
+    g, w = (attention.backward(Q, K, V, o, dO, 0.5, r, r) for o in (O, O * (1 + 2.0 ** -9)))
+    n = attention.EXACT
+    np.testing.assert_array_equal(g["dQ"][:n], w["dQ"][:n])
+    assert (g["dQ"][n:] != w["dQ"][n:]).any(axis=(1, 2)).all()
+    for k in ("dK", "dV"):
+        np.testing.assert_array_equal(g[k], w[k])
+    # where O is exact both forms are the same
+    for x in (g, w):
+        x["dQ"][n:] = 0
+    P, _ = attention._weights(Q[:, 0], K[:, 0], 0.5)
+    dP = dO[:, 0] @ V[:, 0].T
+    for delta in ((dO[:, 0] * O[:, 0]).sum(axis=1), (P * dP).sum(axis=1)):
+        d = (P * (dP - delta[:, None])) @ K[:, 0] * 0.5
+        np.testing.assert_allclose(d[:n], g["dQ"][:n, 0], rtol=1e-9, atol=1e-12)

@@ -874,11 +874,12 @@ static __global__ __launch_bounds__(THREADS) void k_attn_dkv_sum(Params p) {
   const int64_t n = p.Tk * p.Hkv * p.D;
   const int w = p.Hkv * p.D;
   const int keys = min(16, t.Lk - t.tile * 16);
-  for (int i = threadIdx.x * 4; i < keys * w; i += THREADS * 4) {
+  for (int i = (blockIdx.y * THREADS + threadIdx.x) * 4; i < keys * w; i += gridDim.y * THREADS * 4) {
     const int64_t kr = t.k0 + t.tile * 16 + i / w;
     const int col = i % w;
     const float *src = p.part + kr * w + col;
     f32x4_t a = {0.f, 0.f, 0.f, 0.f}, b = a;
+#pragma unroll 4
     for (int s = 0; s < p.splits; ++s) {
       a += *reinterpret_cast<const f32x4_t *>(src + 2 * s * n);
       b += *reinterpret_cast<const f32x4_t *>(src + (2 * s + 1) * n);

@@ -57,7 +57,11 @@ AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int 
     }
   } else {
     const int64_t blocks = std::max<int64_t>(1, std::max(Tk / attn::BKEYS, std::min(seqs, Tk)) * Hkv);
-    const int64_t most = std::max<int64_t>(1, rows / (8 * attn::BROWS));
+    // Ranges of at least eight steps, as each costs its partials; where the blocks are
+    // fewer than the CUs, of at least two (a sequence of 531 tokens, 32 over 8 heads: 4
+    // ranges 65 us, 8 56; three of together 531: 1 range 56, 2 46, 5 42).
+    const int64_t steps = rows / attn::BROWS;
+    const int64_t most = std::max<int64_t>({1, steps / 8, std::min(steps / 2, cu_count() / blocks)});
     // Four blocks a CU where the key tiles give fewer: the first keys of a sequence
     // are seen by all of its rows, the last by few, and the long blocks start first
     // (packed 4096 tokens, 8 key heads: 1, 2, 4, 8 ranges 229, 144, 104, 125 us, their
@@ -65,7 +69,7 @@ AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int 
     // are little beside them (8192 tokens, 64 heads: 2 ranges 2439 + 30, 3 2330 + 45).
     pl.ksplits = (int)std::min<int64_t>(std::min<int64_t>(16, most),
                                         std::max<int64_t>(1, ceil_div(2 * attn_full_grid(), blocks)));
-    if (rows / attn::BROWS / (pl.ksplits + 1) >= 256) ++pl.ksplits;
+    if (steps / (pl.ksplits + 1) >= 256) ++pl.ksplits;
     pl.off_part = align256((size_t)std::max<int64_t>(1, Tq * Hq) * 8);
     pl.bytes = pl.off_part + (pl.ksplits > 1 ? align256((size_t)pl.ksplits * 2 * Tk * Hkv * D * 4) : 0);
   }
@@ -178,7 +182,12 @@ lora4_status attn_backward(const lora4_attn *a, const uint16_t *Q, const uint16_
   TRY(launch_fn("attn_dkv", attn::dkv_kernel(pl.dc), pl.kslots * a->Hkv * pl.ksplits, attn::THREADS,
                 attn_lds(pl.dc, true), st, p));
   if (pl.ksplits == 1) return LORA4_OK;
-  return launch_fn("attn_dkv_sum", attn::dkv_sum_kernel(), a->Tk / 16 + a->seqs, attn::THREADS, 0, st, p);
+  // blocks of 16 keys, or of parts of their columns where those are few (1024 tokens,
+  // 32 over 8 heads, 8 ranges: the backward 112 us without parts, 84 with)
+  const int64_t blocks = a->Tk / 16 + a->seqs;
+  const int64_t parts = std::min(ceil_div(16 * wk, 4 * attn::THREADS), ceil_div(8 * cu_count(), blocks));
+  return launch_grid("attn_dkv_sum", attn::dkv_sum_kernel(), dim3((unsigned)blocks, (unsigned)parts), attn::THREADS, 0,
+                     st, p);
 }
 
 }  // namespace

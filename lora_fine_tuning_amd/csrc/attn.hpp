@@ -498,7 +498,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_fwd(Params p) {
 
 // Joins the key ranges of a row: a wave to a row; a lane to a range for its
 // maximum and sum, then to two columns. Bound by latency: 24 tokens, 64 heads over 20
-// ranges 5.5-6.0 us, 3 chunks of 333 tokens, 14 heads 7.1-7.3.
+// ranges 5.5-6.0 us, 3 chunks of 333 tokens, 14 heads over 4 7.1-7.3.
 constexpr int MAX_SPLITS = 64;
 static __global__ __launch_bounds__(THREADS) void k_attn_join(Params p) {
   const int lane = threadIdx.x & 63;

@@ -587,7 +587,7 @@ lora4_status lora4_attention_backward(const lora4_attn *attn, const uint16_t *Q,
  *  total   : fp32 [1] output, 0 if every row is ignored; may be NULL.
  *  dX      : bf16 [M, K] output, zero at ignored rows; NULL: the loss alone.
  *  workspace : lora4_head_loss_workspace_bytes(dX != NULL, M, K, V) bytes (0 is
- *            returned for invalid sizes).
+ *            returned for invalid sizes); one for M rows does for fewer, too.
  * Logits are summed in fp32; the exponentials are rounded to bf16 for their
  * product with W (the target's own, p_t - 1, is not), which is summed in fp32.
  * A NaN in a row of X stays in that row; an infinity or NaN in W reaches every

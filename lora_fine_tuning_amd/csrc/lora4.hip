@@ -1929,7 +1929,7 @@ lora4_status lora4_attention_backward(const lora4_attn *attn, const uint16_t *Q,
 
 size_t lora4_head_loss_workspace_bytes(int grad, int64_t M, int64_t K, int64_t V) {
   if ((grad != 0 && grad != 1) || check_loss_sizes(M, K, V) != LORA4_OK) return 0;
-  return loss_plan(grad != 0, M, K, V).bytes;
+  return loss_workspace(grad != 0, M, K, V);
 }
 
 lora4_status lora4_head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targets, const float *weights,

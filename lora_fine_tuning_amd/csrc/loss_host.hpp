@@ -21,12 +21,12 @@ constexpr int64_t LOSS_E_BYTES = int64_t(256) << 20;
 // The tiles of a launch.
 struct LossTiles {
   bool small;
-  int tt, vt, wv, strip, per_cu, threads;
+  int tt, vt, wv, strip, side, threads;   // (side: blocks that run side by side)
   size_t lds;
 };
 template <typename T>
-LossTiles loss_tiles_of(bool small) {
-  return {small, T::TT, T::VT, T::WV, T::STRIP, T::PER_CU, T::THREADS, T::LDS_BYTES};
+LossTiles loss_tiles_of(bool small, int cus) {
+  return {small, T::TT, T::VT, T::WV, T::STRIP, T::PER_CU * cus, T::THREADS, T::LDS_BYTES};
 }
 
 // Forced tiles for tests and measurements (LORA4_LOSS_TILES): small or big.
@@ -46,33 +46,37 @@ double loss_round_us(bool small, double steps) {
   return small ? 0.8 * steps + 4.0 : 1.75 * steps + 9.0;
 }
 
-// The tiles of the logits: `rows` tokens by V words over K.
-LossTiles loss_logits_tiles(int64_t rows, int64_t K, int64_t V) {
-  const LossTiles t[2] = {loss_tiles_of<loss::Big>(false), loss_tiles_of<loss::Small>(true)};
-  if (const int f = loss_tiles_policy()) return t[f == 1];
-  double us[2];
-  for (int i = 0; i < 2; ++i) {
-    const int64_t tiles = ceil_div(rows, t[i].tt) * ceil_div(V, t[i].vt);
-    us[i] = (double)ceil_div(tiles, t[i].per_cu * cu_count()) * loss_round_us(i == 1, (double)ceil_div(K, loss::BKS));
-  }
-  return t[us[1] < us[0]];
+// Estimated time of the logits, `rows` tokens by V words over K, with tiles t.
+double loss_logits_us(const LossTiles &t, int64_t rows, int64_t K, int64_t V) {
+  const int64_t tiles = ceil_div(rows, t.tt) * ceil_div(V, t.vt);
+  return (double)ceil_div(tiles, t.side) * loss_round_us(t.small, (double)ceil_div(K, loss::BKS));
 }
 
-// The tiles of acc: `rows` tokens by K columns over `words`, in the ranges of
-// split_of; the ranges are read again when they are summed.
-LossTiles loss_acc_tiles(int64_t rows, int64_t K, int64_t words) {
-  const LossTiles t[2] = {loss_tiles_of<loss::Big>(false), loss_tiles_of<loss::Small>(true)};
-  if (const int f = loss_tiles_policy()) return t[f == 1];
-  double us[2];
-  for (int i = 0; i < 2; ++i) {
-    const int64_t tiles = std::max<int64_t>(1, ceil_div(rows, t[i].tt) * ceil_div(K, t[i].vt));
-    const int64_t side = t[i].per_cu * cu_count(), steps = ceil_div(words, loss::BKS);
-    const int64_t n = std::max<int64_t>(1, std::min(side / tiles, steps / 8));
-    us[i] = (double)ceil_div(tiles * n, side) * loss_round_us(i == 1, (double)ceil_div(steps, n)) +
-            1e-6 * (double)n * (double)rows * (double)K;
-  }
-  return t[us[1] < us[0]];
+// That of acc: `rows` tokens by K columns over `words`, in the ranges of split_of;
+// the ranges are read again when they are summed.
+double loss_acc_us(const LossTiles &t, int64_t rows, int64_t K, int64_t words) {
+  const int64_t tiles = std::max<int64_t>(1, ceil_div(rows, t.tt) * ceil_div(K, t.vt));
+  const int64_t steps = ceil_div(words, loss::BKS);
+  const int64_t n = std::max<int64_t>(1, std::min(t.side / tiles, steps / 8));
+  return (double)ceil_div(tiles * n, t.side) * loss_round_us(t.small, (double)ceil_div(steps, n)) +
+         1e-6 * (double)n * (double)rows * (double)K;
 }
+
+// The two kinds of tiles: [0] big, [1] small.
+struct LossKinds {
+  const int cus = cu_count();
+  LossTiles t[2] = {loss_tiles_of<loss::Big>(false, cus), loss_tiles_of<loss::Small>(true, cus)};
+  int forced = loss_tiles_policy();
+  int logits(int64_t rows, int64_t K, int64_t V) const {
+    if (forced) return forced == 1;
+    return loss_logits_us(t[1], rows, K, V) < loss_logits_us(t[0], rows, K, V);
+  }
+  // how much longer acc takes on big tiles (0: those, where they take as long)
+  double acc_gap(int64_t rows, int64_t K, int64_t V) const {
+    if (forced) return forced == 1 ? 1.0 : -1.0;
+    return loss_acc_us(t[0], rows, K, V) - loss_acc_us(t[1], rows, K, V);
+  }
+};
 
 struct LossPlan {
   LossTiles lt, dt;    // tiles of the logits and of acc
@@ -96,15 +100,18 @@ lora4_status check_loss_sizes(int64_t M, int64_t K, int64_t V) {
   return LORA4_OK;
 }
 
-LossPlan loss_plan(bool grad, int64_t M, int64_t K, int64_t V) {
+// A plan of M tokens with tiles lt and dt in chunks of `rows` (at most LOSS_CHUNK,
+// rounded up to the tiles), pieces of at most `widest` tiles of words.
+LossPlan loss_layout(bool grad, int64_t M, int64_t rows, int64_t K, int64_t V, const LossTiles &lt,
+                     const LossTiles &dt, int64_t widest) {
   constexpr int64_t T = loss::TILE;
   LossPlan pl{};
-  pl.lt = loss_logits_tiles(std::min(M, LOSS_CHUNK), K, V);
-  pl.dt = loss_acc_tiles(std::min(M, LOSS_CHUNK), K, V);
+  pl.lt = lt;
+  pl.dt = dt;
   const int64_t unit = std::max(pl.lt.tt, pl.dt.tt);
-  pl.chunk = std::min(LOSS_CHUNK, std::max<int64_t>(unit, ceil_div(M, unit) * unit));
+  pl.chunk = std::max<int64_t>(unit, ceil_div(rows, unit) * unit);
   const int64_t tiles_v = ceil_div(V, T);
-  int64_t piece = std::min(tiles_v, loss_piece_policy());
+  int64_t piece = std::min(tiles_v, widest);
   if (grad) {
     piece = std::max<int64_t>(1, std::min(piece, LOSS_E_BYTES / (pl.chunk * 2 * T)));
   }
@@ -127,10 +134,36 @@ LossPlan loss_plan(bool grad, int64_t M, int64_t K, int64_t V) {
   if (grad) {
     pl.off_e = take((size_t)pl.chunk * pl.piece * 2);
     // the chunk's rows once, or as many ranges of fewer as fill the chip (split_of)
-    pl.off_acc = take((size_t)std::max(pl.chunk, pl.dt.per_cu * cu_count() / ceil_div(K, pl.dt.vt) * pl.dt.tt) * K * 4);
+    pl.off_acc = take((size_t)std::max(pl.chunk, pl.dt.side / ceil_div(K, pl.dt.vt) * pl.dt.tt) * K * 4);
   }
   pl.bytes = off;
   return pl;
+}
+
+LossPlan loss_plan(bool grad, int64_t M, int64_t K, int64_t V) {
+  const LossKinds k;
+  const int64_t rows = std::min(M, LOSS_CHUNK);
+  return loss_layout(grad, M, rows, K, V, k.t[k.logits(rows, K, V)], k.t[k.acc_gap(rows, K, V) > 0.0],
+                     loss_piece_policy());
+}
+
+// Bytes that the plan of any batch of up to M tokens fits in: a shorter one may take
+// small tiles, whose strips are four times as many, or wider pieces. The logits' tiles
+// and the chunk are the same for all rows of a block of 64, and acc's gap is linear in
+// them (where it is close to 0 at an end, both kinds count), so that the ends of each
+// block say it all. On the host 0.1 us a block, 7 us for a whole chunk.
+size_t loss_workspace(bool grad, int64_t M, int64_t K, int64_t V) {
+  const LossKinds k;
+  const int64_t top = std::min(M, LOSS_CHUNK), widest = loss_piece_policy();
+  size_t most = 256;   // (of no tokens: the count)
+  for (int64_t lo = 1; lo <= top; lo += 64) {
+    const int64_t hi = std::min(top, lo + 63);
+    const LossTiles &lt = k.t[k.logits(hi, K, V)];
+    const double a = k.acc_gap(lo, K, V), b = k.acc_gap(hi, K, V);
+    if (std::min(a, b) < 1e-6) most = std::max(most, loss_layout(grad, M, hi, K, V, lt, k.t[0], widest).bytes);
+    if (std::max(a, b) > -1e-6) most = std::max(most, loss_layout(grad, M, hi, K, V, lt, k.t[1], widest).bytes);
+  }
+  return most;
 }
 
 lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targets, const float *weights, int64_t M,
@@ -140,8 +173,8 @@ lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targ
   if (!W || (M > 0 && (!X || !targets || !out_loss))) return LORA4_ERR_NULL;
   if (!all_aligned16({X, W, targets, weights, out_loss, lse, total, dX, ws})) return LORA4_ERR_ALIGN;
   const bool grad = dX != nullptr;
+  if (!ws || ws_bytes < loss_workspace(grad, M, K, V)) return LORA4_ERR_WORKSPACE;
   const LossPlan pl = loss_plan(grad, M, K, V);
-  if (!ws || ws_bytes < pl.bytes) return LORA4_ERR_WORKSPACE;
   loss::Params p{};
   p.X = X;
   p.W = W;
@@ -168,7 +201,7 @@ lora4_status head_loss(const uint16_t *X, const uint16_t *W, const int64_t *targ
   p.strip = pl.lt.strip;
   p.dt = pl.dt.tt;
   p.dv = pl.dt.vt;
-  p.side = pl.dt.per_cu * cu_count();
+  p.side = pl.dt.side;
   p.loss = out_loss;
   p.lse = lse;
   p.total = total;

@@ -791,6 +791,13 @@ def _int64_on(t, name, n, dev):
         _need(t, name, (n,), torch.int64, dev)
 
 
+def _on16(t):
+    """t, or a copy of it (on the current stream) where it is a view that starts off
+    the 16 bytes that the library asks of its pointers: ids[1:] as the next-token
+    targets, a row of a table of offsets."""
+    return t.clone() if t is not None and t.data_ptr() & 15 else t
+
+
 def _given(ws, dev):
     """Checks a caller's workspace tensor; whether it is large enough the
     library says (LORA4_ERR_WORKSPACE)."""
@@ -1176,8 +1183,14 @@ def _attention_args(Q, K, V, scale, q_offsets, k_offsets, k_lengths):
         raise ValueError("k_offsets are only taken with q_offsets")
     if k_lengths is not None:
         _int64_on(k_lengths, "k_lengths", seqs, dev)
-    return lora4_attn(Tq, Tk, seqs, Hq, Hkv, D, float(scale), ldq, ldk, ldv, _ptr(q_offsets), _ptr(k_offsets),
-                      _ptr(k_lengths))
+    qo, ko, kl = _ptr(q_offsets), _ptr(k_offsets), _ptr(k_lengths)
+    copies = None
+    if ((qo or 0) | (ko or 0) | (kl or 0)) & 15:
+        copies = [_on16(t) for t in (q_offsets, k_offsets, k_lengths)]
+        qo, ko, kl = map(_ptr, copies)
+    a = lora4_attn(Tq, Tk, seqs, Hq, Hkv, D, float(scale), ldq, ldk, ldv, qo, ko, kl)
+    a.copies = copies   # (they live until the call has been made)
+    return a
 
 
 def attention_workspace(which, Tq, Tk, seqs, Hq, Hkv, D, device):
@@ -1193,7 +1206,9 @@ def attention(Q, K, V, scale, q_offsets=None, k_offsets=None, k_lengths=None, wa
     output). Packed sequences: q_offsets, k_offsets int64 [S + 1] on the device
     (k_offsets None: the same tokens), and k_lengths int64 [S], the filled rows of
     each sequence's cache. A sequence's last query sees its last key. Rows of no
-    sequence are left as they are (a new O is not initialised there)."""
+    sequence are left as they are (a new O is not initialised there). The offsets and
+    lengths may be views that start anywhere (they are copied where the library's 16
+    bytes ask for it); all other tensors start at 16 bytes."""
     import torch
     out = out or {}
     a = _attention_args(Q, K, V, scale, q_offsets, k_offsets, k_lengths)
@@ -1267,7 +1282,8 @@ def head_loss(X, W, targets, weights=None, ignore_index=-100, want_grad=True, wa
     int64 targets [M]: {"loss" fp32 [M], "total" fp32 [1], "lse" fp32 [M], "dX"
     bf16 [M, K]} (lse and dX None where not wanted). total is the sum of weights
     times losses, dX its gradient; weights fp32 [M], or None for the mean over the
-    rows whose target is not ignore_index."""
+    rows whose target is not ignore_index. targets and weights may be views that
+    start anywhere (ids[1:]); all other tensors, outputs too, start at 16 bytes."""
     import torch
     out = out or {}
     for t, name in ((X, "X"), (W, "W")):
@@ -1301,6 +1317,7 @@ def head_loss(X, W, targets, weights=None, ignore_index=-100, want_grad=True, wa
             workspace = head_loss_workspace(dX is not None, M, K, V, dev)
         else:
             _given(workspace, dev)
+        targets, weights = _on16(targets), _on16(weights)
         st = lora4_head_loss(_ptr(X), _ptr(W), _ptr(targets), _ptr(weights), M, K, V, int(ignore_index), _ptr(loss),
                              _ptr(lse), _ptr(total), _ptr(dX), _ptr(workspace), workspace.numel(), stream)
     _check_ws_status(st, "lora4_head_loss")

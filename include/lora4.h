@@ -556,9 +556,12 @@ lora4_status lora4_attention_forward(const lora4_attn *attn, const uint16_t *Q, 
  *   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
  * (dK and dV summed over the G query heads). P and dS are rounded to bf16 for
  * their products; sums are fp32, in a fixed order. dQ's delta is that of the
- * given bf16 O, but in rows that see at most 32 keys, where O's rounding weighs
- * most: there it is the sum of P (dO V^T). dK's is freed of O's rounding in all
- * rows (by the sum of the row's dS, which would be zero without it).
+ * given bf16 O, but in rows that see at most 32 keys: there it is the sum of P
+ * (dO V^T). O's rounding enters dQ of the other rows as d scale P K, d the sum of
+ * dO times O's error, which is small beside dQ where many keys share a row's weight
+ * (dQ off by 0.0024 of its norm in all) and not where few do (0.0066 with scores of
+ * deviation 36). dK's delta is freed of it in all rows (by the sum of the row's
+ * dS, which would be zero without it).
  *  O, lse : from lora4_attention_forward. dO : bf16 [Tq][Hq][D], dense.
  *  dQ, dK, dV : bf16 outputs with token strides lddq, lddk, lddv (as ldq .. ldv).
  *             A sequence without queries has dK = dV = 0.

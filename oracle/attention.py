@@ -97,3 +97,37 @@ def backward(Q, K, V, O, dO, scale, q_ranges, k_ranges):
             o["I_dK"][c:d, g] += np.abs(dSk).T @ np.abs(q)
             o["I_dV"][c:d, g] += P.T @ np.abs(do)
     return o
+
+
+def dq(Q, K, V, dO, scale, q_ranges, k_ranges, u):
+    """{"dQ", "I_dQ", "E_dQ", "D_dQ", "N_dQ"} of the definition alone: delta is the sum
+    of P (dO V^T) in all rows, whatever O a caller holds. An implementation that takes
+    delta from an O of unit roundoff u has it off by d = sum dO (the error of O), and
+    dQ by d scale P K, in D_dQ at most (each element of O off by 1.01 u (|O| + I_O) +
+    E_O, as forward states) and in N_dQ [rows] the root of the mean square of the row's
+    norm: the roundings of O's elements and P's are independent, uniform within u at
+    most, of variance below u^2 of their terms' squares."""
+    f = forward(Q, K, V, scale, q_ranges, k_ranges)
+    o = {n: np.full(Q.shape, np.nan) for n in ("dQ", "I_dQ", "E_dQ", "D_dQ")}
+    o["N_dQ"] = np.full(Q.shape[:2], np.nan)
+    G = Q.shape[1] // K.shape[1]
+    for (a, b), (c, d) in zip(q_ranges, k_ranges):
+        for h in range(Q.shape[1]):
+            q, k, v, do = Q[a:b, h], K[c:d, h // G], V[c:d, h // G], dO[a:b, h]
+            P, lse = _weights(q, k, scale)
+            dP = do @ v.T
+            dS = P * (dP - (P * dP).sum(axis=1, keepdims=True)) * scale
+            O, I, E = (f[n][a:b, h] for n in ("O", "I_O", "E_O"))
+            off = (np.abs(do) * (1.01 * u * (np.abs(O) + I) + E)).sum(axis=1, keepdims=True)
+            rms = u * np.sqrt((do ** 2 * (O ** 2 + I ** 2)).sum(axis=1))
+            r = weight_error(q, k, lse, scale)[:, None]
+            terms = np.abs(do) @ np.abs(v).T + (np.abs(do) * I).sum(axis=1, keepdims=True)
+            e = r * np.abs(dS) + P * terms * scale * Q.shape[2] * 2.0 ** -24 + TINY * (1 + scale * (1 + terms))
+            e += P * scale * ((r + (d - c) * 2.0 ** -24) * (P * terms).sum(axis=1, keepdims=True))
+            o["dQ"][a:b, h] = dS @ k
+            o["I_dQ"][a:b, h] = np.abs(dS) @ np.abs(k)
+            o["E_dQ"][a:b, h] = e @ np.abs(k) + TINY
+            # (dS is rounded with delta's error in it)
+            o["D_dQ"][a:b, h] = scale * off * (np.abs(P @ k) + 2 * u * (P @ np.abs(k)))
+            o["N_dQ"][a:b, h] = scale * rms * np.linalg.norm(P @ k, axis=1)
+    return o

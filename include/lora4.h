@@ -508,7 +508,7 @@ lora4_status lora4_backward_epilogue(const lora4_W *W, int32_t activation, const
  *  Hq, Hkv  : query heads and key heads, Hq a multiple of Hkv, at most 64 query
  *             heads to a key head (G = Hq / Hkv; head h reads key head h / G).
  *  D        : elements of a head, a multiple of 8 up to 128.
- *  scale    : finite, > 0.
+ *  scale    : > 0, and scale log2(e) a finite fp32 number.
  *  ldq, ldk, ldv : elements between the tokens of Q, K and V (multiples of 8,
  *             at least Hq D, Hkv D and Hkv D): the heads of a token are
  *             contiguous, and q, k and v may be columns of one projection's output.

@@ -86,7 +86,8 @@ bool bad_stride(int64_t ld, int64_t width) { return ld < width || ld % 8 != 0 ||
 lora4_status check_attn(const lora4_attn *a) {
   if (!a) return LORA4_ERR_NULL;
   TRY(check_attn_sizes(a->Tq, a->Tk, a->seqs, a->Hq, a->Hkv, a->D));
-  if (!std::isfinite(a->scale) || a->scale <= 0.0f) return LORA4_ERR_SHAPE;
+  // (the kernels take scale log2 e)
+  if (!(a->scale > 0.0f) || !std::isfinite(a->scale * attn::LOG2E)) return LORA4_ERR_SHAPE;
   const int64_t wq = (int64_t)a->Hq * a->D, wk = (int64_t)a->Hkv * a->D;
   if (bad_stride(a->ldq, wq) || bad_stride(a->ldk, wk) || bad_stride(a->ldv, wk)) return LORA4_ERR_SHAPE;
   if (!a->q_offsets && a->seqs != 1) return LORA4_ERR_NULL;

@@ -518,6 +518,8 @@ lora4_status lora4_backward_epilogue(const lora4_W *W, int32_t activation, const
  *  k_lengths : DEVICE int64 [seqs] or NULL: only the first k_lengths[i] of
  *             sequence i's key rows are keys (a cache's filled part; at most
  *             the rows that k_offsets gives it).
+ * At most 2^30 tokens and keys, 2^20 sequences, strides of 2^22 elements, Tq Hq
+ * below 2^31 and (Tq G + 128) G below 2^32. Outputs and inputs are distinct.
  * Offsets and lengths are held inside the tensors whatever they say. Rows
  * behind the last sequence (and before the first), and key rows past
  * k_lengths, are neither read nor written, in outputs and gradients alike. An
@@ -591,6 +593,10 @@ lora4_status lora4_attention_backward(const lora4_attn *attn, const uint16_t *Q,
  *  dX      : bf16 [M, K] output, zero at ignored rows; NULL: the loss alone.
  *  workspace : lora4_head_loss_workspace_bytes(dX != NULL, M, K, V) bytes (0 is
  *            returned for invalid sizes); one for M rows does for fewer, too.
+ * M and V are at most 2^30, K at most 2^20. LORA4_LOSS_TILES (small or big) and
+ * LORA4_LOSS_PIECE (words) in the environment, read by each of the two functions
+ * on every call, force the tiles and the pieces for tests and measurements; with a
+ * change between the two a workspace may be refused.
  * Logits are summed in fp32; the exponentials are rounded to bf16 for their
  * product with W (the target's own, p_t - 1, is not), which is summed in fp32.
  * A NaN in a row of X stays in that row; an infinity or NaN in W reaches every

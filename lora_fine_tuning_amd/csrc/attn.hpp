@@ -329,7 +329,7 @@ __device__ __forceinline__ void two_stages(int s0, int s1, F &&body) {
 // Bound: one token's rows, by the caches' bytes (24 tokens over 5 to 32 thousand
 // keys, 64 heads: 363-373 us for 1.91 GB, 5.2 TB/s) or, over one short cache, by the
 // latency of 4 steps (7 us). Long prompts, by the matrix cores at the clock the card
-// holds under them: 32768 tokens, 40 heads 9.7-9.9 ms, 1110-1130 TFLOP/s, products
+// holds under them: 32768 tokens, 40 heads 9.5-9.9 ms, 1110-1150 TFLOP/s, products
 // in flight 59-63 % of the cycles at 1.62-1.65 GHz, no LDS bank conflicts; the rest of
 // the issue is exp2, the row maxima and the packing of P. Two blocks a CU (256
 // registers a wave) let one's softmax run under the other's products. LDS reads
@@ -564,8 +564,8 @@ static __global__ __launch_bounds__(THREADS) void k_attn_join(Params p) {
 // sums of dQ over key tiles in memory, whose order would change the results. dS is
 // rounded to bf16 for dS K (an error of 2^-8 of each term; a second product of what
 // that drops cost 15 to 25 % of the time). Bound by the matrix cores: 8192 tokens,
-// 64 heads 1.42-1.46 ms, 1.13-1.16 PFLOP/s of its three products, in flight 64 % of
-// the cycles at 1.65 GHz; packed 4096 tokens, 32 heads 71-73 us.
+// 64 heads 1.40-1.52 ms, 1.08-1.18 PFLOP/s of its three products, in flight 64 % of
+// the cycles at 1.65 GHz; packed 4096 tokens, 32 heads 69-80 us.
 template <int DC>
 __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
   using T = Lds<DC>;
@@ -714,9 +714,9 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dq(Params p) {
 // (2^-8 of each term); both sums stay in registers over all rows.
 //
 // Bound by registers: K, V, dK and dV of a wave take 192 of 256, so the reads of Q
-// and dO run only 3 products ahead. 8192 tokens, 64 heads over 8 key heads 2.20-2.31
-// ms, 0.95-1.0 PFLOP/s of its four products, in flight 49 % of the cycles at 1.6-1.8
-// GHz; packed 4096 tokens, 32 heads over 8 101-104 us. First form 6.7 ms (63 registers
+// and dO run only 3 products ahead. 8192 tokens, 64 heads over 8 key heads 2.18-2.33
+// ms, 0.94-1.0 PFLOP/s of its four products, in flight 49 % of the cycles at 1.6-1.8
+// GHz; packed 4096 tokens, 32 heads over 8 101-119 us. First form 6.7 ms (63 registers
 // spilled); without spills 3.1, statistics of the rows by direct loads 2.5, ranges and
 // reads without branches 2.3. One wave a SIMD with 512 registers took 5.7 ms (moves
 // between the two register files), V in LDS with 32-row steps 2.6-2.7, row ranges of
@@ -870,8 +870,8 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_dkv(Params p) {
 
 // Sums the row ranges' dK (times scale) and dV in order: 4 columns a thread. The
 // grid runs over the key slots, so that keys of no sequence are left alone. Bound by
-// the partials' bytes: 8192 keys, 8 heads, 3 ranges 43-45 us (4.9 TB/s), 4096 keys, 4
-// ranges 27.
+// the partials' bytes: 8192 keys, 8 heads, 3 ranges 41-42 us (235 MB, 5.6 TB/s), 4096
+// keys, 4 ranges 24.
 static __global__ __launch_bounds__(THREADS) void k_attn_dkv_sum(Params p) {
   const Tile t = map_tile<true>(p, blockIdx.x, 16);
   if (t.tile < 0) return;

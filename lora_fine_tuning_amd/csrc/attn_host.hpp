@@ -64,9 +64,9 @@ AttnPlan attn_plan(int which, int64_t Tq, int64_t Tk, int64_t seqs, int Hq, int 
     const int64_t most = std::max<int64_t>({1, steps / 8, std::min(steps / 2, cu_count() / blocks)});
     // Four blocks a CU where the key tiles give fewer: the first keys of a sequence
     // are seen by all of its rows, the last by few, and the long blocks start first
-    // (packed 4096 tokens, 8 key heads: 1, 2, 4, 8 ranges 229, 144, 104, 125 us, their
-    // sums 0, 17, 28, 101). One more where it leaves each 256 steps, whose partials
-    // are little beside them (8192 tokens, 64 heads: 2 ranges 2439 + 30, 3 2330 + 45).
+    // (packed 4096 tokens, 8 key heads: 1, 2, 4, 8 ranges 195, 141, 119, 141 us, their
+    // sums 0, 14, 24, 56). One more where it leaves each 256 steps, whose partials
+    // are little beside them (8192 tokens, 64 heads: 2 ranges 2481 + 29, 3 2327 + 42).
     pl.ksplits = (int)std::min<int64_t>(std::min<int64_t>(16, most),
                                         std::max<int64_t>(1, ceil_div(2 * attn_full_grid(), blocks)));
     if (steps / (pl.ksplits + 1) >= 256) ++pl.ksplits;

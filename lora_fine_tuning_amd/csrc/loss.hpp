@@ -330,9 +330,9 @@ __device__ __forceinline__ int strip_ld(int live) { return (live + 7) & ~7; }
 // softmax rounded to bf16 would be).
 //
 // Bound by the matrix cores at the clock the card holds under them (products in flight
-// 61 % of the cycles at 1.9 GHz): 3686 rows, 4096 -> 32768 with E 831-866 us, 1.14-1.19
+// 61 % of the cycles at 1.9 GHz): 3686 rows, 4096 -> 32768 with E 831-868 us, 1.14-1.19
 // PFLOP/s (a library product of the same operands, whose logits are then in memory,
-// 1.39); 2048 rows, 5120 -> 32003 without 534-548, 1.22-1.26 PFLOP/s. Few rows, by the
+// 1.39); 2048 rows, 5120 -> 32003 without 522-553, 1.21-1.29 PFLOP/s. Few rows, by the
 // head's bytes: 8 rows, 4096 -> 128256 170-195 us, 5.4-6.2 TB/s. 32-deep stages, five of
 // them, took 865 us where two of 64 took 840.
 template <bool GRAD, typename T>
@@ -580,7 +580,7 @@ __device__ __forceinline__ u32x4_t frag_w(const uint16_t *lds, int v0, int col0,
 // acc of a tile of tokens and hidden columns over a range of the piece's words, fp32,
 // added to the pieces' before it. The head is read as it lies, the reduction over its
 // rows, by transposing LDS reads. Bound by the matrix cores (61 % of the cycles at 1.9
-// GHz): 3686 rows, 32768 words, 4096 columns 764-785 us, 1.26-1.30 PFLOP/s (a library
+// GHz): 3686 rows, 32768 words, 4096 columns 764-837 us, 1.18-1.30 PFLOP/s (a library
 // product 1.23); 933 rows, 50021 words, 2080 columns in 7 ranges on their XCDs 199 us,
 // with ranges on any XCD 352. Two stages of 64; five of 32 took 808 us beside 777.
 template <typename T>
